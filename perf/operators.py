@@ -246,6 +246,7 @@ def prepare(case, seed):
             slots >= case["length"] * 3 // 4, 2.0).sort(dim=-1, stable=True).indices
         s["pos"] = (mixed * 3 + 7).int()
         s["acc_out"], s["pos_out"] = torch.zeros_like(s["acc"]), torch.zeros_like(s["pos"])
+        s["lens_out"] = torch.zeros_like(b["lens"])
     else:
         q = torch.randn((b["rows"], case["heads"], case["dim"]), generator=g, device="cuda") * 1.5
         s["q"] = q.to(_dtype(case["dtype"]))
@@ -421,7 +422,8 @@ def run(s):
         return {"k": k, "v": v}
     if kind == "evict":
         acc, pos, lens = bqe.rfpx_kv_evict(cache, batch, s["keep"], s["recent"], s["acc"], s["pos"],
-                                           acc_out=s["acc_out"], pos_out=s["pos_out"])
+                                           acc_out=s["acc_out"], pos_out=s["pos_out"],
+                                           lens_out=s["lens_out"])
         return {"acc": acc, "pos": pos, "lens": lens, "pool": s["pool"]}
     lse = torch.empty(s["q"].shape[:2], device="cuda")
     r = {"out": bqe.rfpx_attn_forward(cache, batch, s["q"], s["scale"], lse=lse), "lse": lse}
