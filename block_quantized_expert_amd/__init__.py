@@ -1,4 +1,5 @@
-"""Python binding of librfpx (include/rfpx.h): argument marshalling only.
+"""Python binding of librfpx (include/rfpx.h and include/rfpx_attn.h):
+argument marshalling only.
 
 Every computation runs in the HIP kernels of librfpx.so; PyTorch supplies
 device memory and the current stream.  The functions carry the C names and
@@ -41,6 +42,14 @@ SYMBOLS = (
     "rfpx_status_str", "rfpx_last_error",
 )
 
+# ... and include/rfpx_attn.h
+ATTN_SYMBOLS = (
+    "rfpx_kv_pool_bytes", "rfpx_qk_norm_rope", "rfpx_kv_append", "rfpx_kv_unpack",
+    "rfpx_attn_workspace_bytes", "rfpx_attn_forward", "rfpx_attn_weights",
+    "rfpx_kv_evict_workspace_bytes", "rfpx_kv_evict",
+)
+RFPX_ROPE_HALF, RFPX_ROPE_PAIRS = 0, 1
+
 
 class RfpxError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
@@ -55,6 +64,21 @@ class MoeLayerC(C.Structure):
                 ("fmts", C.POINTER(C.c_int)), ("image_bytes", C.c_size_t)]
 
 
+class KvCacheC(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int), ("head_dim", C.c_int), ("page_tokens", C.c_int),
+                ("n_pages", C.c_int), ("pool", C.c_void_p), ("pool_bytes", C.c_size_t)]
+
+
+class KvBatchC(C.Structure):
+    _fields_ = [("n_seqs", C.c_int), ("pages_per_seq", C.c_int), ("max_cols", C.c_int),
+                ("max_len", C.c_int), ("page_table", C.c_void_p), ("lens", C.c_void_p),
+                ("starts", C.c_void_p)]
+
+
+class RopeC(C.Structure):
+    _fields_ = [("dim", C.c_int), ("style", C.c_int), ("inv_freq_host", C.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -63,6 +87,8 @@ def lib():
     """Load librfpx.so once (after torch, so that both share one HIP
     runtime)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -110,6 +136,20 @@ def lib():
             "rfpx_status_str": (C.c_char_p, [I]),
             "rfpx_last_error": (C.c_char_p, []),
         }
+        L, F = C.c_longlong, C.c_float
+        KP, BP = C.POINTER(KvCacheC), C.POINTER(KvBatchC)
+        sig.update({
+            "rfpx_kv_pool_bytes": (S, [I, I, I, I]),
+            "rfpx_qk_norm_rope": (I, [P, L, I, P, L, I, I, I, I, P, P, P, F, C.POINTER(RopeC),
+                                      P, L, P, L, I, P]),
+            "rfpx_kv_append": (I, [KP, BP, P, L, P, L, I, I, P, P, P, P]),
+            "rfpx_kv_unpack": (I, [KP, BP, I, P, P, I, P]),
+            "rfpx_attn_workspace_bytes": (S, [KP, BP, I, I]),
+            "rfpx_attn_forward": (I, [KP, BP, P, L, I, I, I, F, P, L, P, P, S, P]),
+            "rfpx_attn_weights": (I, [KP, BP, P, L, I, I, I, F, P, F, P, P, P]),
+            "rfpx_kv_evict_workspace_bytes": (S, [KP, BP, I]),
+            "rfpx_kv_evict": (I, [KP, BP, I, I, P, P, P, P, P, P, S, P]),
+        })
         for name, (res, args) in sig.items():
             fn = getattr(l, name)
             fn.restype = res
@@ -452,6 +492,293 @@ def rfpx_dense_forward(m: DenseMatrix, x, y=None, ws=None, stream=None):
         m.fmt, _ptr(m.image), m.rows, m.cols, _ptr(x), _xtype(x), q, _ptr(y), _ptr(ws),
         ws.numel(), _stream(stream)))
     return y
+
+
+# -------------------------------------------------------------- attention
+#
+# The step between a layer's qkv projection and its output projection, over a
+# paged key/value cache in FP4 blocks (include/rfpx_attn.h).  Tensors of rows
+# are [rows][heads][head_dim], heads and values adjacent, rows any multiple of
+# 16 bytes apart, so that slices of one projection's output go in as they are.
+# All tensors of a call live on the current device.
+
+def _rows(what: str, t):
+    """(pointer, row stride, xtype) of a tensor of rows."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [rows][heads][head_dim]")
+    n, h, d = t.shape
+    s = t.stride()
+    if s[2] != 1 or (h > 1 and s[1] != d):
+        raise ValueError(f"{what}: heads and values must be adjacent")
+    return t.data_ptr(), (s[0] if n > 1 else h * d), _xtype(t)
+
+
+def _same_device(torch, *ts):
+    dev = torch._C._cuda_getDevice()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor must be on the current device, cuda:{dev}")
+    return dev
+
+
+def _raw_stream(torch, dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _flat(what: str, t, dtype, shape):
+    """Pointer of a contiguous tensor of that dtype and shape (None: null)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _scratch(n: int, device, stream):
+    """n bytes that live until the work on `stream` is done with them."""
+    import torch
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _used_on(ws, stream)
+    return ws
+
+
+def _used_on(t, stream):
+    """Tell the allocator that a tensor made here is used on `stream`."""
+    import torch
+    if stream is not None and stream != torch.cuda.current_stream():
+        t.record_stream(stream)
+
+
+class Rope:
+    """The rotation of a head's first `dim` values (rfpx_rope): frequencies
+    theta^(-2i/dim), or inv_freq (dim/2 numbers, radians a position)."""
+
+    def __init__(self, dim: int, theta: float = 10000.0, style: int = RFPX_ROPE_HALF,
+                 inv_freq: Optional[Sequence[float]] = None):
+        half = max(0, dim // 2)
+        if inv_freq is None:
+            inv_freq = [float(theta) ** (-2.0 * i / dim) for i in range(half)]
+        if len(inv_freq) != half:
+            raise ValueError(f"inv_freq must hold {half} numbers")
+        self._freq = (C.c_double * max(1, half))(*[float(f) for f in inv_freq])
+        self.c = RopeC(dim, style, C.cast(self._freq, C.c_void_p))
+        self.dim, self.style = dim, style
+
+
+def rfpx_kv_pool_bytes(n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int) -> int:
+    return lib().rfpx_kv_pool_bytes(n_kv_heads, head_dim, page_tokens, n_pages)
+
+
+class KvCache:
+    """A paged FP4 key/value cache (rfpx_kv_cache) and its pool, which is
+    allocated here unless given.  Pages are numbered 0 .. n_pages-1."""
+
+    def __init__(self, n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, pool=None,
+                 device="cuda"):
+        import torch
+        n = rfpx_kv_pool_bytes(n_kv_heads, head_dim, page_tokens, n_pages)
+        if n == 0:
+            raise RfpxError("rfpx_kv_pool_bytes", -2, "unsupported cache shape")
+        if pool is None:
+            pool = torch.empty(n, dtype=torch.uint8, device=device)
+        _need_cuda(pool)
+        self.pool = pool
+        self.n_kv_heads, self.head_dim = n_kv_heads, head_dim
+        self.page_tokens, self.n_pages = page_tokens, n_pages
+        self.c = KvCacheC(n_kv_heads, head_dim, page_tokens, n_pages, pool.data_ptr(),
+                          pool.numel() * pool.element_size())
+        self.ref = C.byref(self.c)
+
+
+class KvBatch:
+    """A step of a batch (rfpx_kv_batch): page_table int32 [seqs][pages], lens
+    int32 [seqs] with the step's columns, starts int32 [seqs + 1]; kept by
+    reference, so their contents may change between calls.  max_cols and
+    max_len are what launches are planned for."""
+
+    def __init__(self, page_table, lens, starts, max_cols: int, max_len: int):
+        import torch
+        n, pages = page_table.shape
+        _need_cuda(page_table, lens, starts)
+        _flat("page_table", page_table, torch.int32, (n, pages))
+        _flat("lens", lens, torch.int32, (n,))
+        _flat("starts", starts, torch.int32, (n + 1,))
+        self.page_table, self.lens, self.starts = page_table, lens, starts
+        self.n_seqs, self.pages_per_seq = n, pages
+        self.max_cols, self.max_len = max_cols, max_len
+        self.c = KvBatchC(n, pages, max_cols, max_len, page_table.data_ptr(), lens.data_ptr(),
+                          starts.data_ptr())
+        self.ref = C.byref(self.c)
+
+
+def _slots(cache: KvCache, batch: KvBatch):
+    return (batch.n_seqs, cache.n_kv_heads, batch.pages_per_seq * cache.page_tokens)
+
+
+def rfpx_qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      rope: Optional[Rope] = None, q_out=None, k_out=None, out_dtype=None,
+                      stream=None):
+    """RMS norm (where a weight, fp32 [head_dim], is given) and rotation of
+    the heads of q and k (either may be None); positions int32 [rows], negative
+    for padding rows, which are left as they were.  Returns (q_out, k_out)."""
+    import torch
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is needed")
+    n, _, d = x.shape
+    dev = _same_device(torch, q, k, positions, q_weight, k_weight, q_out, k_out)
+    pos = _flat("positions", positions, torch.int32, (n,))
+    qw = _flat("q_weight", q_weight, torch.float32, (d,))
+    kw = _flat("k_weight", k_weight, torch.float32, (d,))
+    given = next((o for o in (q_out, k_out) if o is not None), None)
+    dtype = out_dtype or (given.dtype if given is not None else x.dtype)
+    outs, args = [], []
+    for what, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            outs.append(None)
+            args.append((None, 0, 0, None, 0))
+            continue
+        if t.shape[0] != n or t.shape[2] != d or t.dtype != x.dtype:
+            raise ValueError("q and k must agree in rows, head_dim and dtype")
+        if o is None:
+            o = torch.empty(t.shape, dtype=dtype, device=t.device)
+            _used_on(o, stream)
+        elif o.shape != t.shape or o.dtype != dtype:
+            raise ValueError(f"{what}_out must be a {dtype} tensor of {what}'s shape")
+        p, s, _ = _rows(what, t)
+        po, so, otype = _rows(what + "_out", o)
+        outs.append(o)
+        args.append((p, s, t.shape[1], po, so))
+    (qp, qs, qh, qo, qos), (kp, ks, kh, ko, kos) = args
+    _check("rfpx_qk_norm_rope", lib().rfpx_qk_norm_rope(
+        qp, qs, qh, kp, ks, kh, d, _xtype(x), n, pos, qw, kw, eps,
+        C.byref(rope.c) if rope is not None else None, qo, qos, ko, kos, otype,
+        _raw_stream(torch, dev, stream)))
+    return outs[0], outs[1]
+
+
+def rfpx_kv_append(cache: KvCache, batch: KvBatch, k, v, positions=None, pos=None, acc=None,
+                   stream=None) -> None:
+    """Quantize the step's k and v into the cache; pos (int32) and acc (fp32),
+    [seqs][kv heads][slots], get positions[row] and 0 at the new slots."""
+    import torch
+    dev = _same_device(torch, cache.pool, batch.lens, k, v, positions, pos, acc)
+    shape = (k.shape[0], cache.n_kv_heads, cache.head_dim)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
+        raise ValueError(f"k and v must be {shape} tensors of one dtype")
+    kp, ks, xt = _rows("k", k)
+    vp, vs, _ = _rows("v", v)
+    slots = _slots(cache, batch)
+    _check("rfpx_kv_append", lib().rfpx_kv_append(
+        cache.ref, batch.ref, kp, ks, vp, vs, xt, k.shape[0],
+        _flat("positions", positions, torch.int32, (k.shape[0],)),
+        _flat("pos", pos, torch.int32, slots), _flat("acc", acc, torch.float32, slots),
+        _raw_stream(torch, dev, stream)))
+
+
+def rfpx_kv_unpack(cache: KvCache, batch: KvBatch, rows: int, k=None, v=None, stream=None):
+    """What the cache holds for the step's columns: (k, v) [rows][kv heads]
+    [head_dim], fp32 unless bf16 tensors are given."""
+    import torch
+    shape = (rows, cache.n_kv_heads, cache.head_dim)
+    out = []
+    for t in (k, v):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.float32, device=cache.pool.device)
+            _used_on(t, stream)
+        out.append(t)
+    k, v = out
+    dev = _same_device(torch, cache.pool, batch.lens, k, v)
+    _check("rfpx_kv_unpack", lib().rfpx_kv_unpack(
+        cache.ref, batch.ref, rows, _flat("k", k, k.dtype, shape), _flat("v", v, k.dtype, shape),
+        _xtype(k), _raw_stream(torch, dev, stream)))
+    return k, v
+
+
+def rfpx_attn_workspace_bytes(cache: KvCache, batch: KvBatch, heads: int, rows: int) -> int:
+    return lib().rfpx_attn_workspace_bytes(cache.ref, batch.ref, heads, rows)
+
+
+def rfpx_attn_forward(cache: KvCache, batch: KvBatch, q, scale: Optional[float] = None, out=None,
+                      lse=None, ws=None, stream=None):
+    """Attention of the step's columns q [rows][heads][head_dim] (fp32 or
+    bf16) over the cache; scale defaults to head_dim^-0.5.  lse (fp32 [rows]
+    [heads]), if given, gets the log of every row's sum of exponentials."""
+    import torch
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [rows][heads][{cache.head_dim}]")
+    rows, heads, d = q.shape
+    if out is None:
+        out = torch.empty((rows, heads, d), dtype=q.dtype, device=q.device)
+        _used_on(out, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if ws is None:
+        n = rfpx_attn_workspace_bytes(cache, batch, heads, rows)
+        if n == 0:
+            raise RfpxError("rfpx_attn_workspace_bytes", -2, lib().rfpx_last_error().decode())
+        ws = _scratch(n, q.device, stream)
+    dev = _same_device(torch, cache.pool, batch.lens, q, out, lse, ws)
+    qp, qs, xt = _rows("q", q)
+    op, os_, _ = _rows("out", out)
+    _check("rfpx_attn_forward", lib().rfpx_attn_forward(
+        cache.ref, batch.ref, qp, qs, xt, heads, rows,
+        d ** -0.5 if scale is None else scale, op, os_,
+        _flat("lse", lse, torch.float32, (rows, heads)), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(torch, dev, stream)))
+    return out
+
+
+def rfpx_attn_weights(cache: KvCache, batch: KvBatch, q, lse, acc, decay: float = 1.0,
+                      scale: Optional[float] = None, acc_out=None, stream=None):
+    """acc_out = decay * acc + the attention weight that every slot receives
+    from the step's columns (acc fp32 [seqs][kv heads][slots]; in place unless
+    acc_out is given); q, scale and lse as in rfpx_attn_forward."""
+    import torch
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [rows][heads][{cache.head_dim}]")
+    rows, heads, d = q.shape
+    if acc_out is None:
+        acc_out = acc
+    dev = _same_device(torch, cache.pool, batch.lens, q, lse, acc, acc_out)
+    slots = _slots(cache, batch)
+    qp, qs, xt = _rows("q", q)
+    _check("rfpx_attn_weights", lib().rfpx_attn_weights(
+        cache.ref, batch.ref, qp, qs, xt, heads, rows, d ** -0.5 if scale is None else scale,
+        _flat("lse", lse, torch.float32, (rows, heads)), decay,
+        _flat("acc", acc, torch.float32, slots), _flat("acc_out", acc_out, torch.float32, slots),
+        _raw_stream(torch, dev, stream)))
+    return acc_out
+
+
+def rfpx_kv_evict_workspace_bytes(cache: KvCache, batch: KvBatch, keep: int) -> int:
+    return lib().rfpx_kv_evict_workspace_bytes(cache.ref, batch.ref, keep)
+
+
+def rfpx_kv_evict(cache: KvCache, batch: KvBatch, keep: int, recent: int, acc, pos, acc_out=None,
+                  pos_out=None, lens_out=None, ws=None, stream=None):
+    """Cut every sequence to its `keep` best slots: the `recent` newest by pos
+    first, then those of largest acc.  acc, pos and the batch's lens are
+    updated in place unless outputs are given.  Returns (acc, pos, lens)."""
+    import torch
+    acc_out = acc if acc_out is None else acc_out
+    pos_out = pos if pos_out is None else pos_out
+    lens_out = batch.lens if lens_out is None else lens_out
+    if ws is None:
+        n = rfpx_kv_evict_workspace_bytes(cache, batch, keep)
+        if n == 0:
+            raise RfpxError("rfpx_kv_evict_workspace_bytes", -2, lib().rfpx_last_error().decode())
+        ws = _scratch(n, cache.pool.device, stream)
+    dev = _same_device(torch, cache.pool, batch.lens, acc, pos, acc_out, pos_out, lens_out, ws)
+    slots = _slots(cache, batch)
+    _check("rfpx_kv_evict", lib().rfpx_kv_evict(
+        cache.ref, batch.ref, keep, recent, _flat("acc", acc, torch.float32, slots),
+        _flat("pos", pos, torch.int32, slots), _flat("acc_out", acc_out, torch.float32, slots),
+        _flat("pos_out", pos_out, torch.int32, slots),
+        _flat("lens_out", lens_out, torch.int32, (batch.n_seqs,)), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(torch, dev, stream)))
+    return acc_out, pos_out, lens_out
 
 
 # ------------------------------------------------------------ measurement

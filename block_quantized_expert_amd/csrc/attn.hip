@@ -1,0 +1,781 @@
+// attn.hip -- attention of new columns over the FP4 cache, and the weight
+// that every cached token has gathered.
+//
+// Mathematics.  With codes c and scales 2^e, a value is (c - 7.5) 2^(e-127).
+// A code masked into the mantissa of 2^(e-127) is the bf16 number (1 + c/16)
+// 2^(e-127), exactly, so that
+//   (c - 7.5) 2^(e-127) / 16 = word - 1.46875 * 2^(e-127):
+// a product of codes runs on the bf16 matrix instruction with one more
+// product that takes the offset off, and the factor 16 goes into the scale
+// of the scores and the last division.  Nothing of the cache is rounded.
+//   Scores:  S^T = K Q^T, a 16-token tile at a time: D/32 products of code
+//   words, and one of the blocks' 2^(e-127) with -1.46875 times the sums of
+//   q over the blocks (three bf16 terms: 24 bits).
+//   Output:  O^T += V^T P^T, 32 tokens at a time: two products for each
+//   block of 32 values (even and odd ones), and one of -1.46875 * 2^(e-127)
+//   that both take off.  Row sums of P: one product with ones.
+// Both are transposed, so that lane (m = lane & 15, g = lane >> 4) holds of
+// query row m the scores of tokens 4g .. 4g+3 and 16+4g .. 16+4g+3, which
+// are the eight k-values that the second product takes from that very lane:
+// P never leaves its registers.  Softmax is the running kind: row maximum
+// and sum in fp32, the maximum moved (and everything rescaled) only when a
+// score exceeds it by 2^8.
+#include "rfpx_attn.hpp"
+
+namespace rfpx {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kTile = 32;          // tokens of one step of a wave
+constexpr float kOffset = 1.46875f;  // (16 + 7.5) / 16
+constexpr uint32_t kCodeMask = 0x00780078u;
+constexpr uint32_t kNegOffset = 0x803C803Cu;  // sign and mantissa of -1.46875, twice
+constexpr float kNegInf = -__builtin_inff();
+
+struct AttnArgs {
+  KvView v;
+  const void *q;
+  void *out;
+  float *lse;
+  float *part;    // [rows * heads][splits][D] numerators (splits > 1)
+  float *part_ml; // [rows * heads][splits][4]: maximum, sum, exact sum
+  long long q_stride, out_stride;
+  int xtype, heads, group, n_rows, splits, row_blocks;
+  float sc;       // 16 * scale * log2(e)
+};
+
+__device__ __forceinline__ floatx4 mfma(const u32x4v &a, const u32x4v &b, const floatx4 &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
+  const floatx2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float max_across_g(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const uint32_t w = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// N dwords from p (aligned to their size, at most 16 bytes a load).
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+  if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+      w[i] = v.x;
+      w[i + 1] = v.y;
+      w[i + 2] = v.z;
+      w[i + 3] = v.w;
+    }
+  }
+}
+
+// ------------------------------------------------------------ the query side
+
+// Operand words of row m's values for every block: terms t = 0 .. VX-1 of
+// pairs (j, j + 4) of the lane's octet, and the offset operand (see top).
+template <int NB, int VX>
+struct QTile {
+  u32x4v w[VX][NB];
+  u32x4v off;
+};
+
+template <int NB, int VX>
+__device__ __forceinline__ void load_q(const void *q, size_t at, bool live, int g,
+                                       QTile<NB, VX> &t) {
+  float sum[NB];
+#pragma unroll
+  for (int kb = 0; kb < NB; ++kb) {
+    float s = 0.f;
+    if constexpr (VX == 1) {
+      uint4 d = make_uint4(0, 0, 0, 0);
+      if (live)
+        d = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q) + at + 32 * kb + 8 * g);
+      // pairs (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
+      t.w[0][kb][0] = __builtin_amdgcn_perm(d.z, d.x, 0x05040100u);
+      t.w[0][kb][1] = __builtin_amdgcn_perm(d.z, d.x, 0x07060302u);
+      t.w[0][kb][2] = __builtin_amdgcn_perm(d.w, d.y, 0x05040100u);
+      t.w[0][kb][3] = __builtin_amdgcn_perm(d.w, d.y, 0x07060302u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += lo_f(t.w[0][kb][i]) + hi_f(t.w[0][kb][i]);
+    } else {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (live) {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(q) + at + 32 * kb + 8 * g);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+#pragma unroll
+      for (int x = 0; x < VX; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t h = pk_bf16(v[i], v[i + 4]);
+          t.w[x][kb][i] = h;
+          v[i] -= lo_f(h);
+          v[i + 4] -= hi_f(h);
+        }
+    }
+    sum[kb] = cross_row_sum(s) * -kOffset;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = 2 * i < NB ? sum[2 * i] : 0.f, b = 2 * i + 1 < NB ? sum[2 * i + 1] : 0.f;
+    uint32_t h = pk_bf16(a, b), mine = g == 0 ? h : 0u;
+#pragma unroll
+    for (int x = 1; x < 3; ++x) {
+      a -= lo_f(h);
+      b -= hi_f(h);
+      h = pk_bf16(a, b);
+      mine = g == x ? h : mine;
+    }
+    t.off[i] = mine;
+  }
+}
+
+// ------------------------------------------------------------- the key side
+
+template <int NB>
+struct KTile {  // a 16-token tile as loaded
+  uint32_t c[NB];
+  uint32_t s[(NB + 3) / 4];
+};
+
+template <int NB>
+__device__ __forceinline__ void load_k(const uint8_t *slab, const KvGeo &g, int t0, int lane,
+                                       KTile<NB> &k) {
+  const int t = t0 + (lane & 15);
+  load_words<NB>(slab + g.kc + t * (16 * NB) + (lane >> 4) * (4 * NB), k.c);
+  const uint8_t *s = slab + g.ks + t * NB;
+  if constexpr (NB == 2) k.s[0] = *reinterpret_cast<const uint16_t *>(s);
+  else if constexpr (NB == 4) k.s[0] = *reinterpret_cast<const uint32_t *>(s);
+  else load_words<2>(s, k.s);
+}
+
+template <int NB>
+struct KWords {  // its operands
+  u32x4v w[NB];
+  u32x4v e;
+};
+
+template <int NB>
+__device__ __forceinline__ void decode_k(const KTile<NB> &k, KWords<NB> &o) {
+  uint32_t base[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const uint32_t sel = 0x0C000C00u | (b & 3) | (b & 3) << 16;
+    base[b] = __builtin_amdgcn_perm(0u, k.s[b >> 2], sel) << 7;
+    o.w[b][0] = and_or(k.c[b] << 3, kCodeMask, base[b]);
+    o.w[b][1] = and_or(k.c[b] >> 1, kCodeMask, base[b]);
+    o.w[b][2] = and_or(k.c[b] >> 5, kCodeMask, base[b]);
+    o.w[b][3] = and_or(k.c[b] >> 9, kCodeMask, base[b]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o.e[i] = 2 * i < NB ? __builtin_amdgcn_perm(base[2 * i + 1 < NB ? 2 * i + 1 : 0],
+                                                base[2 * i < NB ? 2 * i : 0], 0x05040100u)
+                        : 0u;
+}
+
+template <int NB, int VX>
+__device__ __forceinline__ floatx4 scores(const KWords<NB> &k, const QTile<NB, VX> &q) {
+  floatx4 s = {0.f, 0.f, 0.f, 0.f};
+  // the offsets and the leading terms first: the sum is back at its own size
+  // before the smaller terms come
+  s = mfma(k.e, q.off, s);
+#pragma unroll
+  for (int x = 0; x < VX; ++x)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) s = mfma(k.w[b], q.w[x][b], s);
+  return s;
+}
+
+// ----------------------------------------------------------- the value side
+
+template <int NB>
+struct VTile {  // 32 tokens as loaded: tokens 4g .. of the two 16-token tiles
+  uint32_t c[2][NB];
+  uint32_t s[2][NB];
+};
+
+template <int NB>
+__device__ __forceinline__ void load_v(const uint8_t *slab, const KvGeo &g, int t0, int lane,
+                                       VTile<NB> &v) {
+  const int r = lane & 15, grp = lane >> 4;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int t = t0 + 16 * u + 4 * grp;
+    load_words<NB>(slab + g.vc + (t * 4 + r) * (4 * NB), v.c[u]);
+    load_words<NB>(slab + g.vs + t * NB, v.s[u]);
+  }
+}
+
+// The scale of page token i (0..3) of half u, block b.
+template <int NB>
+__device__ __forceinline__ uint32_t v_scale(const VTile<NB> &v, int u, int i, int b) {
+  const int at = i * NB + b;
+  return (v.s[u][at >> 2] >> (8 * (at & 3))) & 0xFFu;
+}
+
+template <int NB, int RT, int VX>
+__device__ __forceinline__ void add_values(const VTile<NB> &v, const u32x4v (&p)[RT][VX],
+                                           floatx4 (&acc)[RT][NB][2], floatx4 (&l)[RT]) {
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    u32x4v even, odd, off;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // token pairs
+      const int u = i >> 1, a0 = (2 * (i & 1)) * NB + b, a1 = a0 + NB;
+      const uint32_t sel = 0x0C000C00u | (a0 & 3) | (4 + (a1 & 3)) << 16;
+      const uint32_t base = __builtin_amdgcn_perm(v.s[u][a1 >> 2], v.s[u][a0 >> 2], sel) << 7;
+      const uint32_t w = v.c[u][(i & 1) * (NB / 2) + (b >> 1)];
+      even[i] = and_or(b & 1 ? w >> 5 : w << 3, kCodeMask, base);
+      odd[i] = and_or(b & 1 ? w >> 9 : w >> 1, kCodeMask, base);
+      off[i] = base | kNegOffset;
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int x = 0; x < VX; ++x) {
+        acc[t][b][0] = mfma(off, p[t][x], acc[t][b][0]);
+        acc[t][b][1] = mfma(off, p[t][x], acc[t][b][1]);
+        acc[t][b][0] = mfma(even, p[t][x], acc[t][b][0]);
+        acc[t][b][1] = mfma(odd, p[t][x], acc[t][b][1]);
+      }
+  }
+  const u32x4v ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int x = 0; x < VX; ++x) l[t] = mfma(ones, p[t][x], l[t]);
+}
+
+// ------------------------------------------------------------------ forward
+
+// Workgroup (x, y, z): kv head and row block x, split y, sequence z.  A row
+// block is 16 RT of the sequence's rows (column, head of the group); its four
+// waves share out the split's 32-token tiles and join their sums in LDS.
+template <int NB, int VX, int RT>
+__global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
+  constexpr int D = 32 * NB;
+  constexpr int LD = D + 4;
+  __shared__ float sh_ml[kWaves][RT * 16][3];
+  __shared__ __align__(16) float sh_o[kWaves][16][LD];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int head = blockIdx.x % a.v.hk, rb0 = blockIdx.x / a.v.hk;
+  const int split = blockIdx.y, seq = blockIdx.z;
+  const int s0 = a.v.starts[seq];
+  const int n = min(a.v.starts[seq + 1], a.n_rows) - s0;
+  const int n_all = a.v.starts[seq + 1] - s0;
+  if (s0 < 0 || n <= 0) return;
+  const int len = kv_len(a.v, seq);
+  const long long rows = (long long)n * a.group;
+  const KvGeo geo = a.v.g;
+  const int32_t *table = a.v.table + (size_t)seq * a.v.pages_per_seq;
+
+  for (long long r0 = (long long)rb0 * (16 * RT); r0 < rows; r0 += (long long)a.row_blocks * (16 * RT)) {
+    QTile<NB, VX> q[RT];
+    int vis[RT];
+    int first_vis, last_vis;
+    {
+      const int c0 = (int)(r0 / a.group);
+      long long e = r0 + 16 * RT - 1;
+      if (e >= rows) e = rows - 1;
+      const int c1 = (int)(e / a.group);
+      first_vis = min(len, max(0, len - n_all + c0 + 1));
+      last_vis = min(len, max(0, len - n_all + c1 + 1));
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      long long r = r0 + 16 * t + m;
+      const bool live = r < rows;
+      if (!live) r = rows - 1;
+      const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
+      vis[t] = min(len, max(0, len - n_all + col + 1));
+      load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q[t]);
+    }
+    const int tiles = (last_vis + kTile - 1) / kTile;
+    const int per = (tiles + a.splits - 1) / a.splits;
+    const int t_first = min(tiles, split * per), t_last = min(tiles, t_first + per);
+
+    floatx4 acc[RT][NB][2], l[RT];
+    // l is the sum of the numerators as they enter the second product, the
+    // output's denominator; exact the one before bf16 rounding, for lse
+    float mx[RT], thr[RT], exact[RT];
+    uint32_t poison[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      l[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+      mx[t] = thr[t] = kNegInf;
+      exact[t] = 0.f;
+      poison[t] = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[t][b][0] = acc[t][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    for (int tile = t_first + wave; tile < t_last; tile += kWaves) {
+      const int t0 = tile * kTile;
+      const int page = uniform(table[t0 >> geo.page_log]);
+      const bool held = (unsigned)page < (unsigned)a.v.n_pages;
+      const uint8_t *slab = a.v.pool + ((size_t)(held ? page : 0) * a.v.hk + head) * geo.slab;
+      const int tp = t0 & (geo.page_tokens - 1);
+      KTile<NB> k[2];
+      VTile<NB> v;
+      load_k<NB>(slab, geo, tp, lane, k[0]);
+      load_k<NB>(slab, geo, tp + 16, lane, k[1]);
+      load_v<NB>(slab, geo, tp, lane, v);
+      floatx4 s[RT][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        KWords<NB> kw;
+        decode_k<NB>(k[u], kw);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) s[t][u] = scores<NB, VX>(kw, q[t]);
+      }
+      if (!held || t0 + kTile > first_vis) {
+        // some row does not see some token: its score is -inf, and what its
+        // scale says must not reach any row
+        const int lim = held ? len : 0;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (t0 + 16 * u + 4 * g + i >= min(vis[t], lim)) s[t][u][i] = kNegInf;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int slot = t0 + 16 * u + 4 * g + i;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const int at = i * NB + b;
+              const bool bad = v_scale<NB>(v, u, i, b) == 255u;
+              if (slot >= lim || bad) {
+                // a NaN block reaches the rows that see its token, no other
+                v.s[u][at >> 2] &= ~(0xFFu << (8 * (at & 3)));
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                  if (bad && slot < min(vis[t], lim)) poison[t] |= 1u << b;
+              }
+            }
+          }
+      }
+      u32x4v p[RT][VX];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        float top = fmaxf(fmaxf(fmaxf(s[t][0][0], s[t][0][1]), fmaxf(s[t][0][2], s[t][0][3])),
+                          fmaxf(fmaxf(s[t][1][0], s[t][1][1]), fmaxf(s[t][1][2], s[t][1][3])));
+        if (__ballot(top > thr[t])) {
+          top = fmaxf(mx[t], max_across_g(top) * a.sc);
+          const float base = top == kNegInf ? 0.f : top;
+          const float f = __builtin_amdgcn_exp2f(mx[t] - base);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            acc[t][b][0] *= f;
+            acc[t][b][1] *= f;
+          }
+          l[t] *= f;
+          exact[t] *= f;
+          mx[t] = top;
+          thr[t] = (top + 8.f) / a.sc;
+        }
+        const float base = mx[t] == kNegInf ? 0.f : mx[t];
+        float e[8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            e[4 * u + i] = __builtin_amdgcn_exp2f(fmaf(s[t][u][i], a.sc, -base));
+        if (VX == 1)
+          exact[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+        for (int x = 0; x < VX; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t h = pk_bf16(e[2 * i], e[2 * i + 1]);
+            p[t][x][i] = h;
+            if (x + 1 < VX) {
+              e[2 * i] -= lo_f(h);
+              e[2 * i + 1] -= hi_f(h);
+            }
+          }
+      }
+      add_values<NB, RT, VX>(v, p, acc, l);
+    }
+
+    // join the waves: every one scales its sums to the common maximum
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      poison[t] |= __shfl_xor(poison[t], 16);
+      poison[t] |= __shfl_xor(poison[t], 32);
+      const float z = VX == 1 ? cross_row_sum(exact[t]) : l[t][0];
+      if (g == 0) {
+        sh_ml[wave][16 * t + m][0] = mx[t];
+        sh_ml[wave][16 * t + m][1] = l[t][0];
+        sh_ml[wave][16 * t + m][2] = z;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float top = kNegInf;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sh_ml[w][16 * t + m][0]);
+      const float base = top == kNegInf ? 0.f : top;
+      const float f = __builtin_amdgcn_exp2f(mx[t] - base);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float h = (poison[t] >> b) & 1 ? __builtin_nanf("") : f;
+        float4 *o = reinterpret_cast<float4 *>(&sh_o[wave][m][32 * b + 8 * g]);
+        o[0] = make_float4(acc[t][b][0][0] * h, acc[t][b][1][0] * h, acc[t][b][0][1] * h,
+                           acc[t][b][1][1] * h);
+        o[1] = make_float4(acc[t][b][0][2] * h, acc[t][b][1][2] * h, acc[t][b][0][3] * h,
+                           acc[t][b][1][3] * h);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 16 * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), d = 4 * (i % (D / 4));
+        const long long r = r0 + 16 * t + row;
+        if (r < rows) {
+          float rt = kNegInf, sum = 0.f, ex = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) rt = fmaxf(rt, sh_ml[w][16 * t + row][0]);
+          const float rb = rt == kNegInf ? 0.f : rt;
+          floatx4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            const float f = __builtin_amdgcn_exp2f(sh_ml[w][16 * t + row][0] - rb);
+            sum += sh_ml[w][16 * t + row][1] * f;
+            ex += sh_ml[w][16 * t + row][2] * f;
+            o += *reinterpret_cast<const floatx4 *>(&sh_o[w][row][d]);
+          }
+          const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
+          const size_t rh = (size_t)(s0 + col) * a.heads + hd;
+          if (a.splits == 1) {
+            if (rt == kNegInf && sum == 0.f) o = floatx4{0.f, 0.f, 0.f, 0.f};
+            else o *= 16.f / sum;
+            const size_t at = (size_t)(s0 + col) * a.out_stride + (size_t)hd * D + d;
+            if (VX == 1)
+              *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+                  make_uint2(pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]));
+            else
+              *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + at) = o;
+            if (a.lse && d == 0) a.lse[rh] = (rt + log2f(ex)) * 0.69314718055994531f;
+          } else {
+            const size_t at = rh * a.splits + split;
+            if (rt != kNegInf || sum != 0.f) *reinterpret_cast<floatx4 *>(a.part + at * D + d) = o;
+            if (d == 0) *reinterpret_cast<float4 *>(a.part_ml + 4 * at) = make_float4(rt, sum, ex, 0.f);
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Joins the splits of a (row, head): one wave each, D/64 values a lane.
+template <int NB, int VX>
+__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
+  constexpr int PL = NB / 2;  // values a lane
+  const int lane = threadIdx.x & 63;
+  const long long last = (long long)min(a.v.starts[a.v.n_seqs], a.n_rows) * a.heads;
+  for (long long rh = (long long)blockIdx.x * kWaves + uniform(threadIdx.x >> 6); rh < last;
+       rh += (long long)gridDim.x * kWaves) {
+  const int row = (int)(rh / a.heads), hd = (int)(rh % a.heads);
+  if (row < a.v.starts[0]) continue;
+  const float4 *ml = reinterpret_cast<const float4 *>(a.part_ml) + rh * a.splits;
+  float top = kNegInf;
+  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, ml[s].x);
+#pragma unroll
+  for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+  const float base = top == kNegInf ? 0.f : top;
+  float sum = 0.f, ex = 0.f, o[PL];
+#pragma unroll
+  for (int j = 0; j < PL; ++j) o[j] = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float4 w = ml[s];
+    if (w.x == kNegInf && w.y == 0.f) continue;  // no tokens: its numerators were not written
+    const float f = __builtin_amdgcn_exp2f(w.x - base);
+    sum += w.y * f;
+    ex += w.z * f;
+    const float *p = a.part + (rh * a.splits + s) * (32 * NB) + lane * PL;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) o[j] = fmaf(p[j], f, o[j]);
+  }
+  const bool empty = top == kNegInf && sum == 0.f;
+  const float inv = empty ? 0.f : 16.f / sum;
+  const size_t at = (size_t)row * a.out_stride + (size_t)hd * (32 * NB) + lane * PL;
+#pragma unroll
+  for (int j = 0; j < PL; ++j) {
+    const float y = empty ? 0.f : o[j] * inv;
+    if (VX == 1) static_cast<uint16_t *>(a.out)[at + j] = (uint16_t)pk_bf16(y, 0.f);
+    else static_cast<float *>(a.out)[at + j] = y;
+  }
+  if (a.lse && lane == 0) a.lse[rh] = (top + log2f(ex)) * 0.69314718055994531f;
+  }
+}
+
+// ------------------------------------------------------------------ weights
+
+struct WeightArgs {
+  KvView v;
+  const void *q;
+  const float *lse, *acc;
+  float *acc_out;
+  long long q_stride;
+  int heads, group, n_rows;
+  float sc, decay;
+};
+
+// Workgroup (x, y, z): kv head x, tokens 128 y .. of sequence z, 32 to a
+// wave, whose operands stay in registers while the sequence's rows pass, 16
+// at a time.
+template <int NB, int VX>
+__global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
+  constexpr int D = 32 * NB;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int head = blockIdx.x, seq = blockIdx.z;
+  const int len = kv_len(a.v, seq);
+  const KvGeo geo = a.v.g;
+  const int s0 = a.v.starts[seq];
+  const int n_all = a.v.starts[seq + 1] - s0;
+  const int n = s0 < 0 ? 0 : min(a.v.starts[seq + 1], a.n_rows) - s0;
+  const long long rows = n > 0 ? (long long)n * a.group : 0;
+  const size_t cap = kv_capacity(a.v);
+  for (int t0 = (blockIdx.y * kWaves + wave) * kTile; t0 < len; t0 += gridDim.y * kWaves * kTile) {
+    const int page = uniform(a.v.table[(size_t)seq * a.v.pages_per_seq + (t0 >> geo.page_log)]);
+    const bool held = (unsigned)page < (unsigned)a.v.n_pages;
+    const uint8_t *slab = a.v.pool + ((size_t)(held ? page : 0) * a.v.hk + head) * geo.slab;
+    const int tp = t0 & (geo.page_tokens - 1);
+    KTile<NB> k[2];
+    load_k<NB>(slab, geo, tp, lane, k[0]);
+    load_k<NB>(slab, geo, tp + 16, lane, k[1]);
+    KWords<NB> kw[2];
+    decode_k<NB>(k[0], kw[0]);
+    decode_k<NB>(k[1], kw[1]);
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    // columns that see none of the tile's tokens add nothing
+    const long long c0 = held ? max(0, t0 - (len - n_all)) : n;
+    for (long long r0 = c0 * a.group / 16 * 16; r0 < rows; r0 += 16) {
+      const long long r = r0 + m;
+      const bool live = r < rows;
+      const int col = live ? (int)(r / a.group) : 0;
+      const int hd = head * a.group + (live ? (int)(r % a.group) : 0);
+      QTile<NB, VX> q;
+      load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q);
+      float z = live ? a.lse[(size_t)(s0 + col) * a.heads + hd] : 0.f;
+      int vis = live ? min(len, max(0, len - n_all + col + 1)) : 0;
+      if (z == kNegInf) vis = 0, z = 0.f;
+      z *= 1.4426950408889634f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const floatx4 s = scores<NB, VX>(kw[u], q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -z));
+          sum[4 * u + i] += t0 + 16 * u + 4 * g + i < vis ? e : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float r = sum[i];
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) r += __shfl_xor(r, off);
+      const int slot = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+      if (m == i && slot < len) {
+        const size_t at = ((size_t)seq * a.v.hk + head) * cap + slot;
+        a.acc_out[at] = fmaf(a.acc[at], a.decay, r);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct AttnPlan {
+  int rt, row_blocks, splits;
+  size_t part, ml, total;
+};
+
+// Rows of a block: 16 where a sequence has no more, or fp32 is computed in
+// three terms; 32 otherwise.  Splits: about four workgroups a compute unit,
+// each wave with a tile at least.
+AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, int n_rows,
+                   int xtype) {
+  AttnPlan p;
+  const int group = heads / c->n_kv_heads;
+  const long long rows = (long long)(b->max_cols > 1 ? b->max_cols : 1) * group;
+  p.rt = rows <= 16 || xtype == RFPX_X_F32 || c->head_dim == 256 ? 1 : 2;
+  long long rb = (rows + 16 * p.rt - 1) / (16 * p.rt);
+  const long long most_rb = (1 << 20) / c->n_kv_heads;  // a workgroup takes several beyond that
+  p.row_blocks = (int)(rb < most_rb ? rb : most_rb);
+  const long long cap = (long long)b->pages_per_seq * c->page_tokens;
+  const long long len = b->max_len < cap ? b->max_len : cap;
+  const long long wgs = (long long)b->n_seqs * c->n_kv_heads * rb;
+  const long long most = (len + kTile * kWaves - 1) / (kTile * kWaves);
+  long long s = (1024 + wgs - 1) / wgs;
+  if (s > most) s = most;
+  if (s > 128) s = 128;
+  if (s < 1) s = 1;
+  p.splits = (int)s;
+  const size_t rh = (size_t)n_rows * heads;
+  p.part = 0;
+  p.ml = align_up(p.splits > 1 ? rh * p.splits * c->head_dim * 4 : 0, 256);
+  p.total = p.ml + align_up(p.splits > 1 ? rh * p.splits * 16 : 0, 256);
+  return p;
+}
+
+rfpx_status check_heads(const char *fn, const rfpx_kv_cache *c, int heads, int n_rows, int xtype,
+                        float scale) {
+  if (!valid_xtype(xtype)) return fail(RFPX_E_ARG, "%s: xtype=%d", fn, xtype);
+  if (heads < 1 || heads > RFPX_HEADS_MAX || heads % c->n_kv_heads)
+    return fail(RFPX_E_SHAPE, "%s: %d query heads over %d kv heads", fn, heads, c->n_kv_heads);
+  if (n_rows < 0 || n_rows > RFPX_ROWS_MAX)
+    return fail(RFPX_E_SHAPE, "%s: n_rows=%d: must be in [0, %d]", fn, n_rows, RFPX_ROWS_MAX);
+  if (!(scale > 0.f) || !(scale < 1e30f)) return fail(RFPX_E_ARG, "%s: scale=%g", fn, scale);
+  return RFPX_OK;
+}
+
+template <int NB>
+hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
+  const dim3 grid(a.v.hk * p.row_blocks, p.splits, a.v.n_seqs);
+  hipError_t e;
+  if (a.xtype == RFPX_X_F32) e = launch_k(k_attn<NB, 3, 1>, grid, dim3(kThreads), 0, s, a);
+  else if (p.rt == 1) e = launch_k(k_attn<NB, 1, 1>, grid, dim3(kThreads), 0, s, a);
+  else e = launch_k(k_attn<NB, 1, NB == 8 ? 1 : 2>, grid, dim3(kThreads), 0, s, a);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const long long rh = (long long)a.n_rows * a.heads;
+  const long long jb = (rh + kWaves - 1) / kWaves;
+  const dim3 jg((unsigned)(jb < (1 << 20) ? jb : 1 << 20));
+  return a.xtype == RFPX_X_F32 ? launch_k(k_attn_join<NB, 3>, jg, dim3(kThreads), 0, s, a)
+                               : launch_k(k_attn_join<NB, 1>, jg, dim3(kThreads), 0, s, a);
+}
+
+}  // namespace
+}  // namespace rfpx
+
+using namespace rfpx;
+
+extern "C" {
+
+size_t rfpx_attn_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int n_heads,
+                                 int n_rows) {
+  const char *fn = "rfpx_attn_workspace_bytes";
+  if (check_kv(fn, c, b, false) || check_heads(fn, c, n_heads, n_rows, RFPX_X_F32, 1.f)) return 0;
+  const size_t f = attn_plan(c, b, n_heads, n_rows, RFPX_X_F32).total;
+  const size_t h = attn_plan(c, b, n_heads, n_rows, RFPX_X_BF16).total;
+  const size_t n = f > h ? f : h;
+  return n > 256 ? n : 256;  // a supported shape never reads as "unsupported"
+}
+
+rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,
+                              long long q_stride, int xtype, int n_heads, int n_rows, float scale,
+                              void *out, long long out_stride, float *lse, void *ws,
+                              size_t ws_bytes, void *stream) {
+  const char *fn = "rfpx_attn_forward";
+  rfpx_status st = check_kv(fn, c, b, true);
+  if (st) return st;
+  if ((st = check_heads(fn, c, n_heads, n_rows, xtype, scale))) return st;
+  if (n_rows == 0) return RFPX_OK;
+  if ((st = check_rows(fn, "q", q, q_stride, n_heads, c->head_dim, xtype))) return st;
+  if ((st = check_rows(fn, "out", out, out_stride, n_heads, c->head_dim, xtype))) return st;
+  if (q == out) return fail(RFPX_E_ARG, "%s: out is q", fn);
+  if ((uintptr_t)lse % 4) return fail(RFPX_E_ALIGN, "%s: lse not 4-byte aligned", fn);
+  if (!ws) return fail(RFPX_E_ARG, "%s: workspace is null", fn);
+  if ((uintptr_t)ws % 256) return fail(RFPX_E_ALIGN, "%s: workspace not 256-byte aligned", fn);
+  const AttnPlan p = attn_plan(c, b, n_heads, n_rows, xtype);
+  if (ws_bytes < p.total)
+    return fail(RFPX_E_WORKSPACE, "%s: workspace holds %zu bytes, needs %zu", fn, ws_bytes, p.total);
+  AttnArgs a{};
+  a.v = kv_view(c, b);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.part);
+  a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.ml);
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.xtype = xtype;
+  a.heads = n_heads;
+  a.group = n_heads / c->n_kv_heads;
+  a.n_rows = n_rows;
+  a.splits = p.splits;
+  a.row_blocks = p.row_blocks;
+  a.sc = 16.f * scale * 1.4426950408889634f;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = c->head_dim == 64    ? launch_attn<2>(p, a, s)
+                 : c->head_dim == 128 ? launch_attn<4>(p, a, s)
+                                      : launch_attn<8>(p, a, s);
+  return e == hipSuccess ? RFPX_OK : fail(RFPX_E_HIP, "%s: %s", fn, hipGetErrorString(e));
+}
+
+rfpx_status rfpx_attn_weights(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,
+                              long long q_stride, int xtype, int n_heads, int n_rows, float scale,
+                              const float *lse, float decay, const float *acc, float *acc_out,
+                              void *stream) {
+  const char *fn = "rfpx_attn_weights";
+  rfpx_status st = check_kv(fn, c, b, true);
+  if (st) return st;
+  if ((st = check_heads(fn, c, n_heads, n_rows, xtype, scale))) return st;
+  if (n_rows && (st = check_rows(fn, "q", q, q_stride, n_heads, c->head_dim, xtype))) return st;
+  if ((n_rows && !lse) || !acc || !acc_out)
+    return fail(RFPX_E_ARG, "%s: lse, acc or acc_out is null", fn);
+  if ((uintptr_t)lse % 4 || (uintptr_t)acc % 4 || (uintptr_t)acc_out % 4)
+    return fail(RFPX_E_ALIGN, "%s: lse, acc and acc_out must be 4-byte aligned", fn);
+  if (!(decay - decay == 0.f)) return fail(RFPX_E_ARG, "%s: decay=%g", fn, decay);
+  WeightArgs a{};
+  a.v = kv_view(c, b);
+  a.q = q;
+  a.lse = lse;
+  a.acc = acc;
+  a.acc_out = acc_out;
+  a.q_stride = q_stride;
+  a.heads = n_heads;
+  a.group = n_heads / c->n_kv_heads;
+  a.n_rows = n_rows;
+  a.sc = 16.f * scale * 1.4426950408889634f;
+  a.decay = decay;
+  const long long cap = (long long)b->pages_per_seq * c->page_tokens;
+  const long long len = b->max_len < cap ? b->max_len : cap;
+  long long gy = (len + kTile * kWaves - 1) / (kTile * kWaves);
+  if (gy < 1) gy = 1;
+  if (gy > 65535) gy = 65535;
+  const dim3 grid(c->n_kv_heads, (unsigned)gy, b->n_seqs);
+  hipStream_t s = (hipStream_t)stream;
+  const bool f = xtype == RFPX_X_F32;
+  void (*k)(WeightArgs) =
+      c->head_dim == 64    ? (f ? k_attn_weights<2, 3> : k_attn_weights<2, 1>)
+      : c->head_dim == 128 ? (f ? k_attn_weights<4, 3> : k_attn_weights<4, 1>)
+                           : (f ? k_attn_weights<8, 3> : k_attn_weights<8, 1>);
+  const hipError_t e = launch_k(k, grid, dim3(kThreads), 0, s, a);
+  return e == hipSuccess ? RFPX_OK : fail(RFPX_E_HIP, "%s: %s", fn, hipGetErrorString(e));
+}
+
+}  // extern "C"
