@@ -30,7 +30,8 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;         // waves of a workgroup whose work is split over several
+constexpr int kWavesOne = 8;      // ... and of one that has a sequence's head to itself
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32;          // tokens of one step of a wave
 constexpr float kOffset = 1.46875f;  // (16 + 7.5) / 16
@@ -273,14 +274,14 @@ __device__ __forceinline__ void add_values(const VTile<NB> &v, const u32x4v (&p)
 // ------------------------------------------------------------------ forward
 
 // Workgroup (x, y, z): kv head and row block x, split y, sequence z.  A row
-// block is 16 RT of the sequence's rows (column, head of the group); its four
-// waves share out the split's 32-token tiles and join their sums in LDS.
-template <int NB, int VX, int RT>
-__global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
+// block is 16 RT of the sequence's rows (column, head of the group); its W waves
+// share out the split's 32-token tiles and join their sums in LDS.
+template <int NB, int VX, int RT, int W>
+__global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   constexpr int D = 32 * NB;
   constexpr int LD = D + 4;
-  __shared__ float sh_ml[kWaves][RT * 16][3];
-  __shared__ __align__(16) float sh_o[kWaves][16][LD];
+  __shared__ float sh_ml[W][RT * 16][3];
+  __shared__ __align__(16) float sh_o[W][16][LD];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int head = blockIdx.x % a.v.hk, rb0 = blockIdx.x / a.v.hk;
@@ -334,17 +335,36 @@ __global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
       for (int b = 0; b < NB; ++b) acc[t][b][0] = acc[t][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
 
-    for (int tile = t_first + wave; tile < t_last; tile += kWaves) {
-      const int t0 = tile * kTile;
-      const int page = uniform(table[t0 >> geo.page_log]);
-      const bool held = (unsigned)page < (unsigned)a.v.n_pages;
-      const uint8_t *slab = a.v.pool + ((size_t)(held ? page : 0) * a.v.hk + head) * geo.slab;
-      const int tp = t0 & (geo.page_tokens - 1);
+    // a tile's loads are issued while the tile before it is computed, and its
+    // page is looked up one tile before that
+    struct Raw {
       KTile<NB> k[2];
       VTile<NB> v;
-      load_k<NB>(slab, geo, tp, lane, k[0]);
-      load_k<NB>(slab, geo, tp + 16, lane, k[1]);
-      load_v<NB>(slab, geo, tp, lane, v);
+      bool held;
+    } raw;
+    const auto page_of = [&](int tile) {
+      return scalar_read(table + ((min(tile, t_last - 1) * kTile) >> geo.page_log));
+    };
+    const auto load = [&](int tile, int page, Raw &r) {
+      const int tp = (min(tile, t_last - 1) * kTile) & (geo.page_tokens - 1);
+      r.held = (unsigned)page < (unsigned)a.v.n_pages;
+      const uint8_t *slab = a.v.pool + ((size_t)(r.held ? page : 0) * a.v.hk + head) * geo.slab;
+      load_k<NB>(slab, geo, tp, lane, r.k[0]);
+      load_k<NB>(slab, geo, tp + 16, lane, r.k[1]);
+      load_v<NB>(slab, geo, tp, lane, r.v);
+    };
+    int next_page = 0;
+    if (t_first + wave < t_last) {
+      load(t_first + wave, page_of(t_first + wave), raw);
+      next_page = page_of(t_first + wave + W);
+    }
+    for (int tile = t_first + wave; tile < t_last; tile += W) {
+      const int t0 = tile * kTile;
+      KTile<NB> k[2] = {raw.k[0], raw.k[1]};
+      VTile<NB> v = raw.v;
+      const bool held = raw.held;
+      load(tile + W, next_page, raw);
+      next_page = page_of(tile + 2 * W);
       floatx4 s[RT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -443,7 +463,7 @@ __global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
     for (int t = 0; t < RT; ++t) {
       float top = kNegInf;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sh_ml[w][16 * t + m][0]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, sh_ml[w][16 * t + m][0]);
       const float base = top == kNegInf ? 0.f : top;
       const float f = __builtin_amdgcn_exp2f(mx[t] - base);
 #pragma unroll
@@ -456,17 +476,17 @@ __global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
                            acc[t][b][1][3] * h);
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < 16 * (D / 4); i += kThreads) {
+      for (int i = threadIdx.x; i < 16 * (D / 4); i += 64 * W) {
         const int row = i / (D / 4), d = 4 * (i % (D / 4));
         const long long r = r0 + 16 * t + row;
         if (r < rows) {
           float rt = kNegInf, sum = 0.f, ex = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) rt = fmaxf(rt, sh_ml[w][16 * t + row][0]);
+          for (int w = 0; w < W; ++w) rt = fmaxf(rt, sh_ml[w][16 * t + row][0]);
           const float rb = rt == kNegInf ? 0.f : rt;
           floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
+          for (int w = 0; w < W; ++w) {
             const float f = __builtin_amdgcn_exp2f(sh_ml[w][16 * t + row][0] - rb);
             sum += sh_ml[w][16 * t + row][1] * f;
             ex += sh_ml[w][16 * t + row][2] * f;
@@ -496,45 +516,58 @@ __global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
   }
 }
 
-// Joins the splits of a (row, head): one wave each, D/64 values a lane.
+// Joins the splits of a (row, head): a workgroup each, four values a thread,
+// the splits dealt out over the 1024/D groups of threads.
 template <int NB, int VX>
 __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
-  constexpr int PL = NB / 2;  // values a lane
-  const int lane = threadIdx.x & 63;
+  constexpr int D = 32 * NB, TG = D / 4, NG = kThreads / TG;
+  __shared__ __align__(16) float sh_o[NG][D];
+  __shared__ float sh_s[NG][2];
+  const int g = threadIdx.x / TG, d = 4 * (threadIdx.x % TG), lane = threadIdx.x & 63;
   const long long last = (long long)min(a.v.starts[a.v.n_seqs], a.n_rows) * a.heads;
-  for (long long rh = (long long)blockIdx.x * kWaves + uniform(threadIdx.x >> 6); rh < last;
-       rh += (long long)gridDim.x * kWaves) {
-  const int row = (int)(rh / a.heads), hd = (int)(rh % a.heads);
-  if (row < a.v.starts[0]) continue;
-  const float4 *ml = reinterpret_cast<const float4 *>(a.part_ml) + rh * a.splits;
-  float top = kNegInf;
-  for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, ml[s].x);
+  for (long long rh = blockIdx.x; rh < last; rh += gridDim.x) {
+    const int row = (int)(rh / a.heads), hd = (int)(rh % a.heads);
+    if (row < a.v.starts[0]) continue;
+    const float4 *ml = reinterpret_cast<const float4 *>(a.part_ml) + rh * a.splits;
+    float top = kNegInf;
+    for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, ml[s].x);
 #pragma unroll
-  for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-  const float base = top == kNegInf ? 0.f : top;
-  float sum = 0.f, ex = 0.f, o[PL];
-#pragma unroll
-  for (int j = 0; j < PL; ++j) o[j] = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float4 w = ml[s];
-    if (w.x == kNegInf && w.y == 0.f) continue;  // no tokens: its numerators were not written
-    const float f = __builtin_amdgcn_exp2f(w.x - base);
-    sum += w.y * f;
-    ex += w.z * f;
-    const float *p = a.part + (rh * a.splits + s) * (32 * NB) + lane * PL;
-#pragma unroll
-    for (int j = 0; j < PL; ++j) o[j] = fmaf(p[j], f, o[j]);
-  }
-  const bool empty = top == kNegInf && sum == 0.f;
-  const float inv = empty ? 0.f : 16.f / sum;
-  const size_t at = (size_t)row * a.out_stride + (size_t)hd * (32 * NB) + lane * PL;
-#pragma unroll
-  for (int j = 0; j < PL; ++j) {
-    const float y = empty ? 0.f : o[j] * inv;
-    if (VX == 1) static_cast<uint16_t *>(a.out)[at + j] = (uint16_t)pk_bf16(y, 0.f);
-    else static_cast<float *>(a.out)[at + j] = y;
-  }
-  if (a.lse && lane == 0) a.lse[rh] = (top + log2f(ex)) * 0.69314718055994531f;
+    for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    const float base = top == kNegInf ? 0.f : top;
+    float sum = 0.f, ex = 0.f;
+    floatx4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = g; s < a.splits; s += NG) {
+      const float4 w = ml[s];
+      if (w.x == kNegInf && w.y == 0.f) continue;  // no tokens: its numerators were not written
+      const float f = __builtin_amdgcn_exp2f(w.x - base);
+      sum += w.y * f;
+      ex += w.z * f;
+      o += *reinterpret_cast<const floatx4 *>(a.part + (rh * a.splits + s) * D + d) * f;
+    }
+    *reinterpret_cast<floatx4 *>(&sh_o[g][d]) = o;
+    if (d == 0) {
+      sh_s[g][0] = sum;
+      sh_s[g][1] = ex;
+    }
+    __syncthreads();
+    if (g == 0) {
+      for (int i = 1; i < NG; ++i) {
+        sum += sh_s[i][0];
+        ex += sh_s[i][1];
+        o += *reinterpret_cast<const floatx4 *>(&sh_o[i][d]);
+      }
+      if (top == kNegInf && sum == 0.f) o = floatx4{0.f, 0.f, 0.f, 0.f};
+      else o *= 16.f / sum;
+      const size_t at = (size_t)row * a.out_stride + (size_t)hd * D + d;
+      if (VX == 1)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+            make_uint2(pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]));
+      else
+        *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + at) = o;
+      if (a.lse && d == 0) a.lse[rh] = (top + log2f(ex)) * 0.69314718055994531f;
+    }
+    __syncthreads();
   }
 }
 
@@ -620,13 +653,14 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
 // ---------------------------------------------------------------- host side
 
 struct AttnPlan {
-  int rt, row_blocks, splits;
+  int rt, row_blocks, splits, waves;
   size_t part, ml, total;
 };
 
 // Rows of a block: 16 where a sequence has no more, or fp32 is computed in
-// three terms; 32 otherwise.  Splits: about four workgroups a compute unit,
-// each wave with a tile at least.
+// three terms; 32 otherwise.  A short sequence is one workgroup's, with no
+// second launch; a longer one is split so that there are about two workgroups
+// a compute unit, each wave with a tile at least.
 AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, int n_rows,
                    int xtype) {
   AttnPlan p;
@@ -639,12 +673,19 @@ AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, in
   const long long cap = (long long)b->pages_per_seq * c->page_tokens;
   const long long len = b->max_len < cap ? b->max_len : cap;
   const long long wgs = (long long)b->n_seqs * c->n_kv_heads * rb;
-  const long long most = (len + kTile * kWaves - 1) / (kTile * kWaves);
-  long long s = (1024 + wgs - 1) / wgs;
-  if (s > most) s = most;
-  if (s > 128) s = 128;
-  if (s < 1) s = 1;
-  p.splits = (int)s;
+  const long long tiles = (len + kTile - 1) / kTile;
+  if (tiles <= 4 * kWavesOne && wgs < 512 && c->head_dim < 256) {
+    p.waves = kWavesOne;
+    p.splits = 1;
+  } else {
+    p.waves = kWaves;
+    const long long most = (tiles + kWaves - 1) / kWaves;
+    long long s = (512 + wgs - 1) / wgs;
+    if (s > most) s = most;
+    if (s > 128) s = 128;
+    if (s < 1) s = 1;
+    p.splits = (int)s;
+  }
   const size_t rh = (size_t)n_rows * heads;
   p.part = 0;
   p.ml = align_up(p.splits > 1 ? rh * p.splits * c->head_dim * 4 : 0, 256);
@@ -665,17 +706,20 @@ rfpx_status check_heads(const char *fn, const rfpx_kv_cache *c, int heads, int n
 
 template <int NB>
 hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
-  const dim3 grid(a.v.hk * p.row_blocks, p.splits, a.v.n_seqs);
-  hipError_t e;
-  if (a.xtype == RFPX_X_F32) e = launch_k(k_attn<NB, 3, 1>, grid, dim3(kThreads), 0, s, a);
-  else if (p.rt == 1) e = launch_k(k_attn<NB, 1, 1>, grid, dim3(kThreads), 0, s, a);
-  else e = launch_k(k_attn<NB, 1, NB == 8 ? 1 : 2>, grid, dim3(kThreads), 0, s, a);
+  const dim3 grid(a.v.hk * p.row_blocks, p.splits, a.v.n_seqs), block(64 * p.waves);
+  constexpr int RT = NB == 8 ? 1 : 2;
+  constexpr int W1 = NB == 8 ? kWaves : kWavesOne;  // heads of 256 leave no registers for more
+  const bool one = p.waves == kWavesOne;
+  void (*k)(AttnArgs) =
+      a.xtype == RFPX_X_F32 ? (one ? k_attn<NB, 3, 1, W1> : k_attn<NB, 3, 1, kWaves>)
+      : p.rt == 1           ? (one ? k_attn<NB, 1, 1, W1> : k_attn<NB, 1, 1, kWaves>)
+                            : (one ? k_attn<NB, 1, RT, W1> : k_attn<NB, 1, RT, kWaves>);
+  const hipError_t e = launch_k(k, grid, block, 0, s, a);
   if (e != hipSuccess || p.splits == 1) return e;
   const long long rh = (long long)a.n_rows * a.heads;
-  const long long jb = (rh + kWaves - 1) / kWaves;
-  const dim3 jg((unsigned)(jb < (1 << 20) ? jb : 1 << 20));
-  return a.xtype == RFPX_X_F32 ? launch_k(k_attn_join<NB, 3>, jg, dim3(kThreads), 0, s, a)
-                               : launch_k(k_attn_join<NB, 1>, jg, dim3(kThreads), 0, s, a);
+  const dim3 jg((unsigned)(rh < (1 << 20) ? rh : 1 << 20));
+  return launch_k(a.xtype == RFPX_X_F32 ? k_attn_join<NB, 3> : k_attn_join<NB, 1>, jg,
+                  dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

@@ -53,6 +53,11 @@ struct KvView {
 
 #if defined(__HIPCC__)
 
+// A uniform read of device data that no kernel of the call writes: a scalar
+// load, which waits for no vector load in flight.
+__device__ __forceinline__ int scalar_read(const int32_t *p) {
+  return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
+}
 __device__ __forceinline__ int kv_capacity(const KvView &v) {
   const long long cap = (long long)v.pages_per_seq * v.g.page_tokens;
   return cap < 0x7FFFFFFF ? (int)cap : 0x7FFFFFFF;
