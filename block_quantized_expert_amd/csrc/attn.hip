@@ -571,6 +571,356 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
   }
 }
 
+// ------------------------------------------------------- forward, many rows
+//
+// Where a sequence brings many rows, decoding is shared: a workgroup of eight
+// waves, 32 rows each, decodes 64 tokens at a time to exact bf16 values in
+// LDS, in the order in which the 32x32x16 matrix instruction's operands are
+// read (16 bytes a lane, adjacent lanes adjacent), while it computes the 64
+// before.  The offset comes off in the decoding (one dot instruction a value:
+// word * 1 + other * 0 - offset), so no product is spent on it.  Lane (row m
+// = lane & 31, h = lane >> 5) holds of its row the scores of tokens 8 j + 4 h
+// + i (i < 4, j < 4) of 32, and the second product takes j = 2 s and 2 s + 1
+// as its step s from that very lane.
+constexpr int kChunkWaves = 8;
+constexpr int kChunkRows = 32 * kChunkWaves;
+constexpr int kChunkTile = 64;
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ floatx16 mfma32(const u32x4v &a, const u32x4v &b, const floatx16 &c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// The bf16 pairs (1, 0) and (0, 1) in vector registers: as literals the
+// compiler takes them for the inline constant 1.0, which the dot instruction
+// reads as a pair of its own.
+struct Pick {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Pick make_pick() {
+  Pick p;
+  asm("v_mov_b32 %0, 0x3f80" : "=v"(p.lo));
+  asm("v_mov_b32 %0, 0x3f800000" : "=v"(p.hi));
+  return p;
+}
+
+// The pair of values of a pair of code words, less their blocks' offsets
+// (fp32, negative): exact, as bf16.
+__device__ __forceinline__ uint32_t exact_pair(uint32_t w, float neg_lo, float neg_hi, Pick one) {
+  const float lo = dot2(w, one.lo, neg_lo), hi = dot2(w, one.hi, neg_hi);
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+// -1.46875 * 2^(e-127); NaN for e = 255.
+__device__ __forceinline__ float neg_offset(uint32_t e) {
+  return __uint_as_float(0x803C0000u | e << 23);
+}
+
+// A lane's share of 64 tokens: of the keys one token's octet of every block
+// (waves 0..3, 16 tokens each), of the values byte r of every block of four
+// tokens (waves 4..7, 16 tokens each).
+template <int NB>
+struct ChunkRaw {
+  uint32_t c[NB];
+  uint32_t s[NB];  // keys: the token's scales; values: those of the four tokens
+};
+
+template <int NB>
+__device__ __forceinline__ void chunk_load(const uint8_t *slab, const KvGeo &g, int tp, bool key,
+                                           int lane, ChunkRaw<NB> &r) {
+  if (key) {
+    load_words<NB>(slab + g.kc + tp * (16 * NB) + lane * (4 * NB), r.c);
+    const uint8_t *s = slab + g.ks + (tp + (lane >> 2)) * NB;
+    if constexpr (NB == 2) r.s[0] = *reinterpret_cast<const uint16_t *>(s);
+    else if constexpr (NB == 4) r.s[0] = *reinterpret_cast<const uint32_t *>(s);
+    else load_words<2>(s, r.s);
+  } else {
+    load_words<NB>(slab + g.vc + tp * (16 * NB) + lane * (4 * NB), r.c);
+    load_words<NB>(slab + g.vs + (tp + 4 * (lane >> 4)) * NB, r.s);
+  }
+}
+
+// LDS of one decoded tile: keys [32-token half][step of 16 values][h][token]
+// [16 bytes], values [step of 16 tokens][block][h][value][16 bytes].
+template <int NB>
+struct ChunkTile {
+  u32x4v k[2][2 * NB][2][32];
+  u32x4v v[4][NB][2][32];
+};
+
+template <int NB>
+__device__ __forceinline__ void chunk_decode_k(const ChunkRaw<NB> &r, int w, int lane, Pick one,
+                                               ChunkTile<NB> &t) {
+  const int tok = 16 * w + (lane >> 2), g = lane & 3;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const uint32_t e = (r.s[b >> 2] >> (8 * (b & 3))) & 0xFFu;
+    const uint32_t base = e << 7 | e << 23;
+    const float neg = neg_offset(e);
+    u32x4v o;
+    o[0] = exact_pair(and_or(r.c[b] << 3, kCodeMask, base), neg, neg, one);
+    o[1] = exact_pair(and_or(r.c[b] >> 1, kCodeMask, base), neg, neg, one);
+    o[2] = exact_pair(and_or(r.c[b] >> 5, kCodeMask, base), neg, neg, one);
+    o[3] = exact_pair(and_or(r.c[b] >> 9, kCodeMask, base), neg, neg, one);
+    t.k[tok >> 5][2 * b + (g >> 1)][g & 1][tok & 31] = o;
+  }
+}
+
+template <int NB>
+__device__ __forceinline__ void chunk_decode_v(const ChunkRaw<NB> &r, int w, int lane, Pick one,
+                                               ChunkTile<NB> &t) {
+  const int grp = lane >> 4, m = lane & 15;  // step w, tokens 4 grp .. of its 16
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    uint32_t even[2], odd[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int a0 = 2 * i * NB + b, a1 = a0 + NB;
+      const uint32_t e0 = (r.s[a0 >> 2] >> (8 * (a0 & 3))) & 0xFFu;
+      const uint32_t e1 = (r.s[a1 >> 2] >> (8 * (a1 & 3))) & 0xFFu;
+      const uint32_t base = e0 << 7 | e1 << 23;
+      const float n0 = neg_offset(e0), n1 = neg_offset(e1);
+      const uint32_t c = r.c[i * (NB / 2) + (b >> 1)];
+      even[i] = exact_pair(and_or(b & 1 ? c >> 5 : c << 3, kCodeMask, base), n0, n1, one);
+      odd[i] = exact_pair(and_or(b & 1 ? c >> 9 : c >> 1, kCodeMask, base), n0, n1, one);
+    }
+    uint2 *u = reinterpret_cast<uint2 *>(&t.v[w][b][grp & 1][2 * m]);
+    u[grp >> 1] = make_uint2(even[0], even[1]);
+    u[2 + (grp >> 1)] = make_uint2(odd[0], odd[1]);
+  }
+}
+
+template <int NB>
+__global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
+  constexpr int D = 32 * NB;
+  extern __shared__ __align__(16) uint8_t lds[];
+  ChunkTile<NB> *tiles = reinterpret_cast<ChunkTile<NB> *>(lds);                // [2]
+  uint16_t *bad = reinterpret_cast<uint16_t *>(lds + 2 * sizeof(ChunkTile<NB>));  // [2][4][NB]
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int m = lane & 31, h = lane >> 5;
+  const int head = blockIdx.x % a.v.hk, rb0 = blockIdx.x / a.v.hk;
+  const int split = blockIdx.y, seq = blockIdx.z;
+  const int s0 = a.v.starts[seq];
+  const int n_all = a.v.starts[seq + 1] - s0;
+  const int n = min(a.v.starts[seq + 1], a.n_rows) - s0;
+  if (s0 < 0 || n <= 0) return;
+  const int len = kv_len(a.v, seq);
+  const long long rows = (long long)n * a.group;
+  const KvGeo geo = a.v.g;
+  const int32_t *table = a.v.table + (size_t)seq * a.v.pages_per_seq;
+  const bool key = wave < 4;
+  const Pick pick = make_pick();
+  const uint32_t ones = one_one_vgpr_pure();
+  const int w4 = wave & 3;
+
+  for (long long r0 = (long long)rb0 * kChunkRows; r0 < rows;
+       r0 += (long long)a.row_blocks * kChunkRows) {
+    const auto sees = [&](long long r) {  // slots that a row sees
+      if (r >= rows) r = rows - 1;
+      return min(len, max(0, len - n_all + (int)(r / a.group) + 1));
+    };
+    const int last_vis = sees(r0 + kChunkRows - 1);
+    const int first_vis = sees(r0), wave_last = sees(r0 + 32 * wave + 31);
+    const bool wave_live = r0 + 32 * wave < rows;
+    long long r = r0 + 32 * wave + m;
+    const bool live = r < rows;
+    if (!live) r = rows - 1;
+    const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
+    const int vis = sees(r);
+    u32x4v q[2 * NB];
+    {
+      const uint16_t *p = static_cast<const uint16_t *>(a.q) + (size_t)(s0 + col) * a.q_stride +
+                          (size_t)hd * D + 8 * h;
+#pragma unroll
+      for (int ks = 0; ks < 2 * NB; ++ks) {
+        const uint4 d = *reinterpret_cast<const uint4 *>(p + 16 * ks);
+        q[ks][0] = __builtin_amdgcn_perm(d.z, d.x, 0x05040100u);
+        q[ks][1] = __builtin_amdgcn_perm(d.z, d.x, 0x07060302u);
+        q[ks][2] = __builtin_amdgcn_perm(d.w, d.y, 0x05040100u);
+        q[ks][3] = __builtin_amdgcn_perm(d.w, d.y, 0x07060302u);
+      }
+    }
+    const int all = (last_vis + kChunkTile - 1) / kChunkTile;
+    const int per = (all + a.splits - 1) / a.splits;
+    const int t_first = min(all, split * per), t_last = min(all, t_first + per);
+
+    floatx16 acc[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
+    float mx = kNegInf, thr = kNegInf, sum = 0.f, exact = 0.f;
+    uint32_t poison = 0;
+
+    // the page of a token (of the table's last token, past its end)
+    const auto page_at = [&](int token) {
+      return scalar_read(table + min(token >> geo.page_log, a.v.pages_per_seq - 1));
+    };
+    const auto is_page = [&](int page) { return (unsigned)page < (unsigned)a.v.n_pages; };
+    // every row sees every token of the tile
+    const auto is_whole = [&](int tile) {
+      const int t0 = tile * kChunkTile;
+      return t0 + kChunkTile <= first_vis && is_page(page_at(t0)) && is_page(page_at(t0 + 32));
+    };
+    // the page of this wave's 16 tokens of a tile
+    const auto page_of = [&](int tile) {
+      return page_at(min(tile, t_last - 1) * kChunkTile + 16 * w4);
+    };
+    const auto load = [&](int tile, int page, ChunkRaw<NB> &raw) {
+      const int tp = (min(tile, t_last - 1) * kChunkTile + 16 * w4) & (geo.page_tokens - 1);
+      const bool in = is_page(page);
+      chunk_load<NB>(a.v.pool + ((size_t)(in ? page : 0) * a.v.hk + head) * geo.slab, geo, tp, key,
+                     lane, raw);
+    };
+    // Decode the wave's share into `buf`.  Tokens that no row may read lose
+    // their scales; value blocks marked NaN in a tile that some row sees only
+    // a part of become 0 here and a bit in `bad`.
+    const auto decode = [&](int tile, int page, ChunkRaw<NB> &raw, int buf) {
+      const int first = tile * kChunkTile + 16 * w4;
+      const int lim = is_page(page) ? len : 0;
+      if (key) {
+        if (first + 16 > lim && first + (lane >> 2) >= lim) {
+#pragma unroll
+          for (int i = 0; i < (NB + 3) / 4; ++i) raw.s[i] = 0;
+        }
+        chunk_decode_k<NB>(raw, w4, lane, pick, tiles[buf]);
+      } else {
+        if (!is_whole(tile)) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            uint32_t mask = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = i * NB + b;
+              const bool out = first + 4 * (lane >> 4) + i >= lim;
+              const bool nan = !out && ((raw.s[at >> 2] >> (8 * (at & 3))) & 0xFFu) == 255u;
+              if (out || nan) raw.s[at >> 2] &= ~(0xFFu << (8 * (at & 3)));
+              const uint64_t v = __ballot(nan);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) mask |= (uint32_t)((v >> (16 * g)) & 1) << (4 * g + i);
+            }
+            if (lane == 0) bad[(buf * 4 + w4) * NB + b] = (uint16_t)mask;
+          }
+        }
+        chunk_decode_v<NB>(raw, w4, lane, pick, tiles[buf]);
+      }
+    };
+
+    ChunkRaw<NB> raw;
+    int page = 0;
+    if (t_first < t_last) {
+      page = page_of(t_first);
+      load(t_first, page, raw);
+      __syncthreads();
+      decode(t_first, page, raw, 0);
+      page = page_of(t_first + 1);
+      load(t_first + 1, page, raw);
+    }
+    for (int tile = t_first; tile < t_last; ++tile) {
+      const int buf = (tile - t_first) & 1;
+      __syncthreads();
+      if (tile + 1 < t_last) {
+        decode(tile + 1, page, raw, buf ^ 1);
+        page = page_of(tile + 2);
+        load(tile + 2, page, raw);
+      }
+      const int t0 = tile * kChunkTile;
+      if (!wave_live || t0 >= wave_last) continue;
+      const ChunkTile<NB> &t = tiles[buf];
+      const bool whole = is_whole(tile);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        floatx16 s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 2 * NB; ++ks) s = mfma32(t.k[u][ks][h][m], q[ks], s);
+        if (!whole) {
+          const int lim = is_page(page_at(t0 + 32 * u)) ? vis : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (t0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) s[i] = kNegInf;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t v = bad[(buf * 4 + 2 * u) * NB + b] |
+                               (uint32_t)bad[(buf * 4 + 2 * u + 1) * NB + b] << 16;
+            const int seen = lim - (t0 + 32 * u);
+            if (seen > 0 && (v & (seen >= 32 ? 0xFFFFFFFFu : (1u << seen) - 1u))) poison |= 1u << b;
+          }
+        }
+        float top = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+        if (__ballot(top > thr)) {
+          const uint32_t x = __float_as_uint(top);
+          const auto sw = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+          top = fmaxf(mx, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * a.sc);
+          const float f = __builtin_amdgcn_exp2f(mx - (top == kNegInf ? 0.f : top));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[b] *= f;
+          sum *= f;
+          exact *= f;
+          mx = top;
+          thr = (top + 8.f) / a.sc;
+        }
+        const float base = mx == kNegInf ? 0.f : mx;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -base));
+        if (a.lse) {
+          float x = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x += s[i];
+          exact += x;
+        }
+        u32x4v p[2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          p[i >> 2][i & 3] = pk_bf16(s[2 * i], s[2 * i + 1]);
+          sum = dot2(p[i >> 2][i & 3], ones, sum);
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[b] = mfma32(t.v[2 * u + st][b][h][m], p[st], acc[b]);
+      }
+    }
+    __syncthreads();
+
+    sum += __shfl_xor(sum, 32);
+    exact += __shfl_xor(exact, 32);
+    poison |= __shfl_xor(poison, 32);
+    if (live) {
+      const size_t rh = (size_t)(s0 + col) * a.heads + hd;
+      const bool empty = mx == kNegInf && sum == 0.f;
+      const float inv = a.splits > 1 ? 1.f : empty ? 0.f : 16.f / sum;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float f = (poison >> b) & 1 ? __builtin_nanf("") : inv;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          floatx4 o = {acc[b][4 * j], acc[b][4 * j + 1], acc[b][4 * j + 2], acc[b][4 * j + 3]};
+          o *= f;
+          const int d = 32 * b + 8 * j + 4 * h;
+          if (a.splits == 1)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) +
+                                       (size_t)(s0 + col) * a.out_stride + (size_t)hd * D + d) =
+                make_uint2(pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]));
+          else
+            *reinterpret_cast<floatx4 *>(a.part + (rh * a.splits + split) * D + d) = o;
+        }
+      }
+      if (h == 0) {
+        if (a.splits > 1)
+          *reinterpret_cast<float4 *>(a.part_ml + 4 * (rh * a.splits + split)) =
+              make_float4(mx, sum, exact, 0.f);
+        else if (a.lse)
+          a.lse[rh] = (mx + log2f(exact)) * 0.69314718055994531f;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ weights
 
 struct WeightArgs {
@@ -652,8 +1002,11 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
 
 // ---------------------------------------------------------------- host side
 
+constexpr int kChunkMin = 64;  // more rows of a sequence than this go to k_attn_chunk
+
 struct AttnPlan {
   int rt, row_blocks, splits, waves;
+  bool chunk;
   size_t part, ml, total;
 };
 
@@ -667,14 +1020,24 @@ AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, in
   const int group = heads / c->n_kv_heads;
   const long long rows = (long long)(b->max_cols > 1 ? b->max_cols : 1) * group;
   p.rt = rows <= 16 || xtype == RFPX_X_F32 || c->head_dim == 256 ? 1 : 2;
-  long long rb = (rows + 16 * p.rt - 1) / (16 * p.rt);
+  p.chunk = rows > kChunkMin && xtype == RFPX_X_BF16;
+  const int block = p.chunk ? kChunkRows : 16 * p.rt;
+  long long rb = (rows + block - 1) / block;
   const long long most_rb = (1 << 20) / c->n_kv_heads;  // a workgroup takes several beyond that
   p.row_blocks = (int)(rb < most_rb ? rb : most_rb);
   const long long cap = (long long)b->pages_per_seq * c->page_tokens;
   const long long len = b->max_len < cap ? b->max_len : cap;
   const long long wgs = (long long)b->n_seqs * c->n_kv_heads * rb;
   const long long tiles = (len + kTile - 1) / kTile;
-  if (tiles <= 4 * kWavesOne && wgs < 512 && c->head_dim < 256) {
+  if (p.chunk) {
+    p.waves = kChunkWaves;
+    const long long most = (len + 8 * kChunkTile - 1) / (8 * kChunkTile);
+    long long s = (256 + wgs - 1) / wgs;
+    if (s > most) s = most;
+    if (s > 64) s = 64;
+    if (s < 1) s = 1;
+    p.splits = (int)s;
+  } else if (tiles <= 4 * kWavesOne && wgs < 512 && c->head_dim < 256) {
     p.waves = kWavesOne;
     p.splits = 1;
   } else {
@@ -711,10 +1074,12 @@ hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
   constexpr int W1 = NB == 8 ? kWaves : kWavesOne;  // heads of 256 leave no registers for more
   const bool one = p.waves == kWavesOne;
   void (*k)(AttnArgs) =
-      a.xtype == RFPX_X_F32 ? (one ? k_attn<NB, 3, 1, W1> : k_attn<NB, 3, 1, kWaves>)
+      p.chunk               ? k_attn_chunk<NB>
+      : a.xtype == RFPX_X_F32 ? (one ? k_attn<NB, 3, 1, W1> : k_attn<NB, 3, 1, kWaves>)
       : p.rt == 1           ? (one ? k_attn<NB, 1, 1, W1> : k_attn<NB, 1, 1, kWaves>)
                             : (one ? k_attn<NB, 1, RT, W1> : k_attn<NB, 1, RT, kWaves>);
-  const hipError_t e = launch_k(k, grid, block, 0, s, a);
+  const size_t lds = p.chunk ? 2 * sizeof(ChunkTile<NB>) + 2 * 4 * NB * 2 : 0;
+  const hipError_t e = launch_k(k, grid, block, lds, s, a);
   if (e != hipSuccess || p.splits == 1) return e;
   const long long rh = (long long)a.n_rows * a.heads;
   const dim3 jg((unsigned)(rh < (1 << 20) ? rh : 1 << 20));

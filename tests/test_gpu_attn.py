@@ -413,6 +413,9 @@ def test_norm_rope_forms():
     ([200, 40], [130, 40], 2, 4, 128, 64),
     ([333], [100], 1, 3, 64, 32),
     ([150], [150], 1, 2, 256, 64),
+    ([500, 70, 64], [17, 70, 33], 2, 4, 128, 32),
+    ([1500], [66], 1, 5, 64, 256),
+    ([40, 1200], [9, 9], 2, 16, 128, 64),
 ])
 def test_attention(lens, cols, hk, group, d, page, dtype):
     t = torch()
@@ -442,37 +445,38 @@ def test_attention_rows_that_see_nothing(dtype):
         assert bool((out[part] == 7).all()) and bool((z[part] == 7).all())
 
 
-@pytest.mark.parametrize("splits", [False, True])
+@pytest.mark.parametrize("n,heads", [(60, 4), (1500, 4), (90, 40), (3000, 40)])
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_attention_nan_reaches_those_who_see_it(dtype, splits):
+def test_attention_nan_reaches_those_who_see_it(dtype, n, heads):
     t = torch()
-    n = 1500 if splits else 60
     c = Case([n, 50], [4, 2], 2, 128, 32, dt(dtype))
     bad_k, bad_v = c.k_in[n - 4:n].clone(), c.v_in[n - 4:n].clone()
     bad_v[2, 0, 40] = float("nan")   # column 2's values of head 0, block 1
     bad_k[3, 1, 7] = float("inf")    # column 3's keys of head 1
     k, v = t.cat([bad_k, c.k_in[-2:]]), t.cat([bad_v, c.v_in[-2:]])
     bqe.rfpx_kv_append(c.cache, c.batch, k, v)
-    q, out, z, scale = attend(c, 4, dt(dtype))
+    q, out, z, scale = attend(c, heads, dt(dtype))
+    g = heads // 2  # query heads of a kv head
     o = out.float().cpu().numpy()
     assert np.isfinite(o[:2]).all() and np.isfinite(o[4:]).all()
-    assert np.isnan(o[2:4, :2, 32:64]).all()
+    assert np.isnan(o[2:4, :g, 32:64]).all()
     keep = np.ones(128, bool)
     keep[32:64] = False
-    assert np.isfinite(o[2:4, :2][..., keep]).all()
-    assert np.isfinite(o[2, 2:]).all() and np.isnan(o[3, 2:]).all()
+    assert np.isfinite(o[2:4, :g][..., keep]).all()
+    assert np.isfinite(o[2, g:]).all() and np.isnan(o[3, g:]).all()
     zz = z.cpu().numpy()
-    assert np.isnan(zz[3, 2:]).all() and np.isfinite(zz[:3]).all() and np.isfinite(zz[3, :2]).all()
+    assert np.isnan(zz[3, g:]).all() and np.isfinite(zz[:3]).all() and np.isfinite(zz[3, :g]).all()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_attention_bad_pages_hold_nothing(dtype):
+@pytest.mark.parametrize("heads", [4, 70])
+def test_attention_bad_pages_hold_nothing(dtype, heads):
     c = Case([200, 40], [2, 3], 2, 128, 32, dt(dtype))
     ref_vals = c.values()
     c.table[0, 1], c.table[0, 4] = -1, c.cache.n_pages
     c.table[1, :] = 2 ** 31 - 1
     c.values = lambda: ref_vals
-    q, out, z, scale = attend(c, 4, dt(dtype))
+    q, out, z, scale = attend(c, heads, dt(dtype))
     ref = attend64(c, q, scale, seen=lambda b, j: b == 0 and j // 32 not in (1, 4))
     check_out(out, ref, dt(dtype), slice(0, c.rows))
     check_lse(z, ref, slice(0, c.rows))
