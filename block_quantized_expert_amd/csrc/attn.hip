@@ -1000,6 +1000,136 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
   }
 }
 
+// Many rows.  A workgroup takes two 32-token tiles, one from each end of the
+// sequence, one after the other: rows see early tokens more than late ones,
+// and so every workgroup has about the same to do.  A tile's keys are decoded
+// to exact bf16 operands once, by every wave for itself, and stay in registers
+// while the eight waves share out the rows, 32 at a time, straight from
+// memory; their sums meet in LDS.
+template <int NB, int VX>
+__global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightArgs a) {
+  constexpr int D = 32 * NB, KS = 2 * NB;
+  __shared__ float red[kChunkWaves][32];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int m = lane & 31, h = lane >> 5;
+  const int head = blockIdx.x, seq = blockIdx.z;
+  const int len = kv_len(a.v, seq);
+  const KvGeo geo = a.v.g;
+  const int s0 = a.v.starts[seq];
+  const int n_all = a.v.starts[seq + 1] - s0;
+  const int n = s0 < 0 ? 0 : min(a.v.starts[seq + 1], a.n_rows) - s0;
+  const long long rows = n > 0 ? (long long)n * a.group : 0;
+  const size_t cap = kv_capacity(a.v);
+  const int tiles = (len + 31) / 32;
+  const Pick pick = make_pick();
+  const auto sees = [&](long long r) {
+    return min(len, max(0, len - n_all + (int)(r / a.group) + 1));
+  };
+  for (int turn = 2 * blockIdx.y; turn < tiles;
+       turn = turn & 1 ? turn + 2 * (int)gridDim.y - 1 : turn + 1) {
+    const int t0 = 32 * (turn & 1 ? tiles - 1 - (turn >> 1) : turn >> 1);
+    const int page = scalar_read(a.v.table + (size_t)seq * a.v.pages_per_seq + (t0 >> geo.page_log));
+    const bool held = (unsigned)page < (unsigned)a.v.n_pages;
+    const uint8_t *slab = a.v.pool + ((size_t)(held ? page : 0) * a.v.hk + head) * geo.slab;
+    const int tp = (t0 & (geo.page_tokens - 1)) + m;
+    uint32_t c[2][NB], sb[(NB + 3) / 4];
+    load_words<NB>(slab + geo.kc + tp * (16 * NB) + h * (4 * NB), c[0]);
+    load_words<NB>(slab + geo.kc + tp * (16 * NB) + (2 + h) * (4 * NB), c[1]);
+    const uint8_t *sp = slab + geo.ks + tp * NB;
+    if constexpr (NB == 2) sb[0] = *reinterpret_cast<const uint16_t *>(sp);
+    else if constexpr (NB == 4) sb[0] = *reinterpret_cast<const uint32_t *>(sp);
+    else load_words<2>(sp, sb);
+    u32x4v k[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int b = ks >> 1;
+      const uint32_t e = (sb[b >> 2] >> (8 * (b & 3))) & 0xFFu, w = c[ks & 1][b];
+      const uint32_t base = e << 7 | e << 23;
+      const float neg = neg_offset(e);
+      k[ks][0] = exact_pair(and_or(w << 3, kCodeMask, base), neg, neg, pick);
+      k[ks][1] = exact_pair(and_or(w >> 1, kCodeMask, base), neg, neg, pick);
+      k[ks][2] = exact_pair(and_or(w >> 5, kCodeMask, base), neg, neg, pick);
+      k[ks][3] = exact_pair(and_or(w >> 9, kCodeMask, base), neg, neg, pick);
+    }
+    float sum[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+    // columns that see none of the tile's tokens add nothing
+    const long long first = (long long)max(0, t0 - (len - n_all)) * a.group / 32;
+    for (long long r0 = 32 * (first + wave); held && r0 < rows; r0 += 32 * kChunkWaves) {
+      const bool live = r0 + m < rows;
+      const long long r = live ? r0 + m : rows - 1;
+      const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
+      const size_t at = (size_t)(s0 + col) * a.q_stride + (size_t)hd * D + 8 * h;
+      floatx16 s;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 0.f;
+      if constexpr (VX == 1) {
+        uint4 d[KS];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+          d[ks] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at + 16 * ks);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const u32x4v q = {__builtin_amdgcn_perm(d[ks].z, d[ks].x, 0x05040100u),
+                            __builtin_amdgcn_perm(d[ks].z, d[ks].x, 0x07060302u),
+                            __builtin_amdgcn_perm(d[ks].w, d[ks].y, 0x05040100u),
+                            __builtin_amdgcn_perm(d[ks].w, d[ks].y, 0x07060302u)};
+          s = mfma32(k[ks], q, s);
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at + 16 * ks);
+          const float4 x = p[0], y = p[1];
+          float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int t = 0; t < VX; ++t) {
+            u32x4v q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              q[i] = pk_bf16(v[i], v[i + 4]);
+              v[i] -= lo_f(q[i]);
+              v[i + 4] -= hi_f(q[i]);
+            }
+            s = mfma32(k[ks], q, s);
+          }
+        }
+      }
+      float z = a.lse[(size_t)(s0 + col) * a.heads + hd];
+      int vis = live ? sees(r) : 0;
+      if (z == kNegInf) vis = 0, z = 0.f;
+      z *= 1.4426950408889634f;
+      if (__ballot(t0 + 32 > vis)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -z));
+          sum[i] += t0 + 8 * (i >> 2) + 4 * h + (i & 3) < vis ? e : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] += __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -z));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float r = sum[i];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) r += __shfl_xor(r, off);
+      if (m == i) red[wave][8 * (i >> 2) + 4 * h + (i & 3)] = r;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32 && t0 + (int)threadIdx.x < len) {
+      float r = 0.f;
+#pragma unroll
+      for (int w = 0; w < kChunkWaves; ++w) r += red[w][threadIdx.x];
+      const size_t at = ((size_t)seq * a.v.hk + head) * cap + t0 + threadIdx.x;
+      a.acc_out[at] = fmaf(a.acc[at], a.decay, r);
+    }
+    __syncthreads();
+  }
+}
+
 // ---------------------------------------------------------------- host side
 
 constexpr int kChunkMin = 64;  // more rows of a sequence than this go to k_attn_chunk
@@ -1173,12 +1303,22 @@ rfpx_status rfpx_attn_weights(const rfpx_kv_cache *c, const rfpx_kv_batch *b, co
   a.decay = decay;
   const long long cap = (long long)b->pages_per_seq * c->page_tokens;
   const long long len = b->max_len < cap ? b->max_len : cap;
-  long long gy = (len + kTile * kWaves - 1) / (kTile * kWaves);
+  const bool chunk = (long long)b->max_cols * a.group > kChunkMin;
+  const int per = chunk ? 64 : kTile * kWaves;  // tokens of a workgroup
+  long long gy = (len + per - 1) / per;
   if (gy < 1) gy = 1;
   if (gy > 65535) gy = 65535;
   const dim3 grid(c->n_kv_heads, (unsigned)gy, b->n_seqs);
   hipStream_t s = (hipStream_t)stream;
   const bool f = xtype == RFPX_X_F32;
+  if (chunk) {
+    void (*k)(WeightArgs) =
+        c->head_dim == 64    ? (f ? k_attn_weights_chunk<2, 3> : k_attn_weights_chunk<2, 1>)
+        : c->head_dim == 128 ? (f ? k_attn_weights_chunk<4, 3> : k_attn_weights_chunk<4, 1>)
+                             : (f ? k_attn_weights_chunk<8, 3> : k_attn_weights_chunk<8, 1>);
+    const hipError_t e = launch_k(k, grid, dim3(64 * kChunkWaves), 0, s, a);
+    return e == hipSuccess ? RFPX_OK : fail(RFPX_E_HIP, "%s: %s", fn, hipGetErrorString(e));
+  }
   void (*k)(WeightArgs) =
       c->head_dim == 64    ? (f ? k_attn_weights<2, 3> : k_attn_weights<2, 1>)
       : c->head_dim == 128 ? (f ? k_attn_weights<4, 3> : k_attn_weights<4, 1>)

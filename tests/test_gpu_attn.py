@@ -544,7 +544,8 @@ def test_cache_past_32_bits():
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("lens,cols,hk,group,d,page", [
     ([1], [1], 1, 1, 64, 32), ([700, 5, 129], [8, 5, 3], 2, 4, 128, 64), ([90], [5], 1, 16, 256, 32),
-    ([200, 40], [130, 40], 2, 3, 128, 128), ([0, 3, 64], [2, 5, 1], 2, 2, 64, 32)])
+    ([200, 40], [130, 40], 2, 3, 128, 128), ([0, 3, 64], [2, 5, 1], 2, 2, 64, 32),
+    ([500, 70, 0, 65], [17, 70, 9, 33], 2, 4, 128, 32), ([330], [66], 1, 5, 64, 256), ([150], [150], 1, 2, 256, 64)])
 def test_weights(lens, cols, hk, group, d, page, dtype):
     t = torch()
     c = Case(lens, cols, hk, d, page, dt(dtype), seed=3)
