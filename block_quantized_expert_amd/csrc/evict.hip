@@ -6,10 +6,10 @@
 // no slot is both read and written, so that all moves run at once, in place.
 //
 // Two launches.  k_evict_select, a workgroup for each (sequence, kv head):
-// every slot's worth becomes one whole number (32 bits, larger is better), a
-// radix selection finds the number of the keep-th best (eight bits a pass,
+// every slot's worth becomes one whole number (32 bits, larger is better;
+// in registers up to 32768 slots), a radix selection finds the number of the keep-th best (eight bits a pass,
 // a histogram in LDS), and one ordered pass over the slots lists the slots
-// that go and the slots that move.  k_evict_move: a wave a move.
+// that go and the slots that move.  k_evict_move: sixteen lanes a move.
 #include "rfpx_attn.hpp"
 
 namespace rfpx {
@@ -54,8 +54,16 @@ __device__ __forceinline__ int wave_offset(int mine, int *sh, int wave, int lane
   return before;
 }
 
+// Copies of the histogram, by lane: numbers of one sequence share their upper
+// bits, and additions to one address wait for each other.
+constexpr int kHist = 4;
+
+// One workgroup's slots: KPT to a thread in registers (KPT > 0), wave w
+// holding a run of 64 KPT of them, slot i * 64 + lane of the run as number i;
+// or (KPT = 0) as numbers in the workspace, runs of any length.
+template <int KPT>
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
-  __shared__ int hist[256];
+  __shared__ int hist[256 * kHist];
   __shared__ int sh[kSelWaves];
   __shared__ int pick[2];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -67,11 +75,30 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
   uint32_t *worth = a.worth + bh * cap;
   const int len = kv_len(a.v, seq), keep = a.keep;
   const int stay = min(len, keep);
-  if (acc != a.acc_out + bh * cap)
-    for (int j = threadIdx.x; j < stay; j += kSelThreads) a.acc_out[bh * cap + j] = acc[j];
-  if (pos != a.pos_out + bh * cap)
-    for (int j = threadIdx.x; j < stay; j += kSelThreads) a.pos_out[bh * cap + j] = pos[j];
+  const bool copy_acc = a.acc != a.acc_out, copy_pos = a.pos != a.pos_out;
+  const int run = KPT ? 64 * KPT : ((len + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
+  const int j_first = min(len, wave * run), j_last = min(len, j_first + run);
+  uint32_t w[KPT ? KPT : 1];
+  // f(slot of this lane, its place in w) for every group of the wave's run;
+  // slots at or behind j_last are the lanes' own to leave out
+  const auto each = [&](auto &&f) {
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int i = 0; i < KPT; ++i)
+        if (j_first + 64 * i < j_last) f(j_first + 64 * i + lane, i);
+    } else {
+      for (int j0 = j_first; j0 < j_last; j0 += 64) f(j0 + lane, 0);
+    }
+  };
+  const auto number = [&](int j, int i) {
+    if constexpr (KPT > 0) return w[i];
+    else return j < j_last ? worth[j] : 0u;
+  };
   if (len <= keep) {
+    each([&](int j, int) {
+      if (j < stay && copy_acc) a.acc_out[bh * cap + j] = acc[j];
+      if (j < stay && copy_pos) a.pos_out[bh * cap + j] = pos[j];
+    });
     if (threadIdx.x == 0) {
       a.head[2 * bh] = 0;
       a.head[2 * bh + 1] = len;
@@ -79,46 +106,73 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
     return;
   }
   int newest = INT32_MIN;
-  for (int j = threadIdx.x; j < len; j += kSelThreads) newest = max(newest, pos[j]);
+  if constexpr (KPT > 0) {
+    // all loads in flight at once
+    float x[KPT];
+    int p[KPT];
 #pragma unroll
-  for (int off = 32; off; off >>= 1) newest = max(newest, __shfl_xor(newest, off));
-  if (lane == 0) sh[wave] = newest;
-  __syncthreads();
-  newest = sh[0];
+    for (int i = 0; i < KPT; ++i) {
+      const int j = min(j_first + 64 * i + lane, len - 1);
+      x[i] = acc[j];
+      p[i] = pos[j];
+    }
 #pragma unroll
-  for (int w = 1; w < kSelWaves; ++w) newest = max(newest, sh[w]);
-  const long long edge = (long long)newest - a.recent;
-  for (int j = threadIdx.x; j < len; j += kSelThreads) worth[j] = worth_of(acc[j], pos[j], edge);
+    for (int i = 0; i < KPT; ++i) newest = max(newest, p[i]);
+    each([&](int j, int i) {
+      if (j < stay && copy_acc) a.acc_out[bh * cap + j] = x[i];
+      if (j < stay && copy_pos) a.pos_out[bh * cap + j] = p[i];
+    });
+#pragma unroll
+    for (int off = 32; off; off >>= 1) newest = max(newest, __shfl_xor(newest, off));
+    if (lane == 0) sh[wave] = newest;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kSelWaves; ++v) newest = max(newest, sh[v]);
+    const long long edge = (long long)newest - a.recent;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) w[i] = worth_of(x[i], p[i], edge);
+  } else {
+    each([&](int j, int) {
+      if (j >= j_last) return;
+      newest = max(newest, pos[j]);
+      if (j < stay && copy_acc) a.acc_out[bh * cap + j] = acc[j];
+      if (j < stay && copy_pos) a.pos_out[bh * cap + j] = pos[j];
+    });
+#pragma unroll
+    for (int off = 32; off; off >>= 1) newest = max(newest, __shfl_xor(newest, off));
+    if (lane == 0) sh[wave] = newest;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kSelWaves; ++v) newest = max(newest, sh[v]);
+    const long long edge = (long long)newest - a.recent;
+    // (a lane reads back later what it wrote itself)
+    each([&](int j, int) {
+      if (j < j_last) worth[j] = worth_of(acc[j], pos[j], edge);
+    });
+  }
 
   // the keep-th largest number: `want` counts down to its rank among the
-  // numbers that share the bits found so far.  (A thread reads back what it
-  // wrote itself: the same stride in every pass.)
+  // numbers that share the bits found so far
   uint32_t found = 0;
   int want = keep;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < 256 * kHist; i += kSelThreads) hist[i] = 0;
     __syncthreads();
     const uint32_t above = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int j0 = 0; j0 < len; j0 += kSelThreads) {
-      const int j = j0 + threadIdx.x;
-      const uint32_t w = j < len ? worth[j] : 0;
-      const bool in = j < len && (w & above) == found;
-      const int bin = (int)((w >> shift) & 255u);
-      // numbers of one bin count as one addition where the wave agrees
-      const uint64_t who = __ballot(in);
-      if (who) {
-        const int first = __shfl(bin, __ffsll((unsigned long long)who) - 1);
-        const uint64_t same = __ballot(in && bin == first);
-        if (lane == 0) atomicAdd(&hist[first], __popcll(same));
-        if (in && bin != first) atomicAdd(&hist[bin], 1);
-      }
-    }
+    each([&](int j, int i) {
+      const uint32_t v = number(j, i);
+      if (j < j_last && (v & above) == found)
+        atomicAdd(&hist[(v >> shift & 255u) * kHist + (lane & (kHist - 1))], 1);
+    });
     __syncthreads();
     if (wave == 0) {
       // bins from the top: lane l holds bins 255 - 4l .. 252 - 4l
       int c[4], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += c[i] = hist[255 - 4 * lane - i];
+      for (int i = 0; i < 4; ++i) {
+        const int4 v = *reinterpret_cast<const int4 *>(&hist[(255 - 4 * lane - i) * kHist]);
+        sum += c[i] = v.x + v.y + v.z + v.w;
+      }
       int upto = sum;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -140,28 +194,23 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
     __syncthreads();
     found |= (uint32_t)pick[0] << shift;
     want = pick[1];
-    __syncthreads();
   }
 
   // slots worth more than `found` stay, and of those worth as much the first
-  // `want`.  Every wave takes a run of slots.
-  __syncthreads();
-  const int run = ((len + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
-  const int j_first = min(len, wave * run), j_last = min(len, j_first + run);
+  // `want`
   int equal = 0;
-  for (int j0 = j_first; j0 < j_last; j0 += 64)
-    equal += __popcll(__ballot(j0 + lane < j_last && worth[j0 + lane] == found));
+  each([&](int j, int i) { equal += __popcll(__ballot(j < j_last && number(j, i) == found)); });
   int total;
   const int equal_before = wave_offset(equal, sh, wave, lane, &total);
   const uint64_t below = (1ull << lane) - 1;
   int n_hole = 0, n_late = 0, at_hole = 0, at_late = 0;
+#pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     int eq = equal_before, holes = 0, late = 0;
-    for (int j0 = j_first; j0 < j_last; j0 += 64) {
-      const int j = j0 + lane;
-      const uint32_t w = j < j_last ? worth[j] : 0;
-      const uint64_t ties = __ballot(j < j_last && w == found);
-      const bool stays = w > found || (w == found && eq + __popcll(ties & below) < want);
+    each([&](int j, int i) {
+      const uint32_t v = number(j, i);
+      const uint64_t ties = __ballot(j < j_last && v == found);
+      const bool stays = v > found || (v == found && eq + __popcll(ties & below) < want);
       const uint64_t h = __ballot(j < j_last && !stays && j < keep);
       const uint64_t l = __ballot(j < j_last && stays && j >= keep);
       if (pass) {
@@ -173,7 +222,7 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
       eq += __popcll(ties);
       holes += __popcll(h);
       late += __popcll(l);
-    }
+    });
     if (!pass) {
       at_hole = wave_offset(holes, sh, wave, lane, &n_hole);
       at_late = wave_offset(late, sh, wave, lane, &n_late);
@@ -185,8 +234,13 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
   }
 }
 
+// Sixteen lanes a move: lane r moves NB bytes of the key's codes and byte r of
+// every block of the value's, two and two as they lie, the first four also
+// the scales, the weight and the position.
+template <int NB>
 __global__ __launch_bounds__(kMoveThreads) void k_evict_move(EvictArgs a) {
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  typedef uint16_t half_t;
+  const int r = threadIdx.x & 15;
   const int hd = blockIdx.y, seq = blockIdx.z;
   const size_t bh = (size_t)seq * a.v.hk + hd;
   const KvGeo &g = a.v.g;
@@ -194,31 +248,28 @@ __global__ __launch_bounds__(kMoveThreads) void k_evict_move(EvictArgs a) {
   if (blockIdx.x == 0 && hd == 0 && threadIdx.x == 0)
     a.lens_out[seq] = min(a.head[2 * bh + 1], a.keep);
   const size_t cap = kv_capacity(a.v);
-  const int kd = g.head_dim / 8, vh = g.head_dim / 4;  // key dwords, value half-words
-  const int items = kd + vh + 2 * g.nb + 2;
-  for (int i = blockIdx.x * (kMoveThreads / 64) + wave; i < moves;
-       i += gridDim.x * (kMoveThreads / 64)) {
-    const int dst = uniform(a.holes[bh * a.list + i]), src = uniform(a.late[bh * a.list + i]);
+  for (int i = blockIdx.x * (kMoveThreads / 16) + (threadIdx.x >> 4); i < moves;
+       i += gridDim.x * (kMoveThreads / 16)) {
+    const int dst = a.holes[bh * a.list + i], src = a.late[bh * a.list + i];
     const uint8_t *from = kv_slab(a.v, seq, src, hd);
     uint8_t *to = kv_slab(a.v, seq, dst, hd);
+    if (r == 2) a.acc_out[bh * cap + dst] = a.acc[bh * cap + src];
+    if (r == 3) a.pos_out[bh * cap + dst] = a.pos[bh * cap + src];
+    if (!from || !to) continue;
     const int ts = src & (g.page_tokens - 1), td = dst & (g.page_tokens - 1);
-    for (int it = lane; it < items; it += 64) {
-      if (it >= items - 2) {
-        if (it == items - 2) a.acc_out[bh * cap + dst] = a.acc[bh * cap + src];
-        else a.pos_out[bh * cap + dst] = a.pos[bh * cap + src];
-      } else if (!from || !to) {
-      } else if (it < kd) {
-        *reinterpret_cast<uint32_t *>(to + g.kc + td * (g.head_dim / 2) + 4 * it) =
-            *reinterpret_cast<const uint32_t *>(from + g.kc + ts * (g.head_dim / 2) + 4 * it);
-      } else if (it < kd + vh) {
-        const int r = (it - kd) / (g.nb / 2), b = 2 * ((it - kd) % (g.nb / 2));
-        *reinterpret_cast<uint16_t *>(to + g.vc + v_byte(g.nb, td, b, r)) =
-            *reinterpret_cast<const uint16_t *>(from + g.vc + v_byte(g.nb, ts, b, r));
-      } else {
-        const int j = it - kd - vh;
-        const int plane = j < g.nb ? g.ks : g.vs, b = j < g.nb ? j : j - g.nb;
-        to[plane + td * g.nb + b] = from[plane + ts * g.nb + b];
-      }
+    half_t k[NB / 2], v[NB / 2], e[NB / 2];
+    const int plane = r == 0 ? g.ks : g.vs;
+#pragma unroll
+    for (int j = 0; j < NB / 2; ++j) {
+      k[j] = reinterpret_cast<const half_t *>(from + g.kc + ts * (16 * NB) + r * NB)[j];
+      v[j] = *reinterpret_cast<const half_t *>(from + g.vc + v_byte(NB, ts, 2 * j, r));
+      if (r < 2) e[j] = reinterpret_cast<const half_t *>(from + plane + ts * NB)[j];
+    }
+#pragma unroll
+    for (int j = 0; j < NB / 2; ++j) {
+      reinterpret_cast<half_t *>(to + g.kc + td * (16 * NB) + r * NB)[j] = k[j];
+      *reinterpret_cast<half_t *>(to + g.vc + v_byte(NB, td, 2 * j, r)) = v[j];
+      if (r < 2) reinterpret_cast<half_t *>(to + plane + td * NB)[j] = e[j];
     }
   }
 }
@@ -294,14 +345,21 @@ rfpx_status rfpx_kv_evict(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int ke
   a.recent = recent;
   a.list = p.list;
   hipStream_t s = (hipStream_t)stream;
-  hipError_t e = launch_k(k_evict_select, dim3(c->n_kv_heads, b->n_seqs), dim3(kSelThreads), 0, s, a);
+  // numbers in registers where the table's slots allow it
+  const long long cap = (long long)b->pages_per_seq * c->page_tokens;
+  void (*select)(EvictArgs) = cap <= 8 * kSelThreads    ? k_evict_select<8>
+                              : cap <= 32 * kSelThreads ? k_evict_select<32>
+                                                        : k_evict_select<0>;
+  hipError_t e = launch_k(select, dim3(c->n_kv_heads, b->n_seqs), dim3(kSelThreads), 0, s, a);
   if (e == hipSuccess) {
-    // a wave a move, at most sixteen workgroups for each compute unit
+    // sixteen moves a workgroup, at most sixteen workgroups a compute unit
     const long long bh = (long long)b->n_seqs * c->n_kv_heads;
-    long long gx = (p.list + 3) / 4, most = (4096 + bh - 1) / bh;
+    long long gx = (p.list + 15) / 16, most = (4096 + bh - 1) / bh;
     if (gx > most) gx = most;
-    e = launch_k(k_evict_move, dim3((unsigned)gx, c->n_kv_heads, b->n_seqs), dim3(kMoveThreads), 0,
-                 s, a);
+    void (*move)(EvictArgs) = c->head_dim == 64    ? k_evict_move<2>
+                              : c->head_dim == 128 ? k_evict_move<4>
+                                                   : k_evict_move<8>;
+    e = launch_k(move, dim3((unsigned)gx, c->n_kv_heads, b->n_seqs), dim3(kMoveThreads), 0, s, a);
   }
   return e == hipSuccess ? RFPX_OK : fail(RFPX_E_HIP, "%s: %s", fn, hipGetErrorString(e));
 }

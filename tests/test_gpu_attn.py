@@ -598,7 +598,8 @@ def evict_plain(lens, keep, recent, acc, pos, tokens):
     ([100, 64, 65, 3], 64, 16, 2, 128, 32, "spread"), ([1000], 1, 0, 3, 64, 64, "spread"),
     ([700, 10], 333, 400, 1, 256, 128, "spread"), ([513, 400], 200, 50, 2, 128, 256, "ties"),
     ([300], 299, 0, 2, 64, 32, "nan"), ([5000, 4000], 1500, 100, 2, 64, 64, "ties"),
-    ([129], 40, 129, 1, 64, 32, "spread"), ([40, 0], 100, 5, 2, 64, 32, "spread"), ([64], 20, 3, 2, 64, 32, "negative")])
+    ([129], 40, 129, 1, 64, 32, "spread"), ([40, 0], 100, 5, 2, 64, 32, "spread"), ([64], 20, 3, 2, 64, 32, "negative"),
+    ([33000, 9000], 20000, 700, 1, 64, 256, "ties"), ([9000], 8500, 10, 2, 128, 128, "spread")])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_evict(lens, keep, recent, hk, d, page, kind, in_place):
     t = torch()
