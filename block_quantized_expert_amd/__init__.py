@@ -503,14 +503,25 @@ def rfpx_dense_forward(m: DenseMatrix, x, y=None, ws=None, stream=None):
 # All tensors of a call live on the current device.
 
 def _rows(what: str, t):
-    """(pointer, row stride, xtype) of a tensor of rows."""
+    """(pointer, row stride) of a tensor of rows."""
     if t.dim() != 3:
         raise ValueError(f"{what} must be [rows][heads][head_dim]")
     n, h, d = t.shape
-    s = t.stride()
-    if s[2] != 1 or (h > 1 and s[1] != d):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and h > 1):
         raise ValueError(f"{what}: heads and values must be adjacent")
-    return t.data_ptr(), (s[0] if n > 1 else h * d), _xtype(t)
+    return t.data_ptr(), (s0 if n > 1 else h * d)
+
+
+def _one_out(what, t, out, dtype, stream):
+    """out, or a new tensor of t's shape and that dtype."""
+    if out is None:
+        out = t.new_empty(t.shape, dtype=dtype)
+        if stream is not None:
+            _used_on(out, stream)
+    elif out.shape != t.shape or out.dtype != dtype:
+        raise ValueError(f"{what}_out must be a {dtype} tensor of {what}'s shape")
+    return out
 
 
 def _same_device(torch, *ts):
@@ -535,11 +546,13 @@ def _flat(what: str, t, dtype, shape):
     return t.data_ptr()
 
 
-def _scratch(n: int, device, stream):
-    """n bytes that live until the work on `stream` is done with them."""
+def _scratch(n: int, like, stream):
+    """n bytes beside a tensor that live until the work on `stream` is done
+    with them."""
     import torch
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _used_on(ws, stream)
+    ws = like.new_empty(n, dtype=torch.uint8)
+    if stream is not None:
+        _used_on(ws, stream)
     return ws
 
 
@@ -563,6 +576,7 @@ class Rope:
             raise ValueError(f"inv_freq must hold {half} numbers")
         self._freq = (C.c_double * max(1, half))(*[float(f) for f in inv_freq])
         self.c = RopeC(dim, style, C.cast(self._freq, C.c_void_p))
+        self.ref = C.byref(self.c)
         self.dim, self.style = dim, style
 
 
@@ -627,35 +641,27 @@ def rfpx_qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, eps: float 
     if x is None:
         raise ValueError("q or k is needed")
     n, _, d = x.shape
-    dev = _same_device(torch, q, k, positions, q_weight, k_weight, q_out, k_out)
-    pos = _flat("positions", positions, torch.int32, (n,))
-    qw = _flat("q_weight", q_weight, torch.float32, (d,))
-    kw = _flat("k_weight", k_weight, torch.float32, (d,))
-    given = next((o for o in (q_out, k_out) if o is not None), None)
-    dtype = out_dtype or (given.dtype if given is not None else x.dtype)
-    outs, args = [], []
-    for what, t, o in (("q", q, q_out), ("k", k, k_out)):
-        if t is None:
-            outs.append(None)
-            args.append((None, 0, 0, None, 0))
-            continue
-        if t.shape[0] != n or t.shape[2] != d or t.dtype != x.dtype:
+    dtype = out_dtype
+    if dtype is None:
+        given = q_out if q_out is not None else k_out
+        dtype = x.dtype if given is None else given.dtype
+    qp = qs = qh = qo = qos = kp = ks = kh = ko = kos = 0
+    if q is not None:
+        q_out = _one_out("q", q, q_out, dtype, stream)
+        (qp, qs), (qo, qos), qh = _rows("q", q), _rows("q_out", q_out), q.shape[1]
+    if k is not None:
+        if k is not x and (k.shape[0] != n or k.shape[2] != d or k.dtype != x.dtype):
             raise ValueError("q and k must agree in rows, head_dim and dtype")
-        if o is None:
-            o = torch.empty(t.shape, dtype=dtype, device=t.device)
-            _used_on(o, stream)
-        elif o.shape != t.shape or o.dtype != dtype:
-            raise ValueError(f"{what}_out must be a {dtype} tensor of {what}'s shape")
-        p, s, _ = _rows(what, t)
-        po, so, otype = _rows(what + "_out", o)
-        outs.append(o)
-        args.append((p, s, t.shape[1], po, so))
-    (qp, qs, qh, qo, qos), (kp, ks, kh, ko, kos) = args
+        k_out = _one_out("k", k, k_out, dtype, stream)
+        (kp, ks), (ko, kos), kh = _rows("k", k), _rows("k_out", k_out), k.shape[1]
+    dev = _same_device(torch, q, k, positions, q_weight, k_weight, q_out, k_out)
     _check("rfpx_qk_norm_rope", lib().rfpx_qk_norm_rope(
-        qp, qs, qh, kp, ks, kh, d, _xtype(x), n, pos, qw, kw, eps,
-        C.byref(rope.c) if rope is not None else None, qo, qos, ko, kos, otype,
-        _raw_stream(torch, dev, stream)))
-    return outs[0], outs[1]
+        qp, qs, qh, kp, ks, kh, d, _xtype(x), n, _flat("positions", positions, torch.int32, (n,)),
+        _flat("q_weight", q_weight, torch.float32, (d,)),
+        _flat("k_weight", k_weight, torch.float32, (d,)), eps,
+        None if rope is None else rope.ref, qo, qos, ko, kos,
+        _xtype(k_out if q is None else q_out), _raw_stream(torch, dev, stream)))
+    return (None if q is None else q_out), (None if k is None else k_out)
 
 
 def rfpx_kv_append(cache: KvCache, batch: KvBatch, k, v, positions=None, pos=None, acc=None,
@@ -667,11 +673,11 @@ def rfpx_kv_append(cache: KvCache, batch: KvBatch, k, v, positions=None, pos=Non
     shape = (k.shape[0], cache.n_kv_heads, cache.head_dim)
     if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != v.dtype:
         raise ValueError(f"k and v must be {shape} tensors of one dtype")
-    kp, ks, xt = _rows("k", k)
-    vp, vs, _ = _rows("v", v)
+    kp, ks = _rows("k", k)
+    vp, vs = _rows("v", v)
     slots = _slots(cache, batch)
     _check("rfpx_kv_append", lib().rfpx_kv_append(
-        cache.ref, batch.ref, kp, ks, vp, vs, xt, k.shape[0],
+        cache.ref, batch.ref, kp, ks, vp, vs, _xtype(k), k.shape[0],
         _flat("positions", positions, torch.int32, (k.shape[0],)),
         _flat("pos", pos, torch.int32, slots), _flat("acc", acc, torch.float32, slots),
         _raw_stream(torch, dev, stream)))
@@ -682,13 +688,14 @@ def rfpx_kv_unpack(cache: KvCache, batch: KvBatch, rows: int, k=None, v=None, st
     [head_dim], fp32 unless bf16 tensors are given."""
     import torch
     shape = (rows, cache.n_kv_heads, cache.head_dim)
-    out = []
-    for t in (k, v):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.float32, device=cache.pool.device)
-            _used_on(t, stream)
-        out.append(t)
-    k, v = out
+    if k is None:
+        k = cache.pool.new_empty(shape, dtype=torch.float32)
+        if stream is not None:
+            _used_on(k, stream)
+    if v is None:
+        v = cache.pool.new_empty(shape, dtype=k.dtype)
+        if stream is not None:
+            _used_on(v, stream)
     dev = _same_device(torch, cache.pool, batch.lens, k, v)
     _check("rfpx_kv_unpack", lib().rfpx_kv_unpack(
         cache.ref, batch.ref, rows, _flat("k", k, k.dtype, shape), _flat("v", v, k.dtype, shape),
@@ -710,20 +717,21 @@ def rfpx_attn_forward(cache: KvCache, batch: KvBatch, q, scale: Optional[float] 
         raise ValueError(f"q must be [rows][heads][{cache.head_dim}]")
     rows, heads, d = q.shape
     if out is None:
-        out = torch.empty((rows, heads, d), dtype=q.dtype, device=q.device)
-        _used_on(out, stream)
+        out = q.new_empty(q.shape)
+        if stream is not None:
+            _used_on(out, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
         n = rfpx_attn_workspace_bytes(cache, batch, heads, rows)
         if n == 0:
             raise RfpxError("rfpx_attn_workspace_bytes", -2, lib().rfpx_last_error().decode())
-        ws = _scratch(n, q.device, stream)
+        ws = _scratch(n, q, stream)
     dev = _same_device(torch, cache.pool, batch.lens, q, out, lse, ws)
-    qp, qs, xt = _rows("q", q)
-    op, os_, _ = _rows("out", out)
+    qp, qs = _rows("q", q)
+    op, os_ = _rows("out", out)
     _check("rfpx_attn_forward", lib().rfpx_attn_forward(
-        cache.ref, batch.ref, qp, qs, xt, heads, rows,
+        cache.ref, batch.ref, qp, qs, _xtype(q), heads, rows,
         d ** -0.5 if scale is None else scale, op, os_,
         _flat("lse", lse, torch.float32, (rows, heads)), ws.data_ptr(),
         ws.numel() * ws.element_size(), _raw_stream(torch, dev, stream)))
@@ -743,9 +751,9 @@ def rfpx_attn_weights(cache: KvCache, batch: KvBatch, q, lse, acc, decay: float 
         acc_out = acc
     dev = _same_device(torch, cache.pool, batch.lens, q, lse, acc, acc_out)
     slots = _slots(cache, batch)
-    qp, qs, xt = _rows("q", q)
+    qp, qs = _rows("q", q)
     _check("rfpx_attn_weights", lib().rfpx_attn_weights(
-        cache.ref, batch.ref, qp, qs, xt, heads, rows, d ** -0.5 if scale is None else scale,
+        cache.ref, batch.ref, qp, qs, _xtype(q), heads, rows, d ** -0.5 if scale is None else scale,
         _flat("lse", lse, torch.float32, (rows, heads)), decay,
         _flat("acc", acc, torch.float32, slots), _flat("acc_out", acc_out, torch.float32, slots),
         _raw_stream(torch, dev, stream)))
@@ -769,7 +777,7 @@ def rfpx_kv_evict(cache: KvCache, batch: KvBatch, keep: int, recent: int, acc, p
         n = rfpx_kv_evict_workspace_bytes(cache, batch, keep)
         if n == 0:
             raise RfpxError("rfpx_kv_evict_workspace_bytes", -2, lib().rfpx_last_error().decode())
-        ws = _scratch(n, cache.pool.device, stream)
+        ws = _scratch(n, cache.pool, stream)
     dev = _same_device(torch, cache.pool, batch.lens, acc, pos, acc_out, pos_out, lens_out, ws)
     slots = _slots(cache, batch)
     _check("rfpx_kv_evict", lib().rfpx_kv_evict(

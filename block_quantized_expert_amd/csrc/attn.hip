@@ -1183,6 +1183,7 @@ AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, in
   p.part = 0;
   p.ml = align_up(p.splits > 1 ? rh * p.splits * c->head_dim * 4 : 0, 256);
   p.total = p.ml + align_up(p.splits > 1 ? rh * p.splits * 16 : 0, 256);
+  if (p.total < 256) p.total = 256;  // a supported shape never reads as "unsupported"
   return p;
 }
 
@@ -1230,8 +1231,7 @@ size_t rfpx_attn_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b,
   if (check_kv(fn, c, b, false) || check_heads(fn, c, n_heads, n_rows, RFPX_X_F32, 1.f)) return 0;
   const size_t f = attn_plan(c, b, n_heads, n_rows, RFPX_X_F32).total;
   const size_t h = attn_plan(c, b, n_heads, n_rows, RFPX_X_BF16).total;
-  const size_t n = f > h ? f : h;
-  return n > 256 ? n : 256;  // a supported shape never reads as "unsupported"
+  return f > h ? f : h;
 }
 
 rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,
