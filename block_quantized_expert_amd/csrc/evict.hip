@@ -32,39 +32,33 @@ struct EvictArgs {
   int keep, recent, list;
 };
 
-__device__ __forceinline__ uint32_t worth_of(float acc, int pos, long long edge) {
-  if (pos > edge) return 0xFFFFFFFFu;
-  if (acc != acc) return 0u;
+__device__ __forceinline__ uint32_t worth_of(float acc, int pos, int edge, bool all_safe) {
   const uint32_t u = __float_as_uint(acc + 0.0f);  // -0 counts as 0
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// Sum over the waves before this one, and over all, of a wave's count.
-__device__ __forceinline__ int wave_offset(int mine, int *sh, int wave, int lane, int *total) {
-  __syncthreads();
-  if (lane == 0) sh[wave] = mine;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kSelWaves; ++w) {
-    before += w < wave ? sh[w] : 0;
-    all += sh[w];
-  }
-  *total = all;
-  return before;
+  const uint32_t w = acc != acc ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
+  return pos > edge || all_safe ? 0xFFFFFFFFu : w;
 }
 
 // Copies of the histogram, by lane: numbers of one sequence share their upper
 // bits, and additions to one address wait for each other.
 constexpr int kHist = 4;
 
-// One workgroup's slots: KPT to a thread in registers (KPT > 0), wave w
-// holding a run of 64 KPT of them, slot i * 64 + lane of the run as number i;
-// or (KPT = 0) as numbers in the workspace, runs of any length.
+// Lanes before this one in a mask.
+__device__ __forceinline__ int rank_in(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Wave w of the workgroup takes a run of slots (a multiple of 64, the same for
+// every wave), 64 at a time; its numbers lie in registers (KPT > 0: at most
+// 64 KPT of them) or in the workspace (KPT = 0), where a lane reads back what
+// it wrote itself.  Slots behind the sequence count as numbers 0: level with
+// the least at most, and behind it in order, so that they are never among the
+// keep best of more than keep slots.  What bounds the kernel is the number of
+// instructions of its one workgroup, and the fetching of them.
 template <int KPT>
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
-  __shared__ int hist[256 * kHist];
-  __shared__ int sh[kSelWaves];
+  __shared__ __align__(16) int hist[256 * kHist];
+  __shared__ __align__(16) int sh[kSelWaves][4];
   __shared__ int pick[2];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int hd = blockIdx.x, seq = blockIdx.y;
@@ -73,83 +67,72 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
   const float *acc = a.acc + bh * cap;
   const int32_t *pos = a.pos + bh * cap;
   uint32_t *worth = a.worth + bh * cap;
-  const int len = kv_len(a.v, seq), keep = a.keep;
+  const int len = uniform(kv_len(a.v, seq)), keep = a.keep;
   const int stay = min(len, keep);
   const bool copy_acc = a.acc != a.acc_out, copy_pos = a.pos != a.pos_out;
-  const int run = KPT ? 64 * KPT : ((len + kSelWaves - 1) / kSelWaves + 63) / 64 * 64;
-  const int j_first = min(len, wave * run), j_last = min(len, j_first + run);
+  const int groups = ((len + kSelWaves - 1) / kSelWaves + 63) / 64;  // of a wave's run
+  const int j_first = wave * groups * 64;
   uint32_t w[KPT ? KPT : 1];
-  // f(slot of this lane, its place in w) for every group of the wave's run;
-  // slots at or behind j_last are the lanes' own to leave out
+  // f(first slot, place in w) for every group of the wave's run
   const auto each = [&](auto &&f) {
     if constexpr (KPT > 0) {
 #pragma unroll
       for (int i = 0; i < KPT; ++i)
-        if (j_first + 64 * i < j_last) f(j_first + 64 * i + lane, i);
+        if (i < groups) f(j_first + 64 * i, i);
     } else {
-      for (int j0 = j_first; j0 < j_last; j0 += 64) f(j0 + lane, 0);
+      for (int i = 0; i < groups; ++i) f(j_first + 64 * i, 0);
     }
   };
-  const auto number = [&](int j, int i) {
+  const auto number = [&](int j0, int i) -> uint32_t {
     if constexpr (KPT > 0) return w[i];
-    else return j < j_last ? worth[j] : 0u;
+    else return j0 + lane < len ? worth[j0 + lane] : 0u;
   };
-  if (len <= keep) {
-    each([&](int j, int) {
-      if (j < stay && copy_acc) a.acc_out[bh * cap + j] = acc[j];
-      if (j < stay && copy_pos) a.pos_out[bh * cap + j] = pos[j];
+  int newest = INT32_MIN;
+  float x[KPT ? KPT : 1];
+  int p[KPT ? KPT : 1];
+  if constexpr (KPT > 0) {
+    // all loads in flight at once
+    each([&](int j0, int i) {
+      const int at = min(j0 + lane, len - 1);
+      x[i] = acc[at];
+      p[i] = pos[at];
     });
+    each([&](int j0, int i) {
+      newest = max(newest, p[i]);
+      if (j0 < stay) {
+        if (copy_acc && j0 + lane < stay) a.acc_out[bh * cap + j0 + lane] = x[i];
+        if (copy_pos && j0 + lane < stay) a.pos_out[bh * cap + j0 + lane] = p[i];
+      }
+    });
+  } else {
+    each([&](int j0, int) {
+      const int j = j0 + lane;
+      if (j < len) newest = max(newest, pos[j]);
+      if (copy_acc && j < stay) a.acc_out[bh * cap + j] = acc[j];
+      if (copy_pos && j < stay) a.pos_out[bh * cap + j] = pos[j];
+    });
+  }
+  if (len <= keep) {
     if (threadIdx.x == 0) {
       a.head[2 * bh] = 0;
       a.head[2 * bh + 1] = len;
     }
     return;
   }
-  int newest = INT32_MIN;
-  if constexpr (KPT > 0) {
-    // all loads in flight at once
-    float x[KPT];
-    int p[KPT];
 #pragma unroll
-    for (int i = 0; i < KPT; ++i) {
-      const int j = min(j_first + 64 * i + lane, len - 1);
-      x[i] = acc[j];
-      p[i] = pos[j];
-    }
+  for (int off = 32; off; off >>= 1) newest = max(newest, __shfl_xor(newest, off));
+  if (lane == 0) sh[wave][0] = newest;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < KPT; ++i) newest = max(newest, p[i]);
-    each([&](int j, int i) {
-      if (j < stay && copy_acc) a.acc_out[bh * cap + j] = x[i];
-      if (j < stay && copy_pos) a.pos_out[bh * cap + j] = p[i];
-    });
-#pragma unroll
-    for (int off = 32; off; off >>= 1) newest = max(newest, __shfl_xor(newest, off));
-    if (lane == 0) sh[wave] = newest;
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < kSelWaves; ++v) newest = max(newest, sh[v]);
-    const long long edge = (long long)newest - a.recent;
-#pragma unroll
-    for (int i = 0; i < KPT; ++i) w[i] = worth_of(x[i], p[i], edge);
-  } else {
-    each([&](int j, int) {
-      if (j >= j_last) return;
-      newest = max(newest, pos[j]);
-      if (j < stay && copy_acc) a.acc_out[bh * cap + j] = acc[j];
-      if (j < stay && copy_pos) a.pos_out[bh * cap + j] = pos[j];
-    });
-#pragma unroll
-    for (int off = 32; off; off >>= 1) newest = max(newest, __shfl_xor(newest, off));
-    if (lane == 0) sh[wave] = newest;
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < kSelWaves; ++v) newest = max(newest, sh[v]);
-    const long long edge = (long long)newest - a.recent;
-    // (a lane reads back later what it wrote itself)
-    each([&](int j, int) {
-      if (j < j_last) worth[j] = worth_of(acc[j], pos[j], edge);
-    });
-  }
+  for (int v = 0; v < kSelWaves; ++v) newest = max(newest, sh[v][0]);
+  const long long wide = (long long)newest - a.recent;
+  const int edge = wide < INT32_MIN ? INT32_MIN : (int)wide;
+  const bool all_safe = wide < INT32_MIN;  // then INT32_MIN itself is above the edge
+  each([&](int j0, int i) {
+    const int j = j0 + lane;
+    if constexpr (KPT > 0) w[i] = j < len ? worth_of(x[i], p[i], edge, all_safe) : 0u;
+    else if (j < len) worth[j] = worth_of(acc[j], pos[j], edge, all_safe);
+  });
 
   // the keep-th largest number: `want` counts down to its rank among the
   // numbers that share the bits found so far
@@ -159,9 +142,9 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
     for (int i = threadIdx.x; i < 256 * kHist; i += kSelThreads) hist[i] = 0;
     __syncthreads();
     const uint32_t above = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    each([&](int j, int i) {
-      const uint32_t v = number(j, i);
-      if (j < j_last && (v & above) == found)
+    each([&](int j0, int i) {
+      const uint32_t v = number(j0, i);
+      if ((v & above) == found)
         atomicAdd(&hist[(v >> shift & 255u) * kHist + (lane & (kHist - 1))], 1);
     });
     __syncthreads();
@@ -192,44 +175,94 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
       }
     }
     __syncthreads();
-    found |= (uint32_t)pick[0] << shift;
-    want = pick[1];
+    found |= (uint32_t)uniform(pick[0]) << shift;
+    want = uniform(pick[1]);
   }
 
-  // slots worth more than `found` stay, and of those worth as much the first
-  // `want`
-  int equal = 0;
-  each([&](int j, int i) { equal += __popcll(__ballot(j < j_last && number(j, i) == found)); });
-  int total;
-  const int equal_before = wave_offset(equal, sh, wave, lane, &total);
-  const uint64_t below = (1ull << lane) - 1;
-  int n_hole = 0, n_late = 0, at_hole = 0, at_late = 0;
+  // Slots worth more than `found` stay, and of those worth as much the first
+  // `want`.  Counts of both before the cut (0) and behind it (1):
+  int more0 = 0, more1 = 0, level0 = 0, level1 = 0;
+  each([&](int j0, int i) {
+    const uint32_t v = number(j0, i);
+    if (j0 + 64 <= keep) {
+      more0 += v > found;
+      level0 += v == found;
+    } else if (j0 >= keep) {
+      more1 += v > found;
+      level1 += v == found;
+    } else {
+      const bool first = j0 + lane < keep;
+      more0 += first && v > found;
+      level0 += first && v == found;
+      more1 += !first && v > found;
+      level1 += !first && v == found;
+    }
+  });
+  if constexpr (KPT > 0) {  // a wave has at most 64 KPT of each: two to a word
+    int m = more0 | more1 << 16, l = level0 | level1 << 16;
 #pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    int eq = equal_before, holes = 0, late = 0;
-    each([&](int j, int i) {
-      const uint32_t v = number(j, i);
-      const uint64_t ties = __ballot(j < j_last && v == found);
-      const bool stays = v > found || (v == found && eq + __popcll(ties & below) < want);
-      const uint64_t h = __ballot(j < j_last && !stays && j < keep);
-      const uint64_t l = __ballot(j < j_last && stays && j >= keep);
-      if (pass) {
-        const int hi = at_hole + holes + __popcll(h & below);
-        const int li = at_late + late + __popcll(l & below);
-        if ((h >> lane) & 1 && hi < a.list) a.holes[bh * a.list + hi] = j;
-        if ((l >> lane) & 1 && li < a.list) a.late[bh * a.list + li] = j;
-      }
-      eq += __popcll(ties);
-      holes += __popcll(h);
-      late += __popcll(l);
-    });
-    if (!pass) {
-      at_hole = wave_offset(holes, sh, wave, lane, &n_hole);
-      at_late = wave_offset(late, sh, wave, lane, &n_late);
+    for (int off = 32; off; off >>= 1) {
+      m += __shfl_xor(m, off);
+      l += __shfl_xor(l, off);
+    }
+    more0 = m & 0xFFFF;
+    more1 = m >> 16;
+    level0 = l & 0xFFFF;
+    level1 = l >> 16;
+  } else {
+#pragma unroll
+    for (int off = 32; off; off >>= 1) {
+      more0 += __shfl_xor(more0, off);
+      more1 += __shfl_xor(more1, off);
+      level0 += __shfl_xor(level0, off);
+      level1 += __shfl_xor(level1, off);
     }
   }
+  if (lane == 0) *reinterpret_cast<int4 *>(sh[wave]) = make_int4(more0, more1, level0, level1);
+  __syncthreads();
+  int eq = 0, at_hole = 0, at_late = 0, n_late = 0, eq_all = 0;
+#pragma unroll
+  for (int v = 0; v < kSelWaves; ++v) {
+    if (v == wave) {
+      eq = eq_all;
+      at_late = n_late;
+    }
+    const int4 c = *reinterpret_cast<const int4 *>(sh[v]);
+    const int take0 = min(max(want - eq_all, 0), c.z);
+    const int take1 = min(max(want - eq_all - c.z, 0), c.w);
+    if (v < wave) at_hole += min(max(keep - v * groups * 64, 0), groups * 64) - c.x - take0;
+    n_late += c.y + take1;
+    eq_all += c.z + c.w;
+  }
+  eq = uniform(eq);
+  at_hole = uniform(at_hole);
+  at_late = uniform(at_late);
+  int32_t *holes = a.holes + bh * a.list, *late = a.late + bh * a.list;
+  each([&](int j0, int i) {
+    const uint32_t v = number(j0, i);
+    bool stays = v > found;
+    const uint64_t ties = __ballot(v == found);
+    if (ties) {
+      stays = stays || (v == found && eq + rank_in(ties) < want);
+      eq += __popcll(ties);
+    }
+    const bool first = j0 + lane < keep;
+    const bool goes = first && !stays, moves = !first && stays;
+    if (j0 < keep) {
+      const uint64_t go = __ballot(goes);
+      const int at = at_hole + rank_in(go);
+      if (goes && at < a.list) holes[at] = j0 + lane;
+      at_hole += __popcll(go);
+    }
+    if (j0 + 64 > keep) {
+      const uint64_t mv = __ballot(moves);
+      const int at = at_late + rank_in(mv);
+      if (moves && at < a.list) late[at] = j0 + lane;
+      at_late += __popcll(mv);
+    }
+  });
   if (threadIdx.x == 0) {
-    a.head[2 * bh] = min(min(n_hole, n_late), a.list);
+    a.head[2 * bh] = min(n_late, a.list);
     a.head[2 * bh + 1] = len;
   }
 }
