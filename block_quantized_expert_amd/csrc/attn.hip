@@ -73,7 +73,9 @@ __device__ __forceinline__ float max_across_g(float x) {
 // N dwords from p (aligned to their size, at most 16 bytes a load).
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
-  if constexpr (N == 2) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  } else if constexpr (N == 2) {
     const uint2 v = *reinterpret_cast<const uint2 *>(p);
     w[0] = v.x;
     w[1] = v.y;
@@ -593,110 +595,103 @@ __device__ __forceinline__ floatx16 mfma32(const u32x4v &a, const u32x4v &b, con
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// The bf16 pairs (1, 0) and (0, 1) in vector registers: as literals the
-// compiler takes them for the inline constant 1.0, which the dot instruction
-// reads as a pair of its own.
-struct Pick {
-  uint32_t lo, hi;
+// A block's scale 2^(e-127) and offset -1.46875 * 2^(e-127) (NaN for e = 255).
+struct Unit {
+  float scale, offset;
 };
-__device__ __forceinline__ Pick make_pick() {
-  Pick p;
-  asm("v_mov_b32 %0, 0x3f80" : "=v"(p.lo));
-  asm("v_mov_b32 %0, 0x3f800000" : "=v"(p.hi));
-  return p;
+__device__ __forceinline__ Unit unit_of(uint32_t e) {
+  return {__uint_as_float(e << 23), __uint_as_float(0x803C0000u | e << 23)};
 }
 
-// The pair of values of a pair of code words, less their blocks' offsets
-// (fp32, negative): exact, as bf16.
-__device__ __forceinline__ uint32_t exact_pair(uint32_t w, float neg_lo, float neg_hi, Pick one) {
-  const float lo = dot2(w, one.lo, neg_lo), hi = dot2(w, one.hi, neg_hi);
-  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-}
-// -1.46875 * 2^(e-127); NaN for e = 255.
-__device__ __forceinline__ float neg_offset(uint32_t e) {
-  return __uint_as_float(0x803C0000u | e << 23);
+// The values of a pair of codes, each nibble `at` (0..3) of a half-word of w,
+// as bf16, exactly: the code in the mantissa of the fp16 number 1 + c/16, one
+// mixed-precision fma a value with its block's scale and offset, and the upper
+// halves of the two results.
+__device__ __forceinline__ uint32_t exact_pair(uint32_t w, int at, Unit lo, Unit hi) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  const uint32_t x = at == 0 ? w << 6 : at == 1 ? w << 2 : at == 2 ? w >> 2 : w >> 6;
+  const f16x2 v = __builtin_bit_cast(f16x2, and_or(x, 0x03C003C0u, 0x3C003C00u));
+  const float a = __builtin_fmaf((float)v[0], lo.scale, lo.offset);
+  const float b = __builtin_fmaf((float)v[1], hi.scale, hi.offset);
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
-// A lane's share of 64 tokens: of the keys one token's octet of every block
-// (waves 0..3, 16 tokens each), of the values byte r of every block of four
-// tokens (waves 4..7, 16 tokens each).
+// A lane's share of 64 tokens, of which wave w decodes tokens 8 w .. 8 w + 7:
+// of the keys, half the blocks of one token's octet (lane = token, octet,
+// half); of the values, byte r of every block of a pair of tokens (lane =
+// group of four, r, pair).
 template <int NB>
 struct ChunkRaw {
-  uint32_t c[NB];
-  uint32_t s[NB];  // keys: the token's scales; values: those of the four tokens
+  uint32_t k[NB / 2], v[NB / 2];
+  uint32_t ks;          // the half's scales
+  uint32_t vs[NB / 2];  // the pair's scales
 };
 
 template <int NB>
-__device__ __forceinline__ void chunk_load(const uint8_t *slab, const KvGeo &g, int tp, bool key,
-                                           int lane, ChunkRaw<NB> &r) {
-  if (key) {
-    load_words<NB>(slab + g.kc + tp * (16 * NB) + lane * (4 * NB), r.c);
-    const uint8_t *s = slab + g.ks + (tp + (lane >> 2)) * NB;
-    if constexpr (NB == 2) r.s[0] = *reinterpret_cast<const uint16_t *>(s);
-    else if constexpr (NB == 4) r.s[0] = *reinterpret_cast<const uint32_t *>(s);
-    else load_words<2>(s, r.s);
+__device__ __forceinline__ void chunk_load(const uint8_t *slab, const KvGeo &g, int tp, int lane,
+                                           ChunkRaw<NB> &r) {
+  const uint8_t *k = slab + g.kc + tp * (16 * NB) + lane * (2 * NB);
+  const uint8_t *v = slab + g.vc + tp * (16 * NB) + lane * (2 * NB);
+  const uint8_t *ks = slab + g.ks + (tp + (lane >> 3)) * NB + (lane & 1) * (NB / 2);
+  const uint8_t *vs = slab + g.vs + (tp + 4 * (lane >> 5) + 2 * (lane & 1)) * NB;
+  if constexpr (NB == 2) {
+    r.k[0] = *reinterpret_cast<const uint32_t *>(k);
+    r.v[0] = *reinterpret_cast<const uint32_t *>(v);
+    r.ks = *ks;
+    r.vs[0] = *reinterpret_cast<const uint32_t *>(vs);
   } else {
-    load_words<NB>(slab + g.vc + tp * (16 * NB) + lane * (4 * NB), r.c);
-    load_words<NB>(slab + g.vs + (tp + 4 * (lane >> 4)) * NB, r.s);
+    load_words<NB / 2>(k, r.k);
+    load_words<NB / 2>(v, r.v);
+    if constexpr (NB == 4) r.ks = *reinterpret_cast<const uint16_t *>(ks);
+    else r.ks = *reinterpret_cast<const uint32_t *>(ks);
+    load_words<NB / 2>(vs, r.vs);
   }
 }
 
-// LDS of one decoded tile: keys [32-token half][step of 16 values][h][token]
-// [16 bytes], values [step of 16 tokens][block][h][value][16 bytes].
+// Decoded keys [32-token half][step of 16 values][h][token][16 bytes] and
+// values [step of 16 tokens][block][h][value][16 bytes] of one tile.
 template <int NB>
-struct ChunkTile {
-  u32x4v k[2][2 * NB][2][32];
-  u32x4v v[4][NB][2][32];
+struct ChunkK {
+  u32x4v at[2][2 * NB][2][32];
+};
+template <int NB>
+struct ChunkV {
+  u32x4v at[4][NB][2][32];
 };
 
 template <int NB>
-__device__ __forceinline__ void chunk_decode_k(const ChunkRaw<NB> &r, int w, int lane, Pick one,
-                                               ChunkTile<NB> &t) {
-  const int tok = 16 * w + (lane >> 2), g = lane & 3;
+__device__ __forceinline__ void chunk_decode(const ChunkRaw<NB> &r, int wave, int lane,
+                                             ChunkK<NB> &tk, ChunkV<NB> &tv) {
+  const int tok = 8 * wave + (lane >> 3), g = (lane >> 1) & 3, half = lane & 1;
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const uint32_t e = (r.s[b >> 2] >> (8 * (b & 3))) & 0xFFu;
-    const uint32_t base = e << 7 | e << 23;
-    const float neg = neg_offset(e);
+  for (int i = 0; i < NB / 2; ++i) {
+    const Unit e = unit_of((r.ks >> (8 * i)) & 0xFFu);
     u32x4v o;
-    o[0] = exact_pair(and_or(r.c[b] << 3, kCodeMask, base), neg, neg, one);
-    o[1] = exact_pair(and_or(r.c[b] >> 1, kCodeMask, base), neg, neg, one);
-    o[2] = exact_pair(and_or(r.c[b] >> 5, kCodeMask, base), neg, neg, one);
-    o[3] = exact_pair(and_or(r.c[b] >> 9, kCodeMask, base), neg, neg, one);
-    t.k[tok >> 5][2 * b + (g >> 1)][g & 1][tok & 31] = o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = exact_pair(r.k[i], j, e, e);
+    tk.at[tok >> 5][2 * (half * (NB / 2) + i) + (g >> 1)][g & 1][tok & 31] = o;
   }
-}
-
-template <int NB>
-__device__ __forceinline__ void chunk_decode_v(const ChunkRaw<NB> &r, int w, int lane, Pick one,
-                                               ChunkTile<NB> &t) {
-  const int grp = lane >> 4, m = lane & 15;  // step w, tokens 4 grp .. of its 16
+  const int grp = 2 * wave + (lane >> 5), rr = (lane >> 1) & 15;  // group of four tokens, byte
+  uint32_t *u = reinterpret_cast<uint32_t *>(&tv.at[grp >> 2][0][grp & 1][2 * rr]) +
+                2 * ((grp >> 1) & 1) + half;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    uint32_t even[2], odd[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int a0 = 2 * i * NB + b, a1 = a0 + NB;
-      const uint32_t e0 = (r.s[a0 >> 2] >> (8 * (a0 & 3))) & 0xFFu;
-      const uint32_t e1 = (r.s[a1 >> 2] >> (8 * (a1 & 3))) & 0xFFu;
-      const uint32_t base = e0 << 7 | e1 << 23;
-      const float n0 = neg_offset(e0), n1 = neg_offset(e1);
-      const uint32_t c = r.c[i * (NB / 2) + (b >> 1)];
-      even[i] = exact_pair(and_or(b & 1 ? c >> 5 : c << 3, kCodeMask, base), n0, n1, one);
-      odd[i] = exact_pair(and_or(b & 1 ? c >> 9 : c >> 1, kCodeMask, base), n0, n1, one);
-    }
-    uint2 *u = reinterpret_cast<uint2 *>(&t.v[w][b][grp & 1][2 * m]);
-    u[grp >> 1] = make_uint2(even[0], even[1]);
-    u[2 + (grp >> 1)] = make_uint2(odd[0], odd[1]);
+    const Unit e0 = unit_of((r.vs[b >> 2] >> (8 * (b & 3))) & 0xFFu);
+    const Unit e1 = unit_of((r.vs[(NB + b) >> 2] >> (8 * ((NB + b) & 3))) & 0xFFu);
+    u[b * 256] = exact_pair(r.v[b >> 1], 2 * (b & 1), e0, e1);
+    u[b * 256 + 4] = exact_pair(r.v[b >> 1], 2 * (b & 1) + 1, e0, e1);
   }
 }
 
+// One barrier a tile: while a tile is computed from one pair of buffers, the
+// next is decoded into the other.
 template <int NB>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   constexpr int D = 32 * NB;
   extern __shared__ __align__(16) uint8_t lds[];
-  ChunkTile<NB> *tiles = reinterpret_cast<ChunkTile<NB> *>(lds);                // [2]
-  uint16_t *bad = reinterpret_cast<uint16_t *>(lds + 2 * sizeof(ChunkTile<NB>));  // [2][4][NB]
+  ChunkK<NB> *buf_k = reinterpret_cast<ChunkK<NB> *>(lds);
+  ChunkV<NB> *buf_v = reinterpret_cast<ChunkV<NB> *>(buf_k + 2);
+  uint8_t *bad = reinterpret_cast<uint8_t *>(buf_v + 2);  // [2][NB][8 waves]: a bit a token
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 31, h = lane >> 5;
   const int head = blockIdx.x % a.v.hk, rb0 = blockIdx.x / a.v.hk;
@@ -709,10 +704,6 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   const long long rows = (long long)n * a.group;
   const KvGeo geo = a.v.g;
   const int32_t *table = a.v.table + (size_t)seq * a.v.pages_per_seq;
-  const bool key = wave < 4;
-  const Pick pick = make_pick();
-  const uint32_t ones = one_one_vgpr_pure();
-  const int w4 = wave & 3;
 
   for (long long r0 = (long long)rb0 * kChunkRows; r0 < rows;
        r0 += (long long)a.row_blocks * kChunkRows) {
@@ -720,9 +711,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
       if (r >= rows) r = rows - 1;
       return min(len, max(0, len - n_all + (int)(r / a.group) + 1));
     };
-    const int last_vis = sees(r0 + kChunkRows - 1);
-    const int first_vis = sees(r0), wave_last = sees(r0 + 32 * wave + 31);
-    const bool wave_live = r0 + 32 * wave < rows;
+    const int first_vis = sees(r0), last_vis = sees(r0 + kChunkRows - 1);
     long long r = r0 + 32 * wave + m;
     const bool live = r < rows;
     if (!live) r = rows - 1;
@@ -744,13 +733,16 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     const int all = (last_vis + kChunkTile - 1) / kChunkTile;
     const int per = (all + a.splits - 1) / a.splits;
     const int t_first = min(all, split * per), t_last = min(all, t_first + per);
+    // tiles that this wave's rows see
+    const int wave_vis = r0 + 32 * wave < rows ? sees(r0 + 32 * wave + 31) : 0;
+    const int t_wave = min(t_last, (wave_vis + kChunkTile - 1) / kChunkTile);
 
     floatx16 acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
-    float mx = kNegInf, thr = kNegInf, sum = 0.f, exact = 0.f;
+    float mx = kNegInf, base = 0.f, thr = kNegInf, sum = 0.f;
     uint32_t poison = 0;
 
     // the page of a token (of the table's last token, past its end)
@@ -763,48 +755,83 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
       const int t0 = tile * kChunkTile;
       return t0 + kChunkTile <= first_vis && is_page(page_at(t0)) && is_page(page_at(t0 + 32));
     };
-    // the page of this wave's 16 tokens of a tile
+    // the page of this wave's 8 tokens of a tile (of the last, past its end)
     const auto page_of = [&](int tile) {
-      return page_at(min(tile, t_last - 1) * kChunkTile + 16 * w4);
+      return page_at(min(tile, t_last - 1) * kChunkTile + 8 * wave);
     };
     const auto load = [&](int tile, int page, ChunkRaw<NB> &raw) {
-      const int tp = (min(tile, t_last - 1) * kChunkTile + 16 * w4) & (geo.page_tokens - 1);
-      const bool in = is_page(page);
-      chunk_load<NB>(a.v.pool + ((size_t)(in ? page : 0) * a.v.hk + head) * geo.slab, geo, tp, key,
-                     lane, raw);
+      const int tp = (min(tile, t_last - 1) * kChunkTile + 8 * wave) & (geo.page_tokens - 1);
+      chunk_load<NB>(a.v.pool + ((size_t)(is_page(page) ? page : 0) * a.v.hk + head) * geo.slab,
+                     geo, tp, lane, raw);
     };
-    // Decode the wave's share into `buf`.  Tokens that no row may read lose
-    // their scales; value blocks marked NaN in a tile that some row sees only
-    // a part of become 0 here and a bit in `bad`.
-    const auto decode = [&](int tile, int page, ChunkRaw<NB> &raw, int buf) {
-      const int first = tile * kChunkTile + 16 * w4;
+    // In a tile that some row sees only a part of, tokens that no row may read
+    // lose their scales, and value blocks marked NaN become 0 and a bit in
+    // `bad`, from which each row takes what it sees.
+    const auto screen = [&](int tile, int page, ChunkRaw<NB> &raw, int at) {
+      const int first = tile * kChunkTile + 8 * wave;
       const int lim = is_page(page) ? len : 0;
-      if (key) {
-        if (first + 16 > lim && first + (lane >> 2) >= lim) {
+      if (first + (lane >> 3) >= lim) raw.ks = 0;
 #pragma unroll
-          for (int i = 0; i < (NB + 3) / 4; ++i) raw.s[i] = 0;
+      for (int b = 0; b < NB; ++b) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int by = i * NB + b;
+          const bool out = first + 4 * (lane >> 5) + 2 * (lane & 1) + i >= lim;
+          const bool nan = !out && ((raw.vs[by >> 2] >> (8 * (by & 3))) & 0xFFu) == 255u;
+          if (out || nan) raw.vs[by >> 2] &= ~(0xFFu << (8 * (by & 3)));
+          const uint64_t v = __ballot(nan);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int pr = 0; pr < 2; ++pr)
+              mask |= (uint32_t)((v >> (32 * g + pr)) & 1) << (4 * g + 2 * pr + i);
         }
-        chunk_decode_k<NB>(raw, w4, lane, pick, tiles[buf]);
-      } else {
-        if (!is_whole(tile)) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            uint32_t mask = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = i * NB + b;
-              const bool out = first + 4 * (lane >> 4) + i >= lim;
-              const bool nan = !out && ((raw.s[at >> 2] >> (8 * (at & 3))) & 0xFFu) == 255u;
-              if (out || nan) raw.s[at >> 2] &= ~(0xFFu << (8 * (at & 3)));
-              const uint64_t v = __ballot(nan);
-#pragma unroll
-              for (int g = 0; g < 4; ++g) mask |= (uint32_t)((v >> (16 * g)) & 1) << (4 * g + i);
-            }
-            if (lane == 0) bad[(buf * 4 + w4) * NB + b] = (uint16_t)mask;
-          }
-        }
-        chunk_decode_v<NB>(raw, w4, lane, pick, tiles[buf]);
+        if (lane == 0) bad[(at * NB + b) * kChunkWaves + wave] = (uint8_t)mask;
       }
+    };
+    // scores of one half of a tile
+    const auto scores_of = [&](const ChunkK<NB> &t, int u, floatx16 &o) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 2 * NB; ++ks) o = mfma32(t.at[u][ks][h][m], q[ks], o);
+    };
+    const auto hide = [&](int tile, int u, int at, floatx16 &o) {
+      const int t0 = tile * kChunkTile + 32 * u;
+      const int lim = is_page(page_at(t0)) ? vis : 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (t0 + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) o[i] = kNegInf;
+      const int seen = lim - t0;
+      const uint32_t in = seen <= 0 ? 0u : seen >= 32 ? 0xFFFFFFFFu : (1u << seen) - 1u;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (*reinterpret_cast<const uint32_t *>(&bad[(at * NB + b) * kChunkWaves + 4 * u]) & in)
+          poison |= 1u << b;
+    };
+    const auto top_of = [&](const floatx16 &o) {
+      float t = o[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) t = fmaxf(t, o[i]);
+      return t;
+    };
+    const auto numerators = [&](floatx16 &o, u32x4v (&p)[2]) {
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        o[i] = __builtin_amdgcn_exp2f(fmaf(o[i], a.sc, -base));
+        x += o[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = pk_bf16(o[2 * i], o[2 * i + 1]);
+      sum += x;
+    };
+    const auto add_up = [&](const ChunkV<NB> &t, int u, const u32x4v (&p)[2]) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b] = mfma32(t.at[2 * u + st][b][h][m], p[st], acc[b]);
     };
 
     ChunkRaw<NB> raw;
@@ -812,83 +839,63 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     if (t_first < t_last) {
       page = page_of(t_first);
       load(t_first, page, raw);
-      __syncthreads();
-      decode(t_first, page, raw, 0);
+      if (!is_whole(t_first)) screen(t_first, page, raw, 0);
+      chunk_decode<NB>(raw, wave, lane, buf_k[0], buf_v[0]);
       page = page_of(t_first + 1);
       load(t_first + 1, page, raw);
     }
-    for (int tile = t_first; tile < t_last; ++tile) {
-      const int buf = (tile - t_first) & 1;
-      __syncthreads();
-      if (tile + 1 < t_last) {
-        decode(tile + 1, page, raw, buf ^ 1);
+    // The inner loop keeps the base that numerators are relative to: sums in
+    // floating point have room for scores up to 2^60 above it.  A score beyond
+    // leaves it (so does the first tile), and everything summed up so far is
+    // scaled to a new base before the tile is taken up again.
+    bool again = false;
+    for (int tile = t_first; tile < t_last;) {
+      float top = kNegInf;
+      for (; tile < t_last; ++tile) {
+        const int at = (tile - t_first) & 1;
+        if (!again) {
+          __syncthreads();
+          if (tile + 1 < t_last && !is_whole(tile + 1)) screen(tile + 1, page, raw, at ^ 1);
+        }
+        again = false;
+        if (tile < t_wave) {
+          floatx16 s0, s1;
+          scores_of(buf_k[at], 0, s0);
+          scores_of(buf_k[at], 1, s1);
+          if (!is_whole(tile)) {
+            hide(tile, 0, at, s0);
+            hide(tile, 1, at, s1);
+          }
+          top = fmaxf(top_of(s0), top_of(s1));
+          if (__ballot(top > thr)) break;
+          u32x4v p0[2], p1[2];
+          numerators(s0, p0);
+          add_up(buf_v[at], 0, p0);
+          numerators(s1, p1);
+          add_up(buf_v[at], 1, p1);
+        }
+        // (past the last tile this decodes that one again, into a free buffer)
+        chunk_decode<NB>(raw, wave, lane, buf_k[at ^ 1], buf_v[at ^ 1]);
         page = page_of(tile + 2);
         load(tile + 2, page, raw);
       }
-      const int t0 = tile * kChunkTile;
-      if (!wave_live || t0 >= wave_last) continue;
-      const ChunkTile<NB> &t = tiles[buf];
-      const bool whole = is_whole(tile);
+      if (tile < t_last) {
+        const uint32_t x = __float_as_uint(top);
+        const auto sw = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        top = fmaxf(mx, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * a.sc);
+        base = top == kNegInf ? 0.f : top;
+        const float f = __builtin_amdgcn_exp2f(mx - base);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        floatx16 s;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < 2 * NB; ++ks) s = mfma32(t.k[u][ks][h][m], q[ks], s);
-        if (!whole) {
-          const int lim = is_page(page_at(t0 + 32 * u)) ? vis : 0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (t0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) s[i] = kNegInf;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const uint32_t v = bad[(buf * 4 + 2 * u) * NB + b] |
-                               (uint32_t)bad[(buf * 4 + 2 * u + 1) * NB + b] << 16;
-            const int seen = lim - (t0 + 32 * u);
-            if (seen > 0 && (v & (seen >= 32 ? 0xFFFFFFFFu : (1u << seen) - 1u))) poison |= 1u << b;
-          }
-        }
-        float top = s[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-        if (__ballot(top > thr)) {
-          const uint32_t x = __float_as_uint(top);
-          const auto sw = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-          top = fmaxf(mx, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * a.sc);
-          const float f = __builtin_amdgcn_exp2f(mx - (top == kNegInf ? 0.f : top));
-#pragma unroll
-          for (int b = 0; b < NB; ++b) acc[b] *= f;
-          sum *= f;
-          exact *= f;
-          mx = top;
-          thr = (top + 8.f) / a.sc;
-        }
-        const float base = mx == kNegInf ? 0.f : mx;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -base));
-        if (a.lse) {
-          float x = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x += s[i];
-          exact += x;
-        }
-        u32x4v p[2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[i >> 2][i & 3] = pk_bf16(s[2 * i], s[2 * i + 1]);
-          sum = dot2(p[i >> 2][i & 3], ones, sum);
-        }
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) acc[b] = mfma32(t.v[2 * u + st][b][h][m], p[st], acc[b]);
+        for (int b = 0; b < NB; ++b) acc[b] *= f;
+        sum *= f;
+        mx = top;
+        thr = (top + 60.f) / a.sc;
+        again = true;
       }
     }
     __syncthreads();
 
     sum += __shfl_xor(sum, 32);
-    exact += __shfl_xor(exact, 32);
     poison |= __shfl_xor(poison, 32);
     if (live) {
       const size_t rh = (size_t)(s0 + col) * a.heads + hd;
@@ -913,9 +920,9 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
       if (h == 0) {
         if (a.splits > 1)
           *reinterpret_cast<float4 *>(a.part_ml + 4 * (rh * a.splits + split)) =
-              make_float4(mx, sum, exact, 0.f);
+              make_float4(mx, sum, sum, 0.f);
         else if (a.lse)
-          a.lse[rh] = (mx + log2f(exact)) * 0.69314718055994531f;
+          a.lse[rh] = (mx + log2f(sum)) * 0.69314718055994531f;
       }
     }
   }
@@ -1021,7 +1028,6 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
   const long long rows = n > 0 ? (long long)n * a.group : 0;
   const size_t cap = kv_capacity(a.v);
   const int tiles = (len + 31) / 32;
-  const Pick pick = make_pick();
   const auto sees = [&](long long r) {
     return min(len, max(0, len - n_all + (int)(r / a.group) + 1));
   };
@@ -1043,13 +1049,9 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const int b = ks >> 1;
-      const uint32_t e = (sb[b >> 2] >> (8 * (b & 3))) & 0xFFu, w = c[ks & 1][b];
-      const uint32_t base = e << 7 | e << 23;
-      const float neg = neg_offset(e);
-      k[ks][0] = exact_pair(and_or(w << 3, kCodeMask, base), neg, neg, pick);
-      k[ks][1] = exact_pair(and_or(w >> 1, kCodeMask, base), neg, neg, pick);
-      k[ks][2] = exact_pair(and_or(w >> 5, kCodeMask, base), neg, neg, pick);
-      k[ks][3] = exact_pair(and_or(w >> 9, kCodeMask, base), neg, neg, pick);
+      const Unit e = unit_of((sb[b >> 2] >> (8 * (b & 3))) & 0xFFu);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[ks][j] = exact_pair(c[ks & 1][b], j, e, e);
     }
     float sum[16];
 #pragma unroll
@@ -1150,7 +1152,7 @@ AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, in
   const int group = heads / c->n_kv_heads;
   const long long rows = (long long)(b->max_cols > 1 ? b->max_cols : 1) * group;
   p.rt = rows <= 16 || xtype == RFPX_X_F32 || c->head_dim == 256 ? 1 : 2;
-  p.chunk = rows > kChunkMin && xtype == RFPX_X_BF16;
+  p.chunk = rows > kChunkMin && xtype == RFPX_X_BF16 && c->head_dim <= 128;
   const int block = p.chunk ? kChunkRows : 16 * p.rt;
   long long rb = (rows + block - 1) / block;
   const long long most_rb = (1 << 20) / c->n_kv_heads;  // a workgroup takes several beyond that
@@ -1205,11 +1207,12 @@ hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
   constexpr int W1 = NB == 8 ? kWaves : kWavesOne;  // heads of 256 leave no registers for more
   const bool one = p.waves == kWavesOne;
   void (*k)(AttnArgs) =
-      p.chunk               ? k_attn_chunk<NB>
+      p.chunk               ? k_attn_chunk<NB == 8 ? 4 : NB>
       : a.xtype == RFPX_X_F32 ? (one ? k_attn<NB, 3, 1, W1> : k_attn<NB, 3, 1, kWaves>)
       : p.rt == 1           ? (one ? k_attn<NB, 1, 1, W1> : k_attn<NB, 1, 1, kWaves>)
                             : (one ? k_attn<NB, 1, RT, W1> : k_attn<NB, 1, RT, kWaves>);
-  const size_t lds = p.chunk ? 2 * sizeof(ChunkTile<NB>) + 2 * 4 * NB * 2 : 0;
+  const size_t lds =
+      p.chunk ? 2 * sizeof(ChunkK<NB>) + 2 * sizeof(ChunkV<NB>) + 2 * NB * kChunkWaves : 0;
   const hipError_t e = launch_k(k, grid, block, lds, s, a);
   if (e != hipSuccess || p.splits == 1) return e;
   const long long rh = (long long)a.n_rows * a.heads;
