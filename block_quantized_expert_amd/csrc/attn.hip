@@ -617,8 +617,9 @@ __device__ __forceinline__ uint32_t exact_pair(uint32_t w, int at, Unit lo, Unit
 }
 
 // A lane's share of 64 tokens, of which wave w decodes tokens 8 w .. 8 w + 7:
-// of the keys, half the blocks of one token's octet (lane = token, octet,
-// half); of the values, byte r of every block of a pair of tokens (lane =
+// of the keys, half the blocks of one token's octet (lane = octet, half,
+// token: eight neighbouring lanes write 128 neighbouring bytes of LDS); of the
+// values, byte r of every block of a pair of tokens (lane =
 // group of four, r, pair).
 template <int NB>
 struct ChunkRaw {
@@ -630,9 +631,9 @@ struct ChunkRaw {
 template <int NB>
 __device__ __forceinline__ void chunk_load(const uint8_t *slab, const KvGeo &g, int tp, int lane,
                                            ChunkRaw<NB> &r) {
-  const uint8_t *k = slab + g.kc + tp * (16 * NB) + lane * (2 * NB);
+  const uint8_t *k = slab + g.kc + (tp + (lane & 7)) * (16 * NB) + (lane >> 3) * (2 * NB);
   const uint8_t *v = slab + g.vc + tp * (16 * NB) + lane * (2 * NB);
-  const uint8_t *ks = slab + g.ks + (tp + (lane >> 3)) * NB + (lane & 1) * (NB / 2);
+  const uint8_t *ks = slab + g.ks + (tp + (lane & 7)) * NB + ((lane >> 3) & 1) * (NB / 2);
   const uint8_t *vs = slab + g.vs + (tp + 4 * (lane >> 5) + 2 * (lane & 1)) * NB;
   if constexpr (NB == 2) {
     r.k[0] = *reinterpret_cast<const uint32_t *>(k);
@@ -662,7 +663,7 @@ struct ChunkV {
 template <int NB>
 __device__ __forceinline__ void chunk_decode(const ChunkRaw<NB> &r, int wave, int lane,
                                              ChunkK<NB> &tk, ChunkV<NB> &tv) {
-  const int tok = 8 * wave + (lane >> 3), g = (lane >> 1) & 3, half = lane & 1;
+  const int tok = 8 * wave + (lane & 7), g = lane >> 4, half = (lane >> 3) & 1;
 #pragma unroll
   for (int i = 0; i < NB / 2; ++i) {
     const Unit e = unit_of((r.ks >> (8 * i)) & 0xFFu);
@@ -673,7 +674,7 @@ __device__ __forceinline__ void chunk_decode(const ChunkRaw<NB> &r, int wave, in
   }
   const int grp = 2 * wave + (lane >> 5), rr = (lane >> 1) & 15;  // group of four tokens, byte
   uint32_t *u = reinterpret_cast<uint32_t *>(&tv.at[grp >> 2][0][grp & 1][2 * rr]) +
-                2 * ((grp >> 1) & 1) + half;
+                2 * ((grp >> 1) & 1) + (lane & 1);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const Unit e0 = unit_of((r.vs[b >> 2] >> (8 * (b & 3))) & 0xFFu);
@@ -770,7 +771,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     const auto screen = [&](int tile, int page, ChunkRaw<NB> &raw, int at) {
       const int first = tile * kChunkTile + 8 * wave;
       const int lim = is_page(page) ? len : 0;
-      if (first + (lane >> 3) >= lim) raw.ks = 0;
+      if (first + (lane & 7) >= lim) raw.ks = 0;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint32_t mask = 0;
@@ -844,6 +845,18 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
       page = page_of(t_first + 1);
       load(t_first + 1, page, raw);
     }
+    // Decode the tile behind (past the last, that one again, into a free
+    // buffer), and load the one after it.
+    const auto next = [&](int tile, int at) {
+      chunk_decode<NB>(raw, wave, lane, buf_k[at], buf_v[at]);
+      page = page_of(tile + 2);
+      load(tile + 2, page, raw);
+    };
+    // Of the two waves of a SIMD one decodes before its products and one
+    // after them, so that one's vector work stands beside the other's matrix
+    // work.
+    const bool early = wave >= 4;
+
     // The inner loop keeps the base that numerators are relative to: sums in
     // floating point have room for scores up to 2^60 above it.  A score beyond
     // leaves it (so does the first tile), and everything summed up so far is
@@ -856,6 +869,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
         if (!again) {
           __syncthreads();
           if (tile + 1 < t_last && !is_whole(tile + 1)) screen(tile + 1, page, raw, at ^ 1);
+          if (early) next(tile, at ^ 1);
         }
         again = false;
         if (tile < t_wave) {
@@ -874,10 +888,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
           numerators(s1, p1);
           add_up(buf_v[at], 1, p1);
         }
-        // (past the last tile this decodes that one again, into a free buffer)
-        chunk_decode<NB>(raw, wave, lane, buf_k[at ^ 1], buf_v[at ^ 1]);
-        page = page_of(tile + 2);
-        load(tile + 2, page, raw);
+        if (!early) next(tile, at ^ 1);
       }
       if (tile < t_last) {
         const uint32_t x = __float_as_uint(top);
