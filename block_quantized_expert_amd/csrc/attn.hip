@@ -100,6 +100,11 @@ struct QTile {
   u32x4v w[VX][NB];
   u32x4v off;
 };
+// ... of a tile in LDS, where all waves read it.
+template <int NB, int VX>
+struct QShared {
+  u32x4v at[VX * NB + 1][64];
+};
 
 template <int NB, int VX>
 __device__ __forceinline__ void load_q(const void *q, size_t at, bool live, int g,
@@ -201,6 +206,17 @@ __device__ __forceinline__ void decode_k(const KTile<NB> &k, KWords<NB> &o) {
 }
 
 template <int NB, int VX>
+__device__ __forceinline__ floatx4 scores(const KWords<NB> &k, const QShared<NB, VX> &q, int lane) {
+  floatx4 s = {0.f, 0.f, 0.f, 0.f};
+  s = mfma(k.e, q.at[VX * NB][lane], s);
+#pragma unroll
+  for (int x = 0; x < VX; ++x)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) s = mfma(k.w[b], q.at[x * NB + b][lane], s);
+  return s;
+}
+
+template <int NB, int VX>
 __device__ __forceinline__ floatx4 scores(const KWords<NB> &k, const QTile<NB, VX> &q) {
   floatx4 s = {0.f, 0.f, 0.f, 0.f};
   // the offsets and the leading terms first: the sum is back at its own size
@@ -284,6 +300,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   constexpr int LD = D + 4;
   __shared__ float sh_ml[W][RT * 16][3];
   __shared__ __align__(16) float sh_o[W][16][LD];
+  __shared__ QShared<NB, VX> sh_q[RT];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int head = blockIdx.x % a.v.hk, rb0 = blockIdx.x / a.v.hk;
@@ -298,7 +315,6 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   const int32_t *table = a.v.table + (size_t)seq * a.v.pages_per_seq;
 
   for (long long r0 = (long long)rb0 * (16 * RT); r0 < rows; r0 += (long long)a.row_blocks * (16 * RT)) {
-    QTile<NB, VX> q[RT];
     int vis[RT];
     int first_vis, last_vis;
     {
@@ -316,7 +332,15 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       if (!live) r = rows - 1;
       const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
       vis[t] = min(len, max(0, len - n_all + col + 1));
-      load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q[t]);
+      if (wave == t) {
+        QTile<NB, VX> q;
+        load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q);
+#pragma unroll
+        for (int x = 0; x < VX; ++x)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) sh_q[t].at[x * NB + b][lane] = q.w[x][b];
+        sh_q[t].at[VX * NB][lane] = q.off;
+      }
     }
     const int tiles = (last_vis + kTile - 1) / kTile;
     const int per = (tiles + a.splits - 1) / a.splits;
@@ -337,13 +361,13 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       for (int b = 0; b < NB; ++b) acc[t][b][0] = acc[t][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // a tile's loads are issued while the tile before it is computed, and its
-    // page is looked up one tile before that
+    // a wave's loads run two tiles ahead of what it computes, and the page of a
+    // tile is looked up one tile before that
     struct Raw {
       KTile<NB> k[2];
       VTile<NB> v;
       bool held;
-    } raw;
+    } raw0, raw1;
     const auto page_of = [&](int tile) {
       return scalar_read(table + ((min(tile, t_last - 1) * kTile) >> geo.page_log));
     };
@@ -355,25 +379,26 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       load_k<NB>(slab, geo, tp + 16, lane, r.k[1]);
       load_v<NB>(slab, geo, tp, lane, r.v);
     };
-    int next_page = 0;
-    if (t_first + wave < t_last) {
-      load(t_first + wave, page_of(t_first + wave), raw);
-      next_page = page_of(t_first + wave + W);
+    int tile = t_first + wave, next_page = 0;
+    if (tile < t_last) {
+      load(tile, page_of(tile), raw0);
+      load(tile + W, page_of(tile + W), raw1);
+      next_page = page_of(tile + 2 * W);
     }
-    for (int tile = t_first + wave; tile < t_last; tile += W) {
+    __syncthreads();  // the queries are in LDS
+    const auto step = [&](Raw &raw) {
+      asm volatile("" ::: "memory");  // the queries are read from LDS again, not kept in registers
       const int t0 = tile * kTile;
       KTile<NB> k[2] = {raw.k[0], raw.k[1]};
       VTile<NB> v = raw.v;
       const bool held = raw.held;
-      load(tile + W, next_page, raw);
-      next_page = page_of(tile + 2 * W);
       floatx4 s[RT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         KWords<NB> kw;
         decode_k<NB>(k[u], kw);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) s[t][u] = scores<NB, VX>(kw, q[t]);
+        for (int t = 0; t < RT; ++t) s[t][u] = scores<NB, VX>(kw, sh_q[t], lane);
       }
       if (!held || t0 + kTile > first_vis) {
         // some row does not see some token: its score is -inf, and what its
@@ -446,6 +471,14 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
           }
       }
       add_values<NB, RT, VX>(v, p, acc, l);
+      load(tile + 2 * W, next_page, raw);
+      next_page = page_of(tile + 3 * W);
+      tile += W;
+    };
+    while (tile < t_last) {
+      step(raw0);
+      if (tile >= t_last) break;
+      step(raw1);
     }
 
     // join the waves: every one scales its sums to the common maximum
