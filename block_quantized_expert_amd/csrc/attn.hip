@@ -1178,7 +1178,8 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
 
 // ---------------------------------------------------------------- host side
 
-constexpr int kChunkMin = 64;  // more rows of a sequence than this go to k_attn_chunk
+constexpr int kChunkMin = 64;    // rows of a sequence that count as many
+constexpr int kChunkSplit = 16;  // tiles of a split of k_attn_chunk, at least
 
 struct AttnPlan {
   int rt, row_blocks, splits, waves;
@@ -1188,42 +1189,50 @@ struct AttnPlan {
 
 // Rows of a block: 16 where a sequence has no more, or fp32 is computed in
 // three terms; 32 otherwise.  A short sequence is one workgroup's, with no
-// second launch; a longer one is split so that there are about two workgroups
-// a compute unit, each wave with a tile at least.
+// second launch; a longer one is split so that the workgroups fill the chip
+// once (two a compute unit), each wave with a tile at least.
+//
+// Many rows of bf16 go to k_attn_chunk, one workgroup a compute unit, where
+// splits of 16 tiles (1024 tokens) or more give it half the chip: 8 kv heads
+// of 128, rows of a sequence x tokens, k_attn and k_attn_chunk in us: 8192 x
+// 8192 422, 293; 8192 x 2048 95, 82; 512 x 16384 77, 61; and without that
+// 256 x 4096 (two sequences) 36, 43; 256 x 500 16, 30.
 AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, int n_rows,
                    int xtype) {
   AttnPlan p;
   const int group = heads / c->n_kv_heads;
   const long long rows = (long long)(b->max_cols > 1 ? b->max_cols : 1) * group;
-  p.rt = rows <= 16 || xtype == RFPX_X_F32 || c->head_dim == 256 ? 1 : 2;
-  p.chunk = rows > kChunkMin && xtype == RFPX_X_BF16 && c->head_dim <= 128;
-  const int block = p.chunk ? kChunkRows : 16 * p.rt;
-  long long rb = (rows + block - 1) / block;
-  const long long most_rb = (1 << 20) / c->n_kv_heads;  // a workgroup takes several beyond that
-  p.row_blocks = (int)(rb < most_rb ? rb : most_rb);
   const long long cap = (long long)b->pages_per_seq * c->page_tokens;
   const long long len = b->max_len < cap ? b->max_len : cap;
-  const long long wgs = (long long)b->n_seqs * c->n_kv_heads * rb;
-  const long long tiles = (len + kTile - 1) / kTile;
-  if (p.chunk) {
-    p.waves = kChunkWaves;
-    const long long most = (len + 8 * kChunkTile - 1) / (8 * kChunkTile);
-    long long s = (256 + wgs - 1) / wgs;
-    if (s > most) s = most;
-    if (s > 64) s = 64;
-    if (s < 1) s = 1;
-    p.splits = (int)s;
-  } else if (tiles <= 4 * kWavesOne && wgs < 512 && c->head_dim < 256) {
-    p.waves = kWavesOne;
-    p.splits = 1;
-  } else {
-    p.waves = kWaves;
-    const long long most = (tiles + kWaves - 1) / kWaves;
-    long long s = (512 + wgs - 1) / wgs;
-    if (s > most) s = most;
-    if (s > 128) s = 128;
-    if (s < 1) s = 1;
-    p.splits = (int)s;
+  const long long pairs = (long long)b->n_seqs * c->n_kv_heads;
+  const long long most_rb = (1 << 20) / c->n_kv_heads;  // a workgroup takes several beyond that
+  const auto clamp = [](long long v, long long lo, long long hi) {
+    return v > hi ? hi : v < lo ? lo : v;
+  };
+  p.rt = rows <= 16 || xtype == RFPX_X_F32 || c->head_dim == 256 ? 1 : 2;
+  p.chunk = false;
+  if (rows > kChunkMin && xtype == RFPX_X_BF16 && c->head_dim <= 128) {
+    const long long tiles = (len + kChunkTile - 1) / kChunkTile;
+    const long long wgs = pairs * ((rows + kChunkRows - 1) / kChunkRows);
+    const long long s = clamp(clamp(256 / wgs, 1, 64), 1, tiles / kChunkSplit);
+    if (tiles >= kChunkSplit && wgs * s >= 128) {
+      p.chunk = true;
+      p.waves = kChunkWaves;
+      p.splits = (int)s;
+    }
+  }
+  const long long block = p.chunk ? kChunkRows : 16 * p.rt;
+  p.row_blocks = (int)clamp((rows + block - 1) / block, 1, most_rb);
+  if (!p.chunk) {
+    const long long wgs = pairs * p.row_blocks, tiles = (len + kTile - 1) / kTile;
+    if (tiles <= 4 * kWavesOne && wgs < 512 && c->head_dim < 256) {
+      p.waves = kWavesOne;
+      p.splits = 1;
+    } else {
+      p.waves = kWaves;
+      p.splits = (int)clamp(clamp(512 / wgs, 1, 128), 1, (tiles + kWaves - 1) / kWaves);
+      if (p.splits < 1) p.splits = 1;
+    }
   }
   const size_t rh = (size_t)n_rows * heads;
   p.part = 0;

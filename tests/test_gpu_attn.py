@@ -78,10 +78,14 @@ class Case:
         bqe.rfpx_kv_append(self.cache, self.fill, self.k_in, self.v_in)
         self.rows, self.fill_starts = self.starts[-1], fill
 
-    def make(self, lens, starts, cols):
+    def make(self, lens, starts, cols, plan=0):
+        """plan: the length that launches are planned for, if larger."""
         t = torch()
         return bqe.KvBatch(self.table, t.tensor(lens, dtype=t.int32, device="cuda"),
-                           t.tensor(starts, dtype=t.int32, device="cuda"), cols, max(list(lens) + [1]))
+                           t.tensor(starts, dtype=t.int32, device="cuda"), cols, max(list(lens) + [1, plan]))
+
+    def planned(self, plan):
+        return self.make(self.lens, self.starts, max(self.cols), plan)
 
     def values(self):
         """Per sequence: k, v [slots][hk][d] and the units of their blocks."""
@@ -430,6 +434,35 @@ def test_attention(lens, cols, hk, group, d, page, dtype):
     assert t.equal(q, q2) and t.equal(out, out2)
 
 
+# rows of a sequence and planned lengths that take the path of many rows, with
+# and without splits; most splits of the short sequences have nothing to do
+@pytest.mark.parametrize("lens,cols,hk,group,d,page,plan", [
+    ([500, 70, 64], [17, 70, 33], 2, 4, 128, 32, 16384),
+    ([1500, 3, 0, 700], [66, 5, 9, 14], 2, 5, 64, 256, 16384),
+    ([40, 1200], [9, 9], 2, 16, 128, 64, 65536),
+    ([100, 64, 1, 65], [35, 20, 1, 35], 32, 2, 128, 64, 1024),
+    ([130, 64, 257, 65], [70, 64, 3, 35], 32, 1, 64, 32, 1024),
+])
+def test_attention_many_rows(lens, cols, hk, group, d, page, plan):
+    t = torch()
+    c = Case(lens, cols, hk, d, page, t.bfloat16, seed=d, gap=2, capacity=plan)
+    q, out, z, scale = attend(c, hk * group, t.bfloat16, batch=c.planned(plan), gap_rows=3)
+    ref = attend64(c, q, scale)
+    rows = slice(2, c.rows)
+    check_out(out, ref, t.bfloat16, rows)
+    check_lse(z, ref, rows)
+    for part in (slice(0, 2), slice(c.rows, None)):
+        assert bool((out[part] == 7).all()) and bool((z[part] == 7).all())
+    _, out2, _, _ = attend(c, hk * group, t.bfloat16, batch=c.planned(plan), gap_rows=3, lse=False)
+    assert t.equal(out, out2)
+    # scores far apart, and a maximum that comes late
+    c = Case([300, 90], [40, 40], 2, d, page, t.bfloat16, seed=7, capacity=65536, scale=6.0)
+    q, out, z, scale = attend(c, 8, t.bfloat16, batch=c.planned(65536), scale=1.0)
+    ref = attend64(c, q, scale)
+    check_out(out, ref, t.bfloat16, slice(0, c.rows))
+    check_lse(z, ref, slice(0, c.rows))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_attention_rows_that_see_nothing(dtype):
     """No slots at all, fewer slots than columns, no columns, rows outside."""
@@ -445,17 +478,17 @@ def test_attention_rows_that_see_nothing(dtype):
         assert bool((out[part] == 7).all()) and bool((z[part] == 7).all())
 
 
-@pytest.mark.parametrize("n,heads", [(60, 4), (1500, 4), (90, 40), (3000, 40)])
+@pytest.mark.parametrize("n,heads,plan", [(60, 4, 0), (1500, 4, 0), (90, 40, 65536), (3000, 40, 65536)])
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_attention_nan_reaches_those_who_see_it(dtype, n, heads):
+def test_attention_nan_reaches_those_who_see_it(dtype, n, heads, plan):
     t = torch()
-    c = Case([n, 50], [4, 2], 2, 128, 32, dt(dtype))
+    c = Case([n, 50], [4, 2], 2, 128, 32, dt(dtype), capacity=plan)
     bad_k, bad_v = c.k_in[n - 4:n].clone(), c.v_in[n - 4:n].clone()
     bad_v[2, 0, 40] = float("nan")   # column 2's values of head 0, block 1
     bad_k[3, 1, 7] = float("inf")    # column 3's keys of head 1
     k, v = t.cat([bad_k, c.k_in[-2:]]), t.cat([bad_v, c.v_in[-2:]])
     bqe.rfpx_kv_append(c.cache, c.batch, k, v)
-    q, out, z, scale = attend(c, heads, dt(dtype))
+    q, out, z, scale = attend(c, heads, dt(dtype), batch=c.planned(plan))
     g = heads // 2  # query heads of a kv head
     o = out.float().cpu().numpy()
     assert np.isfinite(o[:2]).all() and np.isfinite(o[4:]).all()
@@ -469,14 +502,14 @@ def test_attention_nan_reaches_those_who_see_it(dtype, n, heads):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("heads", [4, 70])
-def test_attention_bad_pages_hold_nothing(dtype, heads):
-    c = Case([200, 40], [2, 3], 2, 128, 32, dt(dtype))
+@pytest.mark.parametrize("heads,plan", [(4, 0), (70, 65536)])
+def test_attention_bad_pages_hold_nothing(dtype, heads, plan):
+    c = Case([200, 40], [2, 3], 2, 128, 32, dt(dtype), capacity=plan)
     ref_vals = c.values()
     c.table[0, 1], c.table[0, 4] = -1, c.cache.n_pages
     c.table[1, :] = 2 ** 31 - 1
     c.values = lambda: ref_vals
-    q, out, z, scale = attend(c, heads, dt(dtype))
+    q, out, z, scale = attend(c, heads, dt(dtype), batch=c.planned(plan))
     ref = attend64(c, q, scale, seen=lambda b, j: b == 0 and j // 32 not in (1, 4))
     check_out(out, ref, dt(dtype), slice(0, c.rows))
     check_lse(z, ref, slice(0, c.rows))
