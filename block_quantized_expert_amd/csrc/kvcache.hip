@@ -101,79 +101,135 @@ struct NormRopeArgs {
   double turns[128];           // inv_freq / 2 pi
 };
 
+// Where a rotation finds a value's mate: in the lane's own eight values
+// (neighbouring pairs), in another lane's register of the same number (halves
+// of a multiple of eight), or anywhere, through LDS.
+enum { kRopeNone, kRopeLane, kRopeShuffle, kRopeLds };
+
 // Workgroup (x, y): rows 4x .. 4x+3, their head rows per * y .. (per a
 // multiple of what a pass takes).  Eight values to a lane, D/8 lanes to a
 // head.  cos and sin of the rows' angles are computed once a workgroup: the
 // angle in turns, its whole turns taken off in 64 bits, the rest (below half
-// a turn) in 32.  A rotation's partner value goes through LDS, so that any
-// even number of values and either pairing takes the same path.
-template <int D>
+// a turn) in 32.  A pass's loads are issued before the pass ahead of it is
+// computed.
+template <int D, int MODE>
 __global__ __launch_bounds__(kThreads) void k_norm_rope(NormRopeArgs a) {
   constexpr int LPH = D / 8, HPP = kThreads / LPH;
-  __shared__ float cs[kRopeRows][128], sn[kRopeRows][128];
-  __shared__ __align__(16) float xn[HPP][D];
+  __shared__ __align__(16) float cs[kRopeRows][128], sn[kRopeRows][128];
+  __shared__ __align__(16) float xn[MODE == kRopeLds ? HPP : 1][D];
   const int row0 = blockIdx.x * kRopeRows;
-  for (int i = threadIdx.x; i < kRopeRows * a.half; i += kThreads) {
-    const int r = i / a.half, j = i - r * a.half;
-    const int row = row0 + r;
-    const double t = row < a.n_rows ? (double)a.positions[row] * a.turns[j] : 0.0;
-    float s, c;
-    sincospif(2.0f * (float)(t - rint(t)), &s, &c);
-    cs[r][j] = c;
-    sn[r][j] = s;
-  }
-  __syncthreads();
   const int slot = threadIdx.x / LPH, l = threadIdx.x % LPH;
   const int heads = a.heads[0] + a.heads[1], rot = 2 * a.half;
   const int first = blockIdx.y * a.per;
   const int last = min(first + a.per, kRopeRows * heads);
-  for (int base = first; base < last; base += HPP) {
-    const int hr = base + slot;
-    const int r = hr / heads, hd = hr - r * heads, row = row0 + r;
-    const bool live = hr < last && row < a.n_rows && a.positions[row] >= 0;
-    const int w = hd >= a.heads[0];
-    const int head = hd - (w ? a.heads[0] : 0);
+  struct Pass {
     float v[8];
-    if (live) {
-      load8(a.x[w], (size_t)row * a.stride[w] + head * D + 8 * l, a.xtype, v);
-      float ss = 0.f;
+    int r, w, head;
+    bool live;
+  };
+  const auto fetch = [&](int hr, Pass &p) {
+    p.r = min(hr / heads, kRopeRows - 1);  // (a lane past the last head row computes nothing)
+    const int hd = hr - p.r * heads, row = row0 + p.r;
+    p.live = hr < last && row < a.n_rows && a.positions[row] >= 0;
+    p.w = hd >= a.heads[0];
+    p.head = hd - (p.w ? a.heads[0] : 0);
+    if (p.live)
+      load8(p.w ? a.x[1] : a.x[0],
+            (size_t)row * (p.w ? a.stride[1] : a.stride[0]) + p.head * D + 8 * l, a.xtype, p.v);
+  };
+  Pass next;
+  fetch(first + slot, next);
+  if (MODE != kRopeNone) {
+    for (int i = threadIdx.x; i < kRopeRows * a.half; i += kThreads) {
+      const int r = i / a.half, j = i - r * a.half;
+      const int row = row0 + r;
+      const double t = row < a.n_rows ? (double)a.positions[row] * a.turns[j] : 0.0;
+      float s, c;
+      sincospif(2.0f * (float)(t - rint(t)), &s, &c);
+      cs[r][j] = c;
+      sn[r][j] = s;
+    }
+    __syncthreads();
+  }
+  for (int base = first; base < last; base += HPP) {
+    Pass p = next;
+    if (base + HPP < last) fetch(base + HPP + slot, next);
+    float *v = p.v;
+    const float *weight = p.w ? a.weight[1] : a.weight[0];
+    float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
 #pragma unroll
-      for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor(ss, off, LPH);
-      if (a.weight[w]) {
-        const float rn = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        const float4 w0 = reinterpret_cast<const float4 *>(a.weight[w])[2 * l];
-        const float4 w1 = reinterpret_cast<const float4 *>(a.weight[w])[2 * l + 1];
-        const float g[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor(ss, off, LPH);
+    if (p.live && weight) {
+      const float rn = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+      const float4 w0 = reinterpret_cast<const float4 *>(weight)[2 * l];
+      const float4 w1 = reinterpret_cast<const float4 *>(weight)[2 * l + 1];
+      const float g[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * rn * g[j];
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * rn * g[j];
+    }
+    if (MODE == kRopeLane) {
+      if (8 * l < rot) {
+        const float4 c4 = *reinterpret_cast<const float4 *>(&cs[p.r][4 * l]);
+        const float4 s4 = *reinterpret_cast<const float4 *>(&sn[p.r][4 * l]);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (8 * l + 2 * j < rot) {
+            const float x = v[2 * j], y = v[2 * j + 1];
+            v[2 * j] = fmaf(-y, s[j], x * c[j]);
+            v[2 * j + 1] = fmaf(x, s[j], y * c[j]);
+          }
       }
-      if (rot) {
+    } else if (MODE == kRopeShuffle) {
+      const int far = a.half / 8;  // lanes to the mate
+      const bool second = l >= far;
+      const int mate = second ? l - far : l + far;
+      const int at = 8 * (second ? l - far : l);  // of the angles
+      float m[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[j] = __shfl(v[j], mate, LPH);
+      if (8 * l < rot) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float c = cs[p.r][at + j], s = sn[p.r][at + j];
+          v[j] = fmaf(second ? m[j] : -m[j], s, v[j] * c);
+        }
+      }
+    } else if (MODE == kRopeLds) {
+      __syncthreads();
+      if (p.live) {
         float4 *d = reinterpret_cast<float4 *>(&xn[slot][8 * l]);
         d[0] = make_float4(v[0], v[1], v[2], v[3]);
         d[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
-    }
-    if (rot) __syncthreads();
-    if (live) {
-      if (rot) {
+      __syncthreads();
+      if (p.live) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int i = 8 * l + j;
-          if (i < rot) {
-            const bool second = a.style == RFPX_ROPE_HALF ? i >= a.half : i & 1;
-            const int p = a.style == RFPX_ROPE_HALF ? (second ? i - a.half : i) : i >> 1;
-            const int mate = a.style == RFPX_ROPE_HALF ? (second ? p : i + a.half) : i ^ 1;
-            const float m = xn[slot][mate], c = cs[r][p], s = sn[r][p];
+          if (i < rot) {  // halves
+            const bool second = i >= a.half;
+            const int q = second ? i - a.half : i;
+            const float m = xn[slot][second ? q : i + a.half], c = cs[p.r][q], s = sn[p.r][q];
             v[j] = second ? fmaf(m, s, v[j] * c) : fmaf(-m, s, v[j] * c);
           }
         }
       }
-      store8(a.out[w], (size_t)row * a.out_stride[w] + head * D + 8 * l, a.otype, v);
     }
-    if (rot) __syncthreads();
+    if (p.live)
+      store8(p.w ? a.out[1] : a.out[0],
+             (size_t)(row0 + p.r) * (p.w ? a.out_stride[1] : a.out_stride[0]) + p.head * D + 8 * l,
+             a.otype, v);
   }
+}
+
+template <int D>
+void (*norm_rope_kernel(int half, int style))(NormRopeArgs) {
+  if (half == 0) return k_norm_rope<D, kRopeNone>;
+  if (style == RFPX_ROPE_PAIRS) return k_norm_rope<D, kRopeLane>;
+  return half % 8 == 0 ? k_norm_rope<D, kRopeShuffle> : k_norm_rope<D, kRopeLds>;
 }
 
 // ----------------------------------------------------- append and unpack
@@ -398,9 +454,10 @@ rfpx_status rfpx_qk_norm_rope(const void *q, long long q_stride, int n_heads, co
   gy = (all + a.per - 1) / a.per;
   hipStream_t s = (hipStream_t)stream;
   const dim3 grid(gx, gy);
-  hipError_t e = head_dim == 64    ? launch_k(k_norm_rope<64>, grid, dim3(kThreads), 0, s, a)
-                 : head_dim == 128 ? launch_k(k_norm_rope<128>, grid, dim3(kThreads), 0, s, a)
-                                   : launch_k(k_norm_rope<256>, grid, dim3(kThreads), 0, s, a);
+  void (*kernel)(NormRopeArgs) = head_dim == 64    ? norm_rope_kernel<64>(a.half, a.style)
+                                 : head_dim == 128 ? norm_rope_kernel<128>(a.half, a.style)
+                                                   : norm_rope_kernel<256>(a.half, a.style);
+  const hipError_t e = launch_k(kernel, grid, dim3(kThreads), 0, s, a);
   return e == hipSuccess ? RFPX_OK : fail(RFPX_E_HIP, "%s: %s", fn, hipGetErrorString(e));
 }
 
