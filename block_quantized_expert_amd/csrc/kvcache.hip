@@ -446,9 +446,9 @@ rfpx_status rfpx_qk_norm_rope(const void *q, long long q_stride, int n_heads, co
   const int gx = (n_rows + kRopeRows - 1) / kRopeRows;
   const int hpp = kThreads / (head_dim / 8), all = kRopeRows * (n_heads + n_kv_heads);
   // few rows: one pass a workgroup, the angles computed again in each; many:
-  // about four workgroups a compute unit
+  // about ten workgroups a compute unit
   int gy = (all + hpp - 1) / hpp;
-  const int most = gx >= 1024 ? 1 : 1024 / gx;
+  const int most = gx >= 2560 ? 1 : 2560 / gx;
   if (gy > most) gy = most;
   a.per = ((all + gy - 1) / gy + hpp - 1) / hpp * hpp;
   gy = (all + a.per - 1) / a.per;
