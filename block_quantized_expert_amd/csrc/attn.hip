@@ -208,24 +208,13 @@ __device__ __forceinline__ void decode_k(const KTile<NB> &k, KWords<NB> &o) {
 template <int NB, int VX>
 __device__ __forceinline__ floatx4 scores(const KWords<NB> &k, const QShared<NB, VX> &q, int lane) {
   floatx4 s = {0.f, 0.f, 0.f, 0.f};
+  // the offsets and the leading terms first: the sum is back at its own size
+  // before the smaller terms come
   s = mfma(k.e, q.at[VX * NB][lane], s);
 #pragma unroll
   for (int x = 0; x < VX; ++x)
 #pragma unroll
     for (int b = 0; b < NB; ++b) s = mfma(k.w[b], q.at[x * NB + b][lane], s);
-  return s;
-}
-
-template <int NB, int VX>
-__device__ __forceinline__ floatx4 scores(const KWords<NB> &k, const QTile<NB, VX> &q) {
-  floatx4 s = {0.f, 0.f, 0.f, 0.f};
-  // the offsets and the leading terms first: the sum is back at its own size
-  // before the smaller terms come
-  s = mfma(k.e, q.off, s);
-#pragma unroll
-  for (int x = 0; x < VX; ++x)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) s = mfma(k.w[b], q.w[x][b], s);
   return s;
 }
 
@@ -984,12 +973,23 @@ struct WeightArgs {
   float sc, decay;
 };
 
-// Workgroup (x, y, z): kv head x, tokens 128 y .. of sequence z, 32 to a
-// wave, whose operands stay in registers while the sequence's rows pass, 16
-// at a time.
+// Sums of eight values over the 16 lanes of a row, all at once: the lanes m
+// with bit 0 clear then hold the total of value ms_index<8>(m).
+__device__ __forceinline__ float row_sums(const float (&v)[8], int lane) {
+  float a[4], b[2], c[1];
+  ms_step<0x140, 3, 8>(v, a, lane);
+  ms_step<0x141, 2, 4>(a, b, lane);
+  ms_step<0x4E, 1, 2>(b, c, lane);
+  return c[0] + dpp_f<0xB1>(c[0]);
+}
+
+// Workgroup (x, y, z): kv head x of sequence z, 32-token tiles shared out over
+// the waves of all y.  The rows' operands stand in LDS, QB tiles of 16 at a
+// time, while the keys pass, the next tile's loads in flight.
 template <int NB, int VX>
 __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
-  constexpr int D = 32 * NB;
+  constexpr int D = 32 * NB, QB = VX == 1 ? 4 : 2;
+  __shared__ QShared<NB, VX> sh_q[QB];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int head = blockIdx.x, seq = blockIdx.z;
@@ -999,54 +999,79 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
   const int n_all = a.v.starts[seq + 1] - s0;
   const int n = s0 < 0 ? 0 : min(a.v.starts[seq + 1], a.n_rows) - s0;
   const long long rows = n > 0 ? (long long)n * a.group : 0;
-  const size_t cap = kv_capacity(a.v);
-  for (int t0 = (blockIdx.y * kWaves + wave) * kTile; t0 < len; t0 += gridDim.y * kWaves * kTile) {
-    const int page = uniform(a.v.table[(size_t)seq * a.v.pages_per_seq + (t0 >> geo.page_log)]);
-    const bool held = (unsigned)page < (unsigned)a.v.n_pages;
-    const uint8_t *slab = a.v.pool + ((size_t)(held ? page : 0) * a.v.hk + head) * geo.slab;
-    const int tp = t0 & (geo.page_tokens - 1);
-    KTile<NB> k[2];
-    load_k<NB>(slab, geo, tp, lane, k[0]);
-    load_k<NB>(slab, geo, tp + 16, lane, k[1]);
-    KWords<NB> kw[2];
-    decode_k<NB>(k[0], kw[0]);
-    decode_k<NB>(k[1], kw[1]);
-    float sum[8];
+  const size_t base = ((size_t)seq * a.v.hk + head) * kv_capacity(a.v);
+  const int32_t *table = a.v.table + (size_t)seq * a.v.pages_per_seq;
+  const int tiles = (len + kTile - 1) / kTile, step = gridDim.y * kWaves;
+  const int first = blockIdx.y * kWaves + wave;
+  const int mine = ms_index<8>(m);  // the value that this lane writes
+  for (long long r0 = 0; r0 == 0 || r0 < rows; r0 += 16 * QB) {
+    float z[QB];
+    int vis[QB];
+    if (r0) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-    // columns that see none of the tile's tokens add nothing
-    const long long c0 = held ? max(0, t0 - (len - n_all)) : n;
-    for (long long r0 = c0 * a.group / 16 * 16; r0 < rows; r0 += 16) {
-      const long long r = r0 + m;
+    for (int t = 0; t < QB; ++t) {
+      const long long r = r0 + 16 * t + m;
       const bool live = r < rows;
       const int col = live ? (int)(r / a.group) : 0;
       const int hd = head * a.group + (live ? (int)(r % a.group) : 0);
-      QTile<NB, VX> q;
-      load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q);
-      float z = live ? a.lse[(size_t)(s0 + col) * a.heads + hd] : 0.f;
-      int vis = live ? min(len, max(0, len - n_all + col + 1)) : 0;
-      if (z == kNegInf) vis = 0, z = 0.f;
-      z *= 1.4426950408889634f;
+      z[t] = live ? a.lse[(size_t)(s0 + col) * a.heads + hd] : 0.f;
+      vis[t] = live ? min(len, max(0, len - n_all + col + 1)) : 0;
+      if (z[t] == kNegInf) vis[t] = 0, z[t] = 0.f;
+      z[t] *= 1.4426950408889634f;
+      if (wave == t && r0 + 16 * t < rows) {
+        QTile<NB, VX> q;
+        load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const floatx4 s = scores<NB, VX>(kw[u], q);
+        for (int x = 0; x < VX; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -z));
-          sum[4 * u + i] += t0 + 16 * u + 4 * g + i < vis ? e : 0.f;
-        }
+          for (int b = 0; b < NB; ++b) sh_q[t].at[x * NB + b][lane] = q.w[x][b];
+        sh_q[t].at[VX * NB][lane] = q.off;
       }
     }
+    const int live_tiles = (int)min((long long)QB, (rows - r0 + 15) / 16);
+    KTile<NB> next[2];
+    bool next_held = false;
+    const auto load = [&](int tile) {
+      const int t0 = min(tile, tiles - 1) * kTile;
+      const int page = scalar_read(table + (t0 >> geo.page_log));
+      next_held = (unsigned)page < (unsigned)a.v.n_pages;
+      const uint8_t *slab = a.v.pool + ((size_t)(next_held ? page : 0) * a.v.hk + head) * geo.slab;
+      const int tp = t0 & (geo.page_tokens - 1);
+      load_k<NB>(slab, geo, tp, lane, next[0]);
+      load_k<NB>(slab, geo, tp + 16, lane, next[1]);
+    };
+    if (first < tiles) load(first);
+    __syncthreads();
+    for (int tile = first; tile < tiles; tile += step) {
+      const int t0 = tile * kTile;
+      const int slot = t0 + 16 * (mine >> 2) + 4 * g + (mine & 3);
+      const bool writes = !(m & 1) && slot < len;
+      float old = 0.f;
+      if (writes) old = r0 ? a.acc_out[base + slot] : a.acc[base + slot] * a.decay;
+      const bool held = next_held;
+      KWords<NB> kw[2];
+      decode_k<NB>(next[0], kw[0]);
+      decode_k<NB>(next[1], kw[1]);
+      load(tile + step);
+      float sum[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float r = sum[i];
+      for (int i = 0; i < 8; ++i) sum[i] = 0.f;
 #pragma unroll
-      for (int off = 1; off < 16; off <<= 1) r += __shfl_xor(r, off);
-      const int slot = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-      if (m == i && slot < len) {
-        const size_t at = ((size_t)seq * a.v.hk + head) * cap + slot;
-        a.acc_out[at] = fmaf(a.acc[at], a.decay, r);
+      for (int t = 0; t < QB; ++t) {
+        if (held && t < live_tiles) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const floatx4 s = scores<NB, VX>(kw[u], sh_q[t], lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float e = __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -z[t]));
+              sum[4 * u + i] += t0 + 16 * u + 4 * g + i < vis[t] ? e : 0.f;
+            }
+          }
+        }
       }
+      const float r = row_sums(sum, lane);
+      if (writes) a.acc_out[base + slot] = old + r;
     }
   }
 }
@@ -1360,8 +1385,12 @@ rfpx_status rfpx_attn_weights(const rfpx_kv_cache *c, const rfpx_kv_batch *b, co
   const long long cap = (long long)b->pages_per_seq * c->page_tokens;
   const long long len = b->max_len < cap ? b->max_len : cap;
   const bool chunk = (long long)b->max_cols * a.group > kChunkMin;
-  const int per = chunk ? 64 : kTile * kWaves;  // tokens of a workgroup
+  const int per = chunk ? 64 : kTile * kWaves;  // tokens of a workgroup's turn
   long long gy = (len + per - 1) / per;
+  if (!chunk) {  // about four workgroups a compute unit, with several turns each
+    const long long most = 1024 / ((long long)c->n_kv_heads * b->n_seqs);
+    if (gy > most) gy = most;
+  }
   if (gy < 1) gy = 1;
   if (gy > 65535) gy = 65535;
   const dim3 grid(c->n_kv_heads, (unsigned)gy, b->n_seqs);
