@@ -125,8 +125,15 @@ def expert_bytes(lay, e):
 # valid while these are unchanged.
 _DECODE_SOURCES = ("expert.hip", "route.hip", "rfpx_impl.hpp", "rfpx_route.hpp", "abi.hip")
 _PREFILL_SOURCES = ("prefill.hip", "rfpx_impl.hpp", "rfpx_route.hpp", "abi.hip")
+_ATTENTION_SOURCES = ("rfpx_attn.hpp", "rfpx_impl.hpp", "abi.hip")
 KERNEL_SOURCES = {"k_gateup": _DECODE_SOURCES, "k_down": _DECODE_SOURCES,
-                  "k_pf_gateup": _PREFILL_SOURCES, "k_pf_down": _PREFILL_SOURCES}
+                  "k_pf_gateup": _PREFILL_SOURCES, "k_pf_down": _PREFILL_SOURCES,
+                  "k_attn": ("attn.hip", *_ATTENTION_SOURCES),
+                  "k_attn_chunk": ("attn.hip", *_ATTENTION_SOURCES),
+                  "k_attn_weights": ("attn.hip", *_ATTENTION_SOURCES),
+                  "k_norm_rope": ("kvcache.hip", *_ATTENTION_SOURCES),
+                  "k_kv_append": ("kvcache.hip", *_ATTENTION_SOURCES),
+                  "k_evict_select": ("evict.hip", *_ATTENTION_SOURCES)}
 
 
 def kernel_source_hash(kernel: str, root: str = ROOT) -> str:

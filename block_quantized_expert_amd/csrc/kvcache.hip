@@ -16,8 +16,8 @@ rfpx_status check_kv(const char *fn, const rfpx_kv_cache *c, const rfpx_kv_batch
                 c->n_pages, c->page_tokens, RFPX_HEADS_MAX);
   if (b->n_seqs < 1 || b->n_seqs > RFPX_SEQS_MAX)
     return fail(RFPX_E_SHAPE, "%s: n_seqs=%d: must be in [1, %d]", fn, b->n_seqs, RFPX_SEQS_MAX);
-  if (b->pages_per_seq < 1 || (long long)b->pages_per_seq * c->page_tokens > 0x7FFFFF00ll)
-    return fail(RFPX_E_SHAPE, "%s: pages_per_seq=%d: 1 or more, below 2^31 tokens", fn,
+  if (b->pages_per_seq < 1 || (long long)b->pages_per_seq * c->page_tokens > (1 << 30))
+    return fail(RFPX_E_SHAPE, "%s: pages_per_seq=%d: 1 or more, up to 2^30 tokens", fn,
                 b->pages_per_seq);
   if (b->max_cols < 0 || b->max_cols > RFPX_ROWS_MAX)
     return fail(RFPX_E_SHAPE, "%s: max_cols=%d: must be in [0, %d]", fn, b->max_cols,

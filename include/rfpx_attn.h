@@ -71,7 +71,8 @@ typedef struct {
 
 typedef struct {
   int n_seqs;                /* 1..RFPX_SEQS_MAX */
-  int pages_per_seq;         /* row length of page_table, 1 or more */
+  int pages_per_seq;         /* row length of page_table, 1 or more; up to
+                                2^30 tokens of pages */
   int max_cols;              /* most columns of a sequence in this step, 0.. */
   int max_len;               /* largest of lens, 0.. */
   const int32_t *page_table; /* device, [n_seqs][pages_per_seq] */
@@ -143,11 +144,11 @@ size_t rfpx_attn_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b,
  * q and out [n_rows][n_heads][head_dim], fp32 or bf16 per xtype, rows
  * q_stride and out_stride elements apart; lse_dev NULL or fp32 [n_rows]
  * [n_heads].  A column that sees nothing gets out = 0, lse = -inf.  The
- * cache's values enter the products exactly.  bf16 q enters as it is and the
- * softmax's numerators as bf16 (their denominator is the sum of the rounded
- * ones); fp32 q and its numerators enter as three bf16 terms, which lose
- * nothing.  Sums and statistics are fp32, in a fixed order: out is the same
- * bit for bit from run to run.  scale > 0, finite.  out may not overlap q. */
+ * cache's values enter the products exactly.  bf16 q enters as it is, and its
+ * softmax numerators as bf16; fp32 q and its numerators enter as three bf16
+ * terms, which lose nothing.  Sums and statistics are fp32, in a fixed order:
+ * out is the same bit for bit from run to run (of one plan: max_cols and
+ * max_len decide how a sequence is split).  scale > 0, finite.  out may not overlap q. */
 rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q_dev,
                               long long q_stride, int xtype, int n_heads, int n_rows, float scale,
                               void *out_dev, long long out_stride, float *lse_dev, void *ws_dev,

@@ -55,7 +55,7 @@ def batch(**kw):
 BAD_CACHE = [(dict(pool=None), ARG), (dict(pool=P + 128), ALIGN), (dict(pool_bytes=10 * 8 * 64 * 136 - 1), WS),
              (dict(head_dim=80), SHAPE), (dict(page_tokens=512), SHAPE), (dict(n_pages=0), SHAPE)]
 BAD_BATCH = [(dict(n_seqs=0), SHAPE), (dict(n_seqs=65536), SHAPE), (dict(pages_per_seq=0), SHAPE),
-             (dict(pages_per_seq=1 << 30), SHAPE), (dict(max_cols=-1), SHAPE), (dict(max_len=-1), SHAPE),
+             (dict(pages_per_seq=(1 << 24) + 1), SHAPE), (dict(max_cols=-1), SHAPE), (dict(max_len=-1), SHAPE),
              (dict(page_table=None), ARG), (dict(lens=None), ARG), (dict(starts=None), ARG),
              (dict(lens=P + 2), ALIGN)]
 
