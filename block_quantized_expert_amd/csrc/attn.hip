@@ -12,8 +12,8 @@
 //   words, and one of the blocks' 2^(e-127) with -1.46875 times the sums of
 //   q over the blocks (three bf16 terms: 24 bits).
 //   Output:  O^T += V^T P^T, 32 tokens at a time: two products for each
-//   block of 32 values (even and odd ones), and one of -1.46875 * 2^(e-127)
-//   that both take off.  Row sums of P: one product with ones.
+//   block of 32 values (even and odd ones), and products of 2^(e-127) that
+//   take the offsets off.  Row sums of P: one product with ones.
 // Both are transposed, so that lane (m = lane & 15, g = lane >> 4) holds of
 // query row m the scores of tokens 4g .. 4g+3 and 16+4g .. 16+4g+3, which
 // are the eight k-values that the second product takes from that very lane:
@@ -245,9 +245,22 @@ __device__ __forceinline__ uint32_t v_scale(const VTile<NB> &v, int u, int i, in
   return (v.s[u][at >> 2] >> (8 * (at & 3))) & 0xFFu;
 }
 
+// The offsets come off in one of two ways.  With three terms (fp32), in the
+// same sums: a product of -1.46875 * 2^(e-127) for every product of words, so
+// that a sum never grows past its own size.  With one (bf16), in a sum of
+// their own: rows 4 g + i of one product hold sum p 2^(e-127) of block i (mod
+// D/32), taken off the others every 2048 tokens of a wave and at its end; that
+// costs a product a tile and four blocks instead of two a block, and rounding
+// errors below 2^-24 * 24 a step, far under the numerators' own.
+template <int NB, int RT>
+struct Offsets {
+  floatx4 sum[RT][(NB + 3) / 4];
+};
+
 template <int NB, int RT, int VX>
 __device__ __forceinline__ void add_values(const VTile<NB> &v, const u32x4v (&p)[RT][VX],
-                                           floatx4 (&acc)[RT][NB][2], floatx4 (&l)[RT]) {
+                                           floatx4 (&acc)[RT][NB][2], floatx4 (&l)[RT],
+                                           Offsets<NB, RT> &offs, int lane) {
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     u32x4v even, odd, off;
@@ -265,11 +278,29 @@ __device__ __forceinline__ void add_values(const VTile<NB> &v, const u32x4v (&p)
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int x = 0; x < VX; ++x) {
-        acc[t][b][0] = mfma(off, p[t][x], acc[t][b][0]);
-        acc[t][b][1] = mfma(off, p[t][x], acc[t][b][1]);
+        if (VX > 1) {
+          acc[t][b][0] = mfma(off, p[t][x], acc[t][b][0]);
+          acc[t][b][1] = mfma(off, p[t][x], acc[t][b][1]);
+        }
         acc[t][b][0] = mfma(even, p[t][x], acc[t][b][0]);
         acc[t][b][1] = mfma(odd, p[t][x], acc[t][b][1]);
       }
+  }
+  if constexpr (VX == 1) {
+    // row r = lane & 15 takes block r mod 4 (or 2) of every token
+    const int r = lane & (NB == 2 ? 1 : 3);
+    const uint32_t sel = 0x0C000C00u | r | ((NB == 2 ? 2 : 4) + r) << 16;
+#pragma unroll
+    for (int j = 0; j < (NB + 3) / 4; ++j) {
+      u32x4v e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = i >> 1, d0 = NB == 2 ? i & 1 : (2 * (i & 1) * NB) / 4 + j;
+        e[i] = __builtin_amdgcn_perm(v.s[u][NB == 2 ? d0 : d0 + NB / 4], v.s[u][d0], sel) << 7;
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) offs.sum[t][j] = mfma(e, p[t][0], offs.sum[t][j]);
+    }
   }
   const u32x4v ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
@@ -336,6 +367,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
     const int t_first = min(tiles, split * per), t_last = min(tiles, t_first + per);
 
     floatx4 acc[RT][NB][2], l[RT];
+    Offsets<NB, RT> offs;
     // l is the sum of the numerators as they enter the second product, the
     // output's denominator; exact the one before bf16 rounding, for lse
     float mx[RT], thr[RT], exact[RT];
@@ -343,6 +375,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       l[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < (NB + 3) / 4; ++j) offs.sum[t][j] = floatx4{0.f, 0.f, 0.f, 0.f};
       mx[t] = thr[t] = kNegInf;
       exact[t] = 0.f;
       poison[t] = 0;
@@ -375,6 +409,22 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       next_page = page_of(tile + 2 * W);
     }
     __syncthreads();  // the queries are in LDS
+    const auto take_off = [&]() {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float o = -kOffset * offs.sum[t][b >> 2][NB == 2 ? b : b & 3];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[t][b][0][i] += o;
+            acc[t][b][1][i] += o;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < (NB + 3) / 4; ++j) offs.sum[t][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+      }
+    };
     const auto step = [&](Raw &raw) {
       asm volatile("" ::: "memory");  // the queries are read from LDS again, not kept in registers
       const int t0 = tile * kTile;
@@ -433,6 +483,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
             acc[t][b][0] *= f;
             acc[t][b][1] *= f;
           }
+#pragma unroll
+          for (int j = 0; j < (NB + 3) / 4; ++j) offs.sum[t][j] *= f;
           l[t] *= f;
           exact[t] *= f;
           mx[t] = top;
@@ -459,16 +511,18 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
             }
           }
       }
-      add_values<NB, RT, VX>(v, p, acc, l);
+      add_values<NB, RT, VX>(v, p, acc, l, offs, lane);
       load(tile + 2 * W, next_page, raw);
       next_page = page_of(tile + 3 * W);
       tile += W;
     };
-    while (tile < t_last) {
+    for (int turn = 1; tile < t_last; ++turn) {
       step(raw0);
       if (tile >= t_last) break;
       step(raw1);
+      if (VX == 1 && (turn & 31) == 0) take_off();
     }
+    if (VX == 1) take_off();
 
     // join the waves: every one scales its sums to the common maximum
 #pragma unroll
