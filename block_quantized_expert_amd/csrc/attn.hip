@@ -310,6 +310,16 @@ __device__ __forceinline__ void add_values(const VTile<NB> &v, const u32x4v (&p)
 }
 
 // ------------------------------------------------------------------ forward
+//
+// What bounds it: instruction issue, then HBM.  A wave's 32-token tile of a
+// head of 128 is 4352 bytes, about 290 vector instructions (164 of them the
+// two decodes) and, at 32 rows, 40 matrix instructions, and the two kinds
+// overlap little.  Measured on an MI355X: 5 columns of 32 heads over 131071
+// tokens (143 MB) 38 us, 3.7 TB/s, 79% of a plain copy's rate; 64 sequences
+// of up to 4096 tokens 4.0 TB/s; one column over 1021 tokens 11.6 us, a chain
+// of loads.  Tried and not kept: 256, 768, 1024 and 2048 workgroups instead
+// of 512 (8, 12, 25 and 45% slower at 16 ragged sequences; a second round of
+// workgroups costs more than it evens out).
 
 // Workgroup (x, y, z): kv head and row block x, split y, sequence z.  A row
 // block is 16 RT of the sequence's rows (column, head of the group); its W waves
@@ -762,6 +772,13 @@ __device__ __forceinline__ void chunk_decode(const ChunkRaw<NB> &r, int wave, in
 
 // One barrier a tile: while a tile is computed from one pair of buffers, the
 // next is decoded into the other.
+//
+// Measured on an MI355X: 2048 columns of 32 heads of 128 at the end of 8192
+// tokens 275 us, 876 TFLOP/s, 76% of a library's 8192^3 bf16 product (1158);
+// matrix units a third busy, vector units 45%.  Tried and not kept, all
+// within 3%: operands read six products ahead, both halves' score chains in
+// turn, pages read three tiles ahead, rows written through LDS; the scores of
+// a tile beside the exps of the tile before it spills (355 us).
 template <int NB>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   constexpr int D = 32 * NB;
@@ -1039,7 +1056,8 @@ __device__ __forceinline__ float row_sums(const float (&v)[8], int lane) {
 
 // Workgroup (x, y, z): kv head x of sequence z, 32-token tiles shared out over
 // the waves of all y.  The rows' operands stand in LDS, QB tiles of 16 at a
-// time, while the keys pass, the next tile's loads in flight.
+// time, while the keys pass, the next tile's loads in flight.  Measured: 4
+// sequences of up to 16384 tokens, 4 columns of 32 heads, 14.4 us.
 template <int NB, int VX>
 __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
   constexpr int D = 32 * NB, QB = VX == 1 ? 4 : 2;
@@ -1135,7 +1153,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
 // and so every workgroup has about the same to do.  A tile's keys are decoded
 // to exact bf16 operands once, by every wave for itself, and stay in registers
 // while the eight waves share out the rows, 32 at a time, straight from
-// memory; their sums meet in LDS.
+// memory; their sums meet in LDS.  Measured: 2048 columns of 32 heads of 128
+// over their own 2048 tokens 64 us; bound by the loads of the rows from the
+// caches (every workgroup reads all rows that see its tiles).
 template <int NB, int VX>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightArgs a) {
   constexpr int D = 32 * NB, KS = 2 * NB;
@@ -1236,12 +1256,19 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
         for (int i = 0; i < 16; ++i) sum[i] += __builtin_amdgcn_exp2f(fmaf(s[i], a.sc, -z));
       }
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float r = sum[i];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) r += __shfl_xor(r, off);
-      if (m == i) red[wave][8 * (i >> 2) + 4 * h + (i & 3)] = r;
+    {
+      // all sixteen sums over the 32 lanes at once: lane m < 16 has number
+      // ms_index<16>(m)
+      float v8[8], v4[4], v2[2], v1[1];
+      ms_step<0x140, 3, 16>(sum, v8, lane);
+      ms_step<0x141, 2, 8>(v8, v4, lane);
+      ms_step<0x4E, 1, 4>(v4, v2, lane);
+      ms_step<0xB1, 0, 2>(v2, v1, lane);
+      const uint32_t u = __float_as_uint(v1[0]);
+      const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+      const int i = ms_index<16>(m & 15);
+      if (m < 16)
+        red[wave][8 * (i >> 2) + 4 * h + (i & 3)] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
     }
     __syncthreads();
     if (threadIdx.x < 32 && t0 + (int)threadIdx.x < len) {
@@ -1258,6 +1285,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
 // ---------------------------------------------------------------- host side
 
 constexpr int kChunkMin = 64;    // rows of a sequence that count as many
+constexpr int kWeightsMin = 512;  // ... for k_attn_weights_chunk
 constexpr int kChunkSplit = 16;  // tiles of a split of k_attn_chunk, at least
 
 struct AttnPlan {
@@ -1438,7 +1466,11 @@ rfpx_status rfpx_attn_weights(const rfpx_kv_cache *c, const rfpx_kv_batch *b, co
   a.decay = decay;
   const long long cap = (long long)b->pages_per_seq * c->page_tokens;
   const long long len = b->max_len < cap ? b->max_len : cap;
-  const bool chunk = (long long)b->max_cols * a.group > kChunkMin;
+  // Many rows pay for a tile's operands in every wave: k_attn_weights and
+  // k_attn_weights_chunk in us, 8 kv heads of 128, rows x tokens: 80 x 9594
+  // 12, 50; 233 x 9594 26, 63; 512 x 4096 32, 25; 1024 x 4096 61, 40; 4096 x
+  // 2048 233, 64; heads of 64: 512 x 4096 27, 13.
+  const bool chunk = (long long)b->max_cols * a.group >= kWeightsMin;
   const int per = chunk ? 64 : kTile * kWaves;  // tokens of a workgroup's turn
   long long gy = (len + per - 1) / per;
   if (!chunk) {  // about four workgroups a compute unit, with several turns each

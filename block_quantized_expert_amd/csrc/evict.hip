@@ -54,7 +54,10 @@ __device__ __forceinline__ int rank_in(uint64_t mask) {
 // it wrote itself.  Slots behind the sequence count as numbers 0: level with
 // the least at most, and behind it in order, so that they are never among the
 // keep best of more than keep slots.  What bounds the kernel is the number of
-// instructions of its one workgroup, and the fetching of them.
+// instructions of its one workgroup, and the fetching of them: 64 heads of
+// 4224 slots 13.3 us, 8 heads of 32768 slots 35 us (loads a quarter, the four
+// radix passes a quarter, counting and listing the rest).  Numbers in LDS with
+// rolled loops measured 62 us, ballots instead of counts per lane 42 us.
 template <int KPT>
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
   __shared__ __align__(16) int hist[256 * kHist];
@@ -267,7 +270,8 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
   }
 }
 
-// Sixteen lanes a move: lane r moves NB bytes of the key's codes and byte r of
+// Sixteen lanes a move (8 heads cut from 32768 to 8192 slots, some 6100 moves
+// each: 11.5 us; a wave a move 27 us): lane r moves NB bytes of the key's codes and byte r of
 // every block of the value's, two and two as they lie, the first four also
 // the scales, the weight and the position.
 template <int NB>

@@ -111,7 +111,8 @@ enum { kRopeNone, kRopeLane, kRopeShuffle, kRopeLds };
 // head.  cos and sin of the rows' angles are computed once a workgroup: the
 // angle in turns, its whole turns taken off in 64 bits, the rest (below half
 // a turn) in 32.  A pass's loads are issued before the pass ahead of it is
-// computed.
+// computed.  Bound by HBM: 2048 rows of 40 heads of 128 in bf16 (42 MB) 13 us,
+// 3.2 TB/s; five rows 3.9 us, which is a launch and two chains of loads.
 template <int D, int MODE>
 __global__ __launch_bounds__(kThreads) void k_norm_rope(NormRopeArgs a) {
   constexpr int LPH = D / 8, HPP = kThreads / LPH;
@@ -253,7 +254,9 @@ __device__ __forceinline__ int fp4_exponent(float a) {
   return e < 1 ? 1 : e;
 }
 
-// One row a workgroup; eight values to a lane, four lanes to a block.
+// One row a workgroup; eight values to a lane, four lanes to a block.  64-bit
+// arithmetic for the codes costs nothing that shows: 2048 rows of 8 heads of
+// 128 in fp32 (17 MB in, 2.2 MB of blocks out) 8 us; 38 rows 4.1 us.
 __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs a) {
   const KvGeo &g = a.v.g;
   const int row = blockIdx.x, lane = threadIdx.x & 63;

@@ -578,7 +578,9 @@ def test_cache_past_32_bits():
 @pytest.mark.parametrize("lens,cols,hk,group,d,page", [
     ([1], [1], 1, 1, 64, 32), ([700, 5, 129], [8, 5, 3], 2, 4, 128, 64), ([90], [5], 1, 16, 256, 32),
     ([200, 40], [130, 40], 2, 3, 128, 128), ([0, 3, 64], [2, 5, 1], 2, 2, 64, 32),
-    ([500, 70, 0, 65], [17, 70, 9, 33], 2, 4, 128, 32), ([330], [66], 1, 5, 64, 256), ([150], [150], 1, 2, 256, 64)])
+    ([500, 70, 0, 65], [17, 70, 9, 33], 2, 4, 128, 32), ([330], [66], 1, 5, 64, 256), ([150], [150], 1, 2, 256, 64),
+    # rows enough for the path of many
+    ([500, 70, 0, 65, 33], [130, 70, 9, 33, 3], 2, 4, 128, 32), ([97], [90], 1, 6, 64, 64), ([140], [140], 1, 4, 256, 128)])
 def test_weights(lens, cols, hk, group, d, page, dtype):
     t = torch()
     c = Case(lens, cols, hk, d, page, dt(dtype), seed=3)
@@ -835,6 +837,50 @@ def test_captured_steps_follow_device_lengths():
         for name in ("out", "lse"):
             assert t.equal(A[name], B[name]), (i, name)
         assert t.equal(A["acc"][:, :, :n], B["acc"][:, :, :n]) and t.equal(A["pos"][:, :, :n], B["pos"][:, :, :n])
+        _ = (q.float() @ q.float().transpose(1, 2)).sum().item()  # eager work between
+
+
+def test_captured_chunk_follows_device_lengths():
+    """A captured chunk (append, attention of many rows, its weights) replayed
+    with other lengths and fewer columns than it was captured with."""
+    t = torch()
+    hk, g, d, page, cap, rows = 2, 8, 128, 64, 65536, 80
+    c = Case([900, 700], [40, 40], hk, d, page, t.bfloat16, capacity=cap)
+    batch = c.planned(cap)
+    gen = t.Generator(device="cuda").manual_seed(9)
+    q = t.randn((rows, hk * g, d), generator=gen, device="cuda").to(t.bfloat16)
+    k, v = (t.randn((rows, hk, d), generator=gen, device="cuda").to(t.bfloat16) for _ in range(2))
+    out, lse = t.zeros_like(q), t.zeros((rows, hk * g), device="cuda")
+    acc, acc_out = t.zeros((2, hk, c.per * page), device="cuda"), t.zeros((2, hk, c.per * page), device="cuda")
+    ws = t.empty(bqe.rfpx_attn_workspace_bytes(c.cache, batch, hk * g, rows), dtype=t.uint8, device="cuda")
+
+    def step(out, lse, acc_out, ws=None):
+        bqe.rfpx_kv_append(c.cache, batch, k, v)
+        bqe.rfpx_attn_forward(c.cache, batch, q, out=out, lse=lse, ws=ws)
+        bqe.rfpx_attn_weights(c.cache, batch, q, lse, acc, 1.0, acc_out=acc_out)
+
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        step(out, lse, acc_out, ws)
+    t.cuda.current_stream().wait_stream(side)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        step(out, lse, acc_out, ws)
+    for lens, starts in (([900, 700], [0, 40, 80]), ([950, 33], [0, 40, 73]), ([400, 80], [0, 3, 80]),
+                         ([64, 0], [0, 64, 64]), ([900, 700], [0, 40, 80])):
+        batch.lens.copy_(t.tensor(lens, dtype=t.int32))
+        batch.starts.copy_(t.tensor(starts, dtype=t.int32))
+        for x in (out, lse, acc_out):
+            x.fill_(3)
+        graph.replay()
+        o2, z2, a2 = t.full_like(out, 3), t.full_like(lse, 3), t.full_like(acc_out, 3)
+        step(o2, z2, a2)
+        t.cuda.synchronize()
+        # (950 slots reach tokens that were never appended, which read as NaN)
+        for x, y in ((out, o2), (lse, z2), (acc_out, a2)):
+            assert t.allclose(x, y, rtol=0.0, atol=0.0, equal_nan=True), lens
+        assert bool((out[starts[-1]:] == 3).all())
         _ = (q.float() @ q.float().transpose(1, 2)).sum().item()  # eager work between
 
 
