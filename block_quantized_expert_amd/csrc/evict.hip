@@ -271,9 +271,9 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs a) {
 }
 
 // Sixteen lanes a move (8 heads cut from 32768 to 8192 slots, some 6100 moves
-// each: 11.5 us; a wave a move 27 us): lane r moves NB bytes of the key's codes and byte r of
-// every block of the value's, two and two as they lie, the first four also
-// the scales, the weight and the position.
+// each: 11.3 us; a wave a move 27 us): lane r moves NB bytes of the key's
+// codes and byte r of every block of the value's, two and two as they lie,
+// the first four also the scales, the weight and the position.
 template <int NB>
 __global__ __launch_bounds__(kMoveThreads) void k_evict_move(EvictArgs a) {
   typedef uint16_t half_t;
