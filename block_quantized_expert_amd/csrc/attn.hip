@@ -333,7 +333,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   __shared__ QShared<NB, VX> sh_q[RT];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
-  const int head = blockIdx.x % a.v.hk, rb0 = blockIdx.x / a.v.hk;
+  const int head = blockIdx.x % a.v.hk, rb0 = a.row_blocks - 1 - blockIdx.x / a.v.hk;
   const int split = blockIdx.y, seq = blockIdx.z;
   const int s0 = a.v.starts[seq];
   const int n = min(a.v.starts[seq + 1], a.n_rows) - s0;
@@ -831,7 +831,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   uint8_t *bad = reinterpret_cast<uint8_t *>(buf_v + 2);  // [2][NB][8 waves]: a bit a token
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 31, h = lane >> 5;
-  const int head = blockIdx.x % a.v.hk, rb0 = blockIdx.x / a.v.hk;
+  const int head = blockIdx.x % a.v.hk, rb0 = a.row_blocks - 1 - blockIdx.x / a.v.hk;
   const int split = blockIdx.y, seq = blockIdx.z;
   const int s0 = a.v.starts[seq];
   const int n_all = a.v.starts[seq + 1] - s0;
