@@ -1191,6 +1191,12 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
   }
 }
 
+// Between a wave's own stores to LDS and its lanes' reads of each other's.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Many rows.  A workgroup takes two 32-token tiles, one from each end of the
 // sequence, one after the other: rows see early tokens more than late ones,
 // and so every workgroup has about the same to do.  A tile's keys are decoded
@@ -1202,9 +1208,15 @@ __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
 template <int NB, int VX>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightArgs a) {
   constexpr int D = 32 * NB, KS = 2 * NB;
-  __shared__ float red[kChunkWaves][32];
+  constexpr int kBytes = D * (VX == 1 ? 2 : 4);     // of a row
+  constexpr int SEG = kBytes >= 256 ? 16 : 8;       // 16-byte pieces of a row staged at a time
+  constexpr int STEPS = VX == 1 ? SEG / 2 : SEG / 4;  // products of a stage
+  __shared__ __align__(16) u32x4v stage[kChunkWaves][32 * SEG];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 31, h = lane >> 5;
+  u32x4v *const mine = stage[wave];
+  const auto red = [&](int w) { return reinterpret_cast<float *>(stage[w]); };
+  const auto piece = [](int row, int at) { return row * SEG + (at ^ (row & (SEG - 1))); };
   const int head = blockIdx.x, seq = blockIdx.z;
   const int len = kv_len(a.v, seq);
   const KvGeo geo = a.v.g;
@@ -1248,39 +1260,49 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
       const bool live = r0 + m < rows;
       const long long r = live ? r0 + m : rows - 1;
       const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
-      const size_t at = (size_t)(s0 + col) * a.q_stride + (size_t)hd * D + 8 * h;
+      const long long off =
+          ((long long)(s0 + col) * a.q_stride + (long long)hd * D) * (VX == 1 ? 2 : 4);
       floatx16 s;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = 0.f;
-      if constexpr (VX == 1) {
-        uint4 d[KS];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          d[ks] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at + 16 * ks);
+      for (int st = 0; st < kBytes / (16 * SEG); ++st) {
+        u32x4v d[SEG / 2];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const u32x4v q = {__builtin_amdgcn_perm(d[ks].z, d[ks].x, 0x05040100u),
-                            __builtin_amdgcn_perm(d[ks].z, d[ks].x, 0x07060302u),
-                            __builtin_amdgcn_perm(d[ks].w, d[ks].y, 0x05040100u),
-                            __builtin_amdgcn_perm(d[ks].w, d[ks].y, 0x07060302u)};
-          s = mfma32(k[ks], q, s);
+        for (int i = 0; i < SEG / 2; ++i) {
+          const int row = (64 * i + lane) / SEG, at = lane % SEG;
+          d[i] = *reinterpret_cast<const u32x4v *>(static_cast<const uint8_t *>(a.q) +
+                                                  __shfl(off, row) + 16 * (SEG * st + at));
         }
-      } else {
+        wave_fence();  // the stage before has been read
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at + 16 * ks);
-          const float4 x = p[0], y = p[1];
-          float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        for (int i = 0; i < SEG / 2; ++i) mine[piece((64 * i + lane) / SEG, lane % SEG)] = d[i];
+        wave_fence();
 #pragma unroll
-          for (int t = 0; t < VX; ++t) {
-            u32x4v q;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              q[i] = pk_bf16(v[i], v[i + 4]);
-              v[i] -= lo_f(q[i]);
-              v[i + 4] -= hi_f(q[i]);
-            }
+        for (int step = 0; step < STEPS; ++step) {
+          const int ks = st * STEPS + step;
+          if constexpr (VX == 1) {
+            const u32x4v x = mine[piece(m, 2 * step + h)];
+            const u32x4v q = {__builtin_amdgcn_perm(x[2], x[0], 0x05040100u),
+                              __builtin_amdgcn_perm(x[2], x[0], 0x07060302u),
+                              __builtin_amdgcn_perm(x[3], x[1], 0x05040100u),
+                              __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
             s = mfma32(k[ks], q, s);
+          } else {
+            const float4 x = __builtin_bit_cast(float4, mine[piece(m, 4 * step + 2 * h)]);
+            const float4 y = __builtin_bit_cast(float4, mine[piece(m, 4 * step + 2 * h + 1)]);
+            float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int t = 0; t < VX; ++t) {
+              u32x4v q;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                q[i] = pk_bf16(v[i], v[i + 4]);
+                v[i] -= lo_f(q[i]);
+                v[i + 4] -= hi_f(q[i]);
+              }
+              s = mfma32(k[ks], q, s);
+            }
           }
         }
       }
@@ -1311,13 +1333,13 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
       const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
       const int i = ms_index<16>(m & 15);
       if (m < 16)
-        red[wave][8 * (i >> 2) + 4 * h + (i & 3)] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+        red(wave)[8 * (i >> 2) + 4 * h + (i & 3)] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
     }
     __syncthreads();
     if (threadIdx.x < 32 && t0 + (int)threadIdx.x < len) {
       float r = 0.f;
 #pragma unroll
-      for (int w = 0; w < kChunkWaves; ++w) r += red[w][threadIdx.x];
+      for (int w = 0; w < kChunkWaves; ++w) r += red(w)[threadIdx.x];
       const size_t at = ((size_t)seq * a.v.hk + head) * cap + t0 + threadIdx.x;
       a.acc_out[at] = fmaf(a.acc[at], a.decay, r);
     }
