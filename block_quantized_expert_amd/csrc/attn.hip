@@ -1201,16 +1201,22 @@ __device__ __forceinline__ void wave_fence() {
 // sequence, one after the other: rows see early tokens more than late ones,
 // and so every workgroup has about the same to do.  A tile's keys are decoded
 // to exact bf16 operands once, by every wave for itself, and stay in registers
-// while the eight waves share out the rows, 32 at a time, straight from
-// memory; their sums meet in LDS.  Measured: 2048 columns of 32 heads of 128
-// over their own 2048 tokens 65 us; bound by the loads of the rows from the
-// caches (every workgroup reads all rows that see its tiles).
+// while the eight waves share out the rows, 32 at a time.  Every workgroup
+// reads all rows that see its tiles, from the caches: a wave reads them whole,
+// neighbouring lanes a row, and turns them over in its own part of
+// LDS (pieces of 16 bytes, a row's exchanged by its number, so that both sides
+// are free of bank conflicts).  Each lane reading its own row from memory was
+// bound by a cache line a lane: 64 us.  The waves' sums meet in LDS.
+// Measured: 2048 columns of 32 heads of 128 over their own 2048 tokens 48 us.
 template <int NB, int VX>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightArgs a) {
   constexpr int D = 32 * NB, KS = 2 * NB;
   constexpr int kBytes = D * (VX == 1 ? 2 : 4);     // of a row
   constexpr int SEG = kBytes >= 256 ? 16 : 8;       // 16-byte pieces of a row staged at a time
   constexpr int STEPS = VX == 1 ? SEG / 2 : SEG / 4;  // products of a stage
+  // Loads a stage ahead: 4096 rows over 2048 tokens in bf16 48.5 -> 46.5 us,
+  // but fp32 92.7 -> 98.5 us, whose three terms leave fewer registers.
+  constexpr bool kAhead = VX == 1;
   __shared__ __align__(16) u32x4v stage[kChunkWaves][32 * SEG];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 31, h = lane >> 5;
@@ -1226,9 +1232,6 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
   const long long rows = n > 0 ? (long long)n * a.group : 0;
   const size_t cap = kv_capacity(a.v);
   const int tiles = (len + 31) / 32;
-  const auto sees = [&](long long r) {
-    return min(len, max(0, len - n_all + (int)(r / a.group) + 1));
-  };
   for (int turn = 2 * blockIdx.y; turn < tiles;
        turn = turn & 1 ? turn + 2 * (int)gridDim.y - 1 : turn + 1) {
     const int t0 = 32 * (turn & 1 ? tiles - 1 - (turn >> 1) : turn >> 1);
@@ -1256,28 +1259,48 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
     for (int i = 0; i < 16; ++i) sum[i] = 0.f;
     // columns that see none of the tile's tokens add nothing
     const long long first = (long long)max(0, t0 - (len - n_all)) * a.group / 32;
-    for (long long r0 = 32 * (first + wave); held && r0 < rows; r0 += 32 * kChunkWaves) {
-      const bool live = r0 + m < rows;
-      const long long r = live ? r0 + m : rows - 1;
-      const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
-      const long long off =
-          ((long long)(s0 + col) * a.q_stride + (long long)hd * D) * (VX == 1 ? 2 : 4);
+    int col, hd;    // of row r0 + m, or of the last one
+    long long off;  // and where it begins
+    const auto locate = [&](long long r0) {
+      const unsigned r = (unsigned)min(r0 + m, rows - 1);  // rows are 2^30 at most
+      col = (int)(r / (unsigned)a.group);
+      hd = (head - col) * a.group + (int)r;
+      off = ((long long)(s0 + col) * a.q_stride + (long long)hd * D) * (VX == 1 ? 2 : 4);
+    };
+    u32x4v d[SEG / 2];
+    const auto fetch = [&](int st) {
+#pragma unroll
+      for (int i = 0; i < SEG / 2; ++i)
+        d[i] = *reinterpret_cast<const u32x4v *>(static_cast<const uint8_t *>(a.q) +
+                                                __shfl(off, (64 * i + lane) / SEG) +
+                                                16 * (SEG * st + lane % SEG));
+    };
+    long long r0 = 32 * (first + wave);
+    if (kAhead && held && r0 < rows) {
+      locate(r0);
+      fetch(0);
+    }
+    for (; held && r0 < rows; r0 += 32 * kChunkWaves) {
+      if (!kAhead) locate(r0);
+      float z = a.lse[(size_t)(s0 + col) * a.heads + hd];
+      int vis = r0 + m < rows ? min(len, max(0, len - n_all + col + 1)) : 0;
       floatx16 s;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
       for (int st = 0; st < kBytes / (16 * SEG); ++st) {
-        u32x4v d[SEG / 2];
-#pragma unroll
-        for (int i = 0; i < SEG / 2; ++i) {
-          const int row = (64 * i + lane) / SEG, at = lane % SEG;
-          d[i] = *reinterpret_cast<const u32x4v *>(static_cast<const uint8_t *>(a.q) +
-                                                  __shfl(off, row) + 16 * (SEG * st + at));
-        }
+        if (!kAhead) fetch(st);
         wave_fence();  // the stage before has been read
 #pragma unroll
         for (int i = 0; i < SEG / 2; ++i) mine[piece((64 * i + lane) / SEG, lane % SEG)] = d[i];
         wave_fence();
+        // the next piece, or the next rows' first (past the end, the last row's)
+        if (kAhead && st + 1 < kBytes / (16 * SEG)) {
+          fetch(st + 1);
+        } else if (kAhead) {
+          locate(r0 + 32 * kChunkWaves);
+          fetch(0);
+        }
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
           const int ks = st * STEPS + step;
@@ -1306,8 +1329,6 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
           }
         }
       }
-      float z = a.lse[(size_t)(s0 + col) * a.heads + hd];
-      int vis = live ? sees(r) : 0;
       if (z == kNegInf) vis = 0, z = 0.f;
       z *= 1.4426950408889634f;
       if (__ballot(t0 + 32 > vis)) {
