@@ -1371,7 +1371,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
 // ---------------------------------------------------------------- host side
 
 constexpr int kChunkMin = 64;    // rows of a sequence that count as many
-constexpr int kWeightsMin = 512;  // ... for k_attn_weights_chunk
+constexpr int kWeightsMin = 256;  // ... for k_attn_weights_chunk
 constexpr int kChunkSplit = 16;  // tiles of a split of k_attn_chunk, at least
 
 struct AttnPlan {
@@ -1557,11 +1557,16 @@ rfpx_status rfpx_attn_weights(const rfpx_kv_cache *c, const rfpx_kv_batch *b, co
   a.decay = decay;
   const long long cap = (long long)b->pages_per_seq * c->page_tokens;
   const long long len = b->max_len < cap ? b->max_len : cap;
-  // Many rows pay for a tile's operands in every wave: k_attn_weights and
-  // k_attn_weights_chunk in us, 8 kv heads of 128, rows x tokens: 80 x 9594
-  // 12, 50; 233 x 9594 26, 63; 512 x 4096 32, 25; 1024 x 4096 61, 40; 4096 x
-  // 2048 233, 64; heads of 64: 512 x 4096 27, 13.
-  const bool chunk = (long long)b->max_cols * a.group >= kWeightsMin;
+  // k_attn_weights_chunk has every wave decode every tile of its workgroup,
+  // for which many rows pay, the fewer the shorter the sequence: there
+  // k_attn_weights has few tiles a wave.  k_attn_weights and
+  // k_attn_weights_chunk in us, 8 kv heads of 128, bf16, rows x tokens: 80 x
+  // 9594 13, 29; 256 x 4096 17, 16; 256 x 8192 20, 28; 512 x 8192 38, 40; 1024
+  // x 8192 73, 59; 512 x 16384 65, 76; 1024 x 16384 129, 115; 1024 x 32768
+  // 194, 237; of 64: 256 x 8192 16.5, 15.7; 512 x 16384 45, 40; 512 x 32768
+  // 69, 75; 1024 x 32768 134, 115.
+  const long long many = (long long)b->max_cols * a.group;
+  const bool chunk = many >= kWeightsMin && many * (c->head_dim == 64 ? 32 : 16) >= len;
   const int per = chunk ? 64 : kTile * kWaves;  // tokens of a workgroup's turn
   long long gy = (len + per - 1) / per;
   if (!chunk) {  // about four workgroups a compute unit, with several turns each
