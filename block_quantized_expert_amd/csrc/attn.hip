@@ -333,6 +333,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   __shared__ QShared<NB, VX> sh_q[RT];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
+  // The last rows see most: they start first (a chunk over its own 2048 tokens,
+  // fp32: 169 -> 162 us).
   const int head = blockIdx.x % a.v.hk, rb0 = a.row_blocks - 1 - blockIdx.x / a.v.hk;
   const int split = blockIdx.y, seq = blockIdx.z;
   const int s0 = a.v.starts[seq];
@@ -831,6 +833,8 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   uint8_t *bad = reinterpret_cast<uint8_t *>(buf_v + 2);  // [2][NB][8 waves]: a bit a token
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 31, h = lane >> 5;
+  // The last rows see most: they start first (4096 columns over their own
+  // tokens 237 -> 198 us).
   const int head = blockIdx.x % a.v.hk, rb0 = a.row_blocks - 1 - blockIdx.x / a.v.hk;
   const int split = blockIdx.y, seq = blockIdx.z;
   const int s0 = a.v.starts[seq];
@@ -1353,6 +1357,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
       const uint32_t u = __float_as_uint(v1[0]);
       const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
       const int i = ms_index<16>(m & 15);
+      wave_fence();
       if (m < 16)
         red(wave)[8 * (i >> 2) + 4 * h + (i & 3)] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
     }
