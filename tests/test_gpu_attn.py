@@ -516,6 +516,22 @@ def test_attention_bad_pages_hold_nothing(dtype, heads, plan):
     assert bool((out[2:] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,plan", [(64, 1100), (128, 1500), (128, 2048), (256, 300), (256, 1500)])
+def test_attention_splits_without_tokens(d, plan, dtype):
+    """9, 12, 16, 3 and 12 splits, of which the short sequence leaves most
+    empty, in a workspace of NaN: none of it reaches a row."""
+    t = torch()
+    c = Case([40, 700, 0], [2, 3, 1], 2, d, 64, dt(dtype), seed=plan, capacity=plan)
+    step = c.planned(plan)
+    q, out, z, scale = attend(c, 6, dt(dtype), batch=step)
+    ref = attend64(c, q, scale)
+    check_out(out, ref, dt(dtype), slice(0, c.rows))
+    check_lse(z, ref, slice(0, c.rows))
+    ws = t.full((bqe.rfpx_attn_workspace_bytes(c.cache, step, 6, c.rows),), 255, dtype=t.uint8, device="cuda")
+    assert t.equal(bqe.rfpx_attn_forward(c.cache, step, q, scale, ws=ws), out)
+
+
 def test_attention_lengths_past_the_plan():
     """max_cols and max_len are for planning alone, and lens past the table's
     end counts as its end."""
