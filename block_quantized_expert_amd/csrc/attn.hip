@@ -1033,14 +1033,18 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
       if (tile < t_last) {
         const uint32_t x = __float_as_uint(top);
         const auto sw = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-        top = fmaxf(mx, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])) * a.sc);
+        const float raw = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+        top = fmaxf(mx, raw * a.sc);
         base = top == kNegInf ? 0.f : top;
         const float f = __builtin_amdgcn_exp2f(mx - base);
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[b] *= f;
         sum *= f;
         mx = top;
-        thr = (top + 60.f) / a.sc;
+        // Never below the tile's own scores, which the same products give again:
+        // so a tile is taken up at most twice.  (From 2^30 on the 60 is lost to
+        // rounding, and top / sc can lie below the score that top came from.)
+        thr = fmaxf(raw, (top + 60.f) / a.sc);
         again = true;
       }
     }
