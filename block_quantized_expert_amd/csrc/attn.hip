@@ -20,6 +20,16 @@
 // P never leaves its registers.  Softmax is the running kind: row maximum
 // and sum in fp32, the maximum moved (and everything rescaled) only when a
 // score exceeds it by 2^8.
+//
+// Bases.  Maxima are kept as the products give them (raw), so that comparing
+// them rounds nothing.  What a row's numerators stand against is base =
+// fl(maximum * sc): 2^(s sc - base) is one fma a score, and what base was
+// rounded by (half a step of it at most) is a factor that the sums, the joins
+// and lse share.  At a base of 2^31 that factor can be 2^64, so from |base| =
+// kWide on numerators are 2^((s - maximum) sc) instead, 1 at the maximum
+// itself, and joins take the same difference.  A wave with such a row has a
+// threshold of -inf, so that all its tiles come by the block where maxima move,
+// and other waves pay nothing for it.
 #include "rfpx_attn.hpp"
 
 namespace rfpx {
@@ -45,7 +55,7 @@ struct AttnArgs {
   void *out;
   float *lse;
   float *part;    // [rows * heads][splits][D] numerators (splits > 1)
-  float *part_ml; // [rows * heads][splits][4]: maximum, sum, exact sum
+  float *part_ml; // [rows * heads][splits][4]: raw maximum, sum, exact sum
   long long q_stride, out_stride;
   int xtype, heads, group, n_rows, splits, row_blocks;
   float sc;       // 16 * scale * log2(e)
@@ -68,6 +78,27 @@ __device__ __forceinline__ float max_across_g(float x) {
   const uint32_t w = __float_as_uint(x);
   const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Half a step of a base of 2^24 is 1, a factor of two at most (and scores of
+// that size have lost as much to their own rounding).
+constexpr float kWide = 16777216.f;
+
+// What numerators against the raw maximum `from` are multiplied by (as a power
+// of two) to stand against `to`, which is no smaller: the difference of the
+// bases as they were rounded, or of the maxima where they are wide.
+__device__ __forceinline__ float base_step(float from, float to, float sc) {
+#pragma clang fp contract(off)
+  if (to == kNegInf) to = 0.f;  // nothing seen yet: numerators against 0
+  const float base = to * sc, was = from * sc;
+  return fabsf(base) < kWide ? was - base : (from - to) * sc;
+}
+
+// Log of a row's sum `ex` of numerators against its raw maximum.
+__device__ __forceinline__ float lse_of(float top, float ex, float sc) {
+#pragma clang fp contract(off)
+  const float base = top * sc;
+  return (base + log2f(ex)) * 0.69314718055994531f;
 }
 
 // N dwords from p (aligned to their size, at most 16 bytes a load).
@@ -382,7 +413,11 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
     Offsets<NB, RT> offs;
     // l is the sum of the numerators as they enter the second product, the
     // output's denominator; exact the one before bf16 rounding, for lse
-    float mx[RT], thr[RT], exact[RT];
+    // mx: raw maximum; a score above thr moves it; numerators are 2^(s sc -
+    // base), with a wide base against 0 and mx taken off s before
+    float mx[RT], thr[RT], base[RT], exact[RT];
+    // (finite, so that a row without a maximum stays without)
+    const float room = fminf(8.f / a.sc, 3.0e38f);
     uint32_t poison[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -390,6 +425,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < (NB + 3) / 4; ++j) offs.sum[t][j] = floatx4{0.f, 0.f, 0.f, 0.f};
       mx[t] = thr[t] = kNegInf;
+      base[t] = 0.f;
       exact[t] = 0.f;
       poison[t] = 0;
 #pragma unroll
@@ -486,10 +522,9 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       for (int t = 0; t < RT; ++t) {
         float top = fmaxf(fmaxf(fmaxf(s[t][0][0], s[t][0][1]), fmaxf(s[t][0][2], s[t][0][3])),
                           fmaxf(fmaxf(s[t][1][0], s[t][1][1]), fmaxf(s[t][1][2], s[t][1][3])));
-        if (__ballot(top > thr[t])) {
-          top = fmaxf(mx[t], max_across_g(top) * a.sc);
-          const float base = top == kNegInf ? 0.f : top;
-          const float f = __builtin_amdgcn_exp2f(mx[t] - base);
+        if (__builtin_expect(__ballot(top > thr[t]) != 0, 0)) {
+          top = fmaxf(mx[t], max_across_g(top));
+          const float f = __builtin_amdgcn_exp2f(base_step(mx[t], top, a.sc));
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             acc[t][b][0] *= f;
@@ -500,15 +535,24 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
           l[t] *= f;
           exact[t] *= f;
           mx[t] = top;
-          thr[t] = (top + 8.f) / a.sc;
+          const float ref = top == kNegInf ? 0.f : top;
+          thr[t] = top + room;
+          base[t] = ref * a.sc;
+          if (__builtin_expect(__ballot(!(fabsf(base[t]) < kWide)) != 0, 0)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[t][u][i] -= ref;
+            thr[t] = kNegInf;
+            base[t] = 0.f;
+          }
         }
-        const float base = mx[t] == kNegInf ? 0.f : mx[t];
         float e[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            e[4 * u + i] = __builtin_amdgcn_exp2f(fmaf(s[t][u][i], a.sc, -base));
+            e[4 * u + i] = __builtin_amdgcn_exp2f(fmaf(s[t][u][i], a.sc, -base[t]));
         if (VX == 1)
           exact[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
@@ -554,8 +598,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       float top = kNegInf;
 #pragma unroll
       for (int w = 0; w < W; ++w) top = fmaxf(top, sh_ml[w][16 * t + m][0]);
-      const float base = top == kNegInf ? 0.f : top;
-      const float f = __builtin_amdgcn_exp2f(mx[t] - base);
+      const float f = __builtin_amdgcn_exp2f(base_step(mx[t], top, a.sc));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float h = (poison[t] >> b) & 1 ? __builtin_nanf("") : f;
@@ -573,11 +616,10 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
           float rt = kNegInf, sum = 0.f, ex = 0.f;
 #pragma unroll
           for (int w = 0; w < W; ++w) rt = fmaxf(rt, sh_ml[w][16 * t + row][0]);
-          const float rb = rt == kNegInf ? 0.f : rt;
           floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            const float f = __builtin_amdgcn_exp2f(sh_ml[w][16 * t + row][0] - rb);
+            const float f = __builtin_amdgcn_exp2f(base_step(sh_ml[w][16 * t + row][0], rt, a.sc));
             sum += sh_ml[w][16 * t + row][1] * f;
             ex += sh_ml[w][16 * t + row][2] * f;
             o += *reinterpret_cast<const floatx4 *>(&sh_o[w][row][d]);
@@ -593,7 +635,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
                   make_uint2(pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]));
             else
               *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + at) = o;
-            if (a.lse && d == 0) a.lse[rh] = (rt + log2f(ex)) * 0.69314718055994531f;
+            if (a.lse && d == 0) a.lse[rh] = lse_of(rt, ex, a.sc);
           } else {
             const size_t at = rh * a.splits + split;
             if (rt != kNegInf || sum != 0.f) *reinterpret_cast<floatx4 *>(a.part + at * D + d) = o;
@@ -618,7 +660,7 @@ __device__ __forceinline__ void join_write(const AttnArgs &a, long long rh, int 
         make_uint2(pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]));
   else
     *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + at) = o;
-  if (a.lse && d == 0) a.lse[rh] = (top + log2f(ex)) * 0.69314718055994531f;
+  if (a.lse && d == 0) a.lse[rh] = lse_of(top, ex, a.sc);
 }
 
 // Joins the splits of a (row, head): a workgroup each, four values a thread,
@@ -637,14 +679,13 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
     for (int s = lane; s < a.splits; s += 64) top = fmaxf(top, ml[s].x);
 #pragma unroll
     for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    const float base = top == kNegInf ? 0.f : top;
     float sum = 0.f, ex = 0.f;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int s = g; s < a.splits; s += NG) {
       const float4 w = ml[s];
       if (w.x == kNegInf && w.y == 0.f) continue;  // no tokens: its numerators were not written
-      const float f = __builtin_amdgcn_exp2f(w.x - base);
+      const float f = __builtin_amdgcn_exp2f(base_step(w.x, top, a.sc));
       sum += w.y * f;
       ex += w.z * f;
       o += *reinterpret_cast<const floatx4 *>(a.part + (rh * a.splits + s) * D + d) * f;
@@ -686,7 +727,6 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
     float top = kNegInf;
 #pragma unroll 4
     for (int s = 0; s < a.splits; ++s) top = fmaxf(top, ml[s].x);
-    const float base = top == kNegInf ? 0.f : top;
     float sum = 0.f, ex = 0.f;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -694,7 +734,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
       const float4 w = ml[s];
       floatx4 v = *reinterpret_cast<const floatx4 *>(a.part + (rh * a.splits + s) * D + d);
       const bool none = w.x == kNegInf && w.y == 0.f;
-      const float f = none ? 0.f : __builtin_amdgcn_exp2f(w.x - base);
+      const float f = none ? 0.f : __builtin_amdgcn_exp2f(base_step(w.x, top, a.sc));
       if (none) v = floatx4{0.f, 0.f, 0.f, 0.f};
       sum += w.y * f;
       ex += w.z * f;
@@ -883,7 +923,8 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
-    float mx = kNegInf, base = 0.f, thr = kNegInf, sum = 0.f;
+    float mx = kNegInf, base = 0.f, thr = kNegInf, sum = 0.f;  // as in k_attn
+    const float room = fminf(60.f / a.sc, 3.0e38f);  // finite, as in k_attn
     uint32_t poison = 0;
 
     // the page of a token (of the table's last token, past its end)
@@ -999,53 +1040,65 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
 
     // The inner loop keeps the base that numerators are relative to: sums in
     // floating point have room for scores up to 2^60 above it.  A score beyond
-    // leaves it (so does the first tile), and everything summed up so far is
-    // scaled to a new base before the tile is taken up again.
-    bool again = false;
-    for (int tile = t_first; tile < t_last;) {
+    // leaves it (so does the first tile); everything summed up so far is scaled
+    // to a new base, and that tile is computed here, whatever its scores.
+    const auto scores_at = [&](int tile, int at, floatx16 &s0, floatx16 &s1) {
+      scores_of(buf_k[at], 0, s0);
+      scores_of(buf_k[at], 1, s1);
+      if (!is_whole(tile)) {
+        hide(tile, 0, at, s0);
+        hide(tile, 1, at, s1);
+      }
+      return fmaxf(top_of(s0), top_of(s1));
+    };
+    const auto take = [&](int at, floatx16 &s0, floatx16 &s1) {
+      u32x4v p0[2], p1[2];
+      numerators(s0, p0);
+      add_up(buf_v[at], 0, p0);
+      numerators(s1, p1);
+      add_up(buf_v[at], 1, p1);
+    };
+    for (int tile = t_first; tile < t_last; ++tile) {
       float top = kNegInf;
       for (; tile < t_last; ++tile) {
         const int at = (tile - t_first) & 1;
-        if (!again) {
-          __syncthreads();
-          if (tile + 1 < t_last && !is_whole(tile + 1)) screen(tile + 1, page, raw, at ^ 1);
-          if (early) next(tile, at ^ 1);
-        }
-        again = false;
+        __syncthreads();
+        if (tile + 1 < t_last && !is_whole(tile + 1)) screen(tile + 1, page, raw, at ^ 1);
+        if (early) next(tile, at ^ 1);
         if (tile < t_wave) {
           floatx16 s0, s1;
-          scores_of(buf_k[at], 0, s0);
-          scores_of(buf_k[at], 1, s1);
-          if (!is_whole(tile)) {
-            hide(tile, 0, at, s0);
-            hide(tile, 1, at, s1);
-          }
-          top = fmaxf(top_of(s0), top_of(s1));
+          top = scores_at(tile, at, s0, s1);
           if (__ballot(top > thr)) break;
-          u32x4v p0[2], p1[2];
-          numerators(s0, p0);
-          add_up(buf_v[at], 0, p0);
-          numerators(s1, p1);
-          add_up(buf_v[at], 1, p1);
+          take(at, s0, s1);
         }
         if (!early) next(tile, at ^ 1);
       }
       if (tile < t_last) {
+        const int at = (tile - t_first) & 1;
         const uint32_t x = __float_as_uint(top);
         const auto sw = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-        const float raw = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
-        top = fmaxf(mx, raw * a.sc);
-        base = top == kNegInf ? 0.f : top;
-        const float f = __builtin_amdgcn_exp2f(mx - base);
+        top = fmaxf(mx, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])));
+        const float f = __builtin_amdgcn_exp2f(base_step(mx, top, a.sc));
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[b] *= f;
         sum *= f;
         mx = top;
-        // Never below the tile's own scores, which the same products give again:
-        // so a tile is taken up at most twice.  (From 2^30 on the 60 is lost to
-        // rounding, and top / sc can lie below the score that top came from.)
-        thr = fmaxf(raw, (top + 60.f) / a.sc);
-        again = true;
+        const float ref = top == kNegInf ? 0.f : top;
+        base = ref * a.sc;
+        thr = top + room;
+        floatx16 s0, s1;
+        scores_at(tile, at, s0, s1);
+        if (__ballot(!(fabsf(base) < kWide))) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s0[i] -= ref;
+            s1[i] -= ref;
+          }
+          thr = kNegInf;
+          base = 0.f;
+        }
+        take(at, s0, s1);
+        if (!early) next(tile, at ^ 1);
       }
     }
     __syncthreads();
@@ -1077,7 +1130,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
           *reinterpret_cast<float4 *>(a.part_ml + 4 * (rh * a.splits + split)) =
               make_float4(mx, sum, sum, 0.f);
         else if (a.lse)
-          a.lse[rh] = (mx + log2f(sum)) * 0.69314718055994531f;
+          a.lse[rh] = lse_of(mx, sum, a.sc);
       }
     }
   }

@@ -1,9 +1,18 @@
 """Attention over the FP4 cache (include/rfpx_attn.h) at the edges of what a
-caller may hand in, with the rows and tolerances of test_gpu_attn.py."""
+caller may hand in, with the rows and tolerances of test_gpu_attn.py.
+
+Where scores are so large that only the best token of a row has any weight,
+the row is that token's values: the numerators of the others are 0, its own and
+the sum of them are the same number (or, in k_attn_chunk, that number rounded to
+bf16 and itself), so that the output is off by at most 2 u(bf16) of the value (4
+u32 in fp32), by the offset's removal (256 u32 of 31 units, as everywhere) and
+by its own type's rounding.
+"""
+import numpy as np
 import pytest
 
 import block_quantized_expert_amd as bqe
-from test_gpu_attn import Case, attend64, check_lse, check_out, torch
+from test_gpu_attn import U32, UBF, Case, attend64, check_lse, check_out, dt, f64, torch, units
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +43,75 @@ def test_many_rows_end_at_any_score(d, scale, low):
         even = {n: x[:, 0:heads_seen:2] for n, x in ref.items() if n not in ("w", "dw")}
         check_out(out[:, 0:heads_seen:2], even, t.bfloat16, slice(0, c.rows))
         check_lse(z[:, 0:heads_seen:2], even, slice(0, c.rows))
+
+
+def peaked(n, hk, d, page, dtype, cols, capacity, seed):
+    """A sequence of n slots whose keys lie along one pattern a head, between
+    one and two of it, but for one four times as long and one a quarter: for a
+    query along the pattern the long one is best by far, for one against it the
+    short one.  Neither stands in the first tiles, so that the running maximum
+    moves."""
+    t = torch()
+    c = Case([n], [cols], hk, d, page, dtype, seed=seed, capacity=capacity)
+    g = t.Generator(device="cuda").manual_seed(seed + 1)
+    signs = t.randint(0, 2, (1, hk, d), generator=g, device="cuda") * 2.0 - 1
+    size = 1 + t.rand((n, hk, 1), generator=g, device="cuda")
+    size[n // 2], size[n // 2 + 7] = 8.0, 0.25
+    k = (signs * size).to(dtype)
+    bqe.rfpx_kv_append(c.cache, c.fill, k, c.v_in)
+    return c, signs
+
+
+def check_peaked(c, signs, heads, dtype, low, high, scale, batch, seed):
+    """Rows whose best score is 2^low .. 2^high in size (as powers of two that
+    the softmax takes), of either sign."""
+    t = torch()
+    g = t.Generator(device="cuda").manual_seed(seed)
+    rows, group = c.rows, heads // c.hk
+    (k, v), = c.values()
+    # the best score of a query of ones is 8 d, or 0.25 d against the pattern
+    sign = t.randint(0, 2, (rows, heads, 1), generator=g, device="cuda") * 2.0 - 1
+    best = c.d * t.where(sign > 0, 8.0, 0.25) * scale * 1.4426950408889634
+    want = 2.0 ** (low + (high - low) * t.rand((rows, heads, 1), generator=g, device="cuda", dtype=t.float64))
+    spread = 0.9 + 0.2 * t.rand((rows, heads, c.d), generator=g, device="cuda")
+    q = (signs.repeat_interleave(group, 1) * sign * spread * (want / best)).to(dtype)
+    out, z = t.full_like(q, 7.0), t.full((rows, heads), 7.0, device="cuda")
+    bqe.rfpx_attn_forward(c.cache, batch, q, scale, out=out, lse=z)
+    o, z, bf = f64(out), f64(z), dtype == t.bfloat16
+    kk = t.from_numpy(k).cuda()
+    q64 = q.double().view(rows, c.hk, group, c.d)
+    s = t.stack([(q64[:, h].reshape(rows * group, c.d) @ kk[:, h].T).view(rows, group, -1) for h in range(c.hk)], 1)
+    s = s.reshape(rows, heads, -1) * scale
+    seen = len(k) - rows + t.arange(rows, device="cuda").view(-1, 1, 1)
+    s = s.masked_fill(t.arange(len(k), device="cuda") > seen, -float("inf"))
+    (top, second), (at, _) = (x.unbind(-1) for x in s.topk(2, -1))
+    # the best token leads by a tenth of its score, which is beyond any rounding of it
+    assert bool((top - second > 0.1 * top.abs()).all()) and bool((top.abs() * 1.44 > 2.0 ** (low - 1)).all())
+    top, at = top.cpu().numpy(), at.cpu().numpy()
+    head = np.arange(heads)[None] // group
+    vv, uu = v[at, head], units(v)[at, head]
+    tol = (3 * UBF if bf else 5 * U32) * np.abs(vv) + 256 * U32 * 31 * uu
+    err = np.abs(o - vv)
+    assert (err <= tol).all(), f"{(~(err <= tol)).sum()} values off, worst {np.nanmax(err / tol):.3g}"
+    # lse is the best score: the products' roundings, and the offset's (beyond
+    # fp32 an infinity)
+    big = scale * np.abs(f64(q)).sum(-1) * 31 * units(k).max()
+    with np.errstate(invalid="ignore"):
+        near = np.abs(z - top) <= 256 * U32 * big + 2.0 ** -21 * np.abs(top)
+    assert (near | (np.isinf(z) & (np.abs(top) > 2.0 ** 127) & (np.sign(z) == np.sign(top)))).all()
+
+
+# 16 rows and 32, one workgroup of eight waves, four waves with both joins, heads
+# of 256; and the path of many rows in 64 splits and whole
+PATHS = [(2, 8, 128, 1, 0), (2, 16, 64, 3, 0), (2, 16, 128, 3, 0), (2, 8, 128, 1, 1500), (2, 8, 64, 5, 4096),
+         (2, 8, 256, 2, 700), (2, 16, 64, 10, 65536), (2, 16, 128, 10, 65536), (128, 128, 128, 80, 1024)]
+
+
+@pytest.mark.parametrize("low,high,scale", [
+    (20, 20.6, 0.125), (23.5, 24.5, 1.0), (30, 30.6, 0.125), (30, 30.6, 128 ** -0.5), (33, 33.6, 1.0), (60, 60.6, 0.125),
+    (100, 100.6, 1.0), (131, 131.6, 1e29)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("hk,heads,d,cols,plan", PATHS)
+def test_scores_of_any_size(hk, heads, d, cols, plan, dtype, low, high, scale):
+    c, signs = peaked(700, hk, d, 64, dt(dtype), cols, max(plan, 700), seed=d)
+    check_peaked(c, signs, heads, dt(dtype), low, high, scale, c.planned(plan), seed=int(100 * low))
