@@ -758,6 +758,10 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
 constexpr int kChunkWaves = 8;
 constexpr int kChunkRows = 32 * kChunkWaves;
 constexpr int kChunkTile = 64;
+// A score may exceed a row's base by this much (as a power of two) before the
+// base moves: rarely reached by scores that rise along a sequence, and little
+// of fp32's range, which values as large as 2^100 need as well.
+constexpr float kChunkRoom = 16.f;
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
@@ -924,7 +928,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
     float mx = kNegInf, base = 0.f, thr = kNegInf, sum = 0.f;  // as in k_attn
-    const float room = fminf(60.f / a.sc, 3.0e38f);  // finite, as in k_attn
+    const float room = fminf(kChunkRoom / a.sc, 3.0e38f);  // finite, as in k_attn
     uint32_t poison = 0;
 
     // the page of a token (of the table's last token, past its end)
@@ -1038,10 +1042,10 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     // work.
     const bool early = wave >= 4;
 
-    // The inner loop keeps the base that numerators are relative to: sums in
-    // floating point have room for scores up to 2^60 above it.  A score beyond
-    // leaves it (so does the first tile); everything summed up so far is scaled
-    // to a new base, and that tile is computed here, whatever its scores.
+    // The inner loop keeps the base that numerators are relative to.  A score
+    // far above it leaves it (so does the first tile); everything summed up so
+    // far is scaled to a new base, and that tile is computed here, whatever its
+    // scores.
     const auto scores_at = [&](int tile, int at, floatx16 &s0, floatx16 &s1) {
       scores_of(buf_k[at], 0, s0);
       scores_of(buf_k[at], 1, s1);

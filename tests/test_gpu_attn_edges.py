@@ -115,3 +115,30 @@ PATHS = [(2, 8, 128, 1, 0), (2, 16, 64, 3, 0), (2, 16, 128, 3, 0), (2, 8, 128, 1
 def test_scores_of_any_size(hk, heads, d, cols, plan, dtype, low, high, scale):
     c, signs = peaked(700, hk, d, 64, dt(dtype), cols, max(plan, 700), seed=d)
     check_peaked(c, signs, heads, dt(dtype), low, high, scale, c.planned(plan), seed=int(100 * low))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("hk,heads,d,cols,plan", PATHS[1:6] + [(2, 8, 64, 20, 65536), (128, 128, 128, 66, 1024)])
+def test_large_values_under_rising_scores(hk, heads, d, cols, plan, dtype):
+    """Values of 2^85 while a row's scores rise by 25 powers of two a tile of 64
+    tokens: numerators and sums stay in fp32's range, and so does the output."""
+    t = torch()
+    n = 400
+    c = Case([n], [cols], hk, d, 64, dt(dtype), seed=d, capacity=max(plan, n))
+    g = t.Generator(device="cuda").manual_seed(3)
+    signs = t.randint(0, 2, (1, hk, d), generator=g, device="cuda") * 2.0 - 1
+    k = signs * (1 + 6 * t.arange(n, device="cuda").view(n, 1, 1) / n)
+    bqe.rfpx_kv_append(c.cache, c.fill, k.to(dt(dtype)), (c.v_in.float() * 2.0 ** 85).to(dt(dtype)))
+    # a score of size s is s * 25.6 powers of two: 25.6 * 6 * 64 / 400 a tile
+    q = signs.repeat_interleave(heads // hk, 1) * t.ones((c.rows, heads, d), device="cuda") * (25.6 / 1.4427 / d)
+    q = q.to(dt(dtype))
+    z = t.zeros((c.rows, heads), device="cuda")
+    out = bqe.rfpx_attn_forward(c.cache, c.planned(plan), q, 1.0, lse=z)
+    (kk, vv), = c.values()
+    few = min(hk, 4)  # heads: the plain form takes its time
+    h = few * heads // hk
+    c.hk, c.values = few, lambda: [(kk[:, :few], vv[:, :few])]
+    ref = attend64(c, q[:, :h], 1.0)
+    check_out(out[:, :h], ref, dt(dtype), slice(0, c.rows))
+    check_lse(z[:, :h], ref, slice(0, c.rows))
+    assert bool(t.isfinite(out).all())
