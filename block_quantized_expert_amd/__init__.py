@@ -174,6 +174,22 @@ def _ptr(t) -> C.c_void_p:
     return C.c_void_p(t.data_ptr())
 
 
+def _new(like, shape, dtype, stream=None):
+    """An uninitialized tensor beside `like` for a call on `stream` (None: the
+    current one).  Its memory comes from that stream's pool, where nothing
+    queued on another stream can still be using it; the caller may go on with
+    it on the current stream."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if stream != here:
+        t.record_stream(here)
+    return t
+
+
 def _need_cuda(*ts):
     for t in ts:
         if not t.is_cuda:
@@ -199,7 +215,7 @@ def rfpx_pack(fmt: int, w, out=None, stream=None):
     rows, cols = w.shape
     n = rfpx_matrix_bytes(fmt, rows, cols)
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=w.device)
+        out = _new(w, n, torch.uint8, stream)
     _check("rfpx_pack", lib().rfpx_pack(fmt, _ptr(w), rows, cols, _ptr(out),
                                         out.numel(), _stream(stream)))
     return out
@@ -215,7 +231,7 @@ def rfpx_pack_weighted(fmt: int, w, imp, out=None, stream=None):
         raise ValueError("imp must hold one importance per column")
     n = rfpx_matrix_bytes(fmt, rows, cols)
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=w.device)
+        out = _new(w, n, torch.uint8, stream)
     _check("rfpx_pack_weighted", lib().rfpx_pack_weighted(
         fmt, _ptr(w), _ptr(imp), rows, cols, _ptr(out), out.numel(), _stream(stream)))
     return out
@@ -229,7 +245,7 @@ def rfpx_pack_codes(fmt: int, codes, scale_bits, out=None, stream=None):
     rows, cols = codes.shape
     n = rfpx_matrix_bytes(fmt, rows, cols)
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=codes.device)
+        out = _new(codes, n, torch.uint8, stream)
     _check("rfpx_pack_codes", lib().rfpx_pack_codes(
         fmt, _ptr(codes), _ptr(scale_bits), rows, cols, _ptr(out), out.numel(),
         _stream(stream)))
@@ -240,7 +256,7 @@ def rfpx_unpack(fmt: int, data, rows: int, cols: int, out=None, stream=None):
     import torch
     _need_cuda(data)
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.float32, device=data.device)
+        out = _new(data, (rows, cols), torch.float32, stream)
     _check("rfpx_unpack", lib().rfpx_unpack(fmt, _ptr(data), rows, cols, _ptr(out),
                                             _stream(stream)))
     return out
@@ -270,7 +286,7 @@ def moe_image_build(d: int, f: int, n_experts: int, fmts,
         _need_cuda(t)
     ptrs = (C.c_void_p * len(canonical))(*[t.data_ptr() for t in canonical])
     if out is None:
-        out = torch.empty(n, dtype=torch.uint8, device=canonical[0].device)
+        out = _new(canonical[0], n, torch.uint8, stream)
     _check("moe_image_build", lib().moe_image_build(
         d, f, n_experts, C.cast(fa, C.c_void_p), C.cast(ptrs, C.c_void_p), _ptr(out),
         out.numel(), _stream(stream)))
@@ -308,7 +324,7 @@ def moe_image_validate(layer: MoeLayer, report=None, stream=None):
     passes."""
     import torch
     if report is None:
-        report = torch.empty(4, dtype=torch.int32, device=layer._image.device)
+        report = _new(layer._image, 4, torch.int32, stream)
     _need_cuda(report)
     _check("moe_image_validate", lib().moe_image_validate(layer.ref, _ptr(report),
                                                           _stream(stream)))
@@ -332,7 +348,7 @@ def moe_image_unpack(layer: MoeLayer, expert: int, matrix: int, out=None,
     import torch
     rows, cols = (layer.f, layer.d) if matrix < 2 else (layer.d, layer.f)
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.float32, device=layer._image.device)
+        out = _new(layer._image, (rows, cols), torch.float32, stream)
     _check("moe_image_unpack", lib().moe_image_unpack(layer.ref, expert, matrix,
                                                       _ptr(out), _stream(stream)))
     return out
@@ -344,14 +360,14 @@ def moe_workspace_bytes(layer: MoeLayer, q_or_T: int, prefill: bool = False) -> 
     return lib().moe_workspace_bytes(layer.ref, q_or_T, 1 if prefill else 0)
 
 
-def workspace(layer: MoeLayer, q_or_T: int, prefill: bool = False):
+def workspace(layer: MoeLayer, q_or_T: int, prefill: bool = False, stream=None):
     """A workspace of the right size (uninitialized: the library needs no
-    particular contents)."""
+    particular contents) for calls on `stream` (None: the current one)."""
     import torch
     n = moe_workspace_bytes(layer, q_or_T, prefill)
     if n == 0:
         raise RfpxError("moe_workspace_bytes", -2, "unsupported shape")
-    return torch.empty(n, dtype=torch.uint8, device=layer._image.device)
+    return _new(layer._image, n, torch.uint8, stream)
 
 
 def _xtype(x) -> int:
@@ -368,11 +384,11 @@ def moe_route_topk(layer: MoeLayer, x, ids=None, w=None, ws=None, stream=None):
     _need_cuda(x)
     q = x.shape[0]
     if ids is None:
-        ids = torch.empty((q, layer.top_k), dtype=torch.int32, device=x.device)
+        ids = _new(x, (q, layer.top_k), torch.int32, stream)
     if w is None:
-        w = torch.empty((q, layer.top_k), dtype=torch.float32, device=x.device)
+        w = _new(x, (q, layer.top_k), torch.float32, stream)
     if ws is None:
-        ws = workspace(layer, q)
+        ws = workspace(layer, q, stream=stream)
     _check("moe_route_topk", lib().moe_route_topk(
         layer.ref, _ptr(x), _xtype(x), q, _ptr(ids), _ptr(w), _ptr(ws), ws.numel(),
         _stream(stream)))
@@ -384,9 +400,9 @@ def moe_layer_forward(layer: MoeLayer, x, y=None, ws=None, stream=None):
     _need_cuda(x)
     q = x.shape[0]
     if y is None:
-        y = torch.empty((q, layer.d), dtype=torch.float32, device=x.device)
+        y = _new(x, (q, layer.d), torch.float32, stream)
     if ws is None:
-        ws = workspace(layer, q)
+        ws = workspace(layer, q, stream=stream)
     _check("moe_layer_forward", lib().moe_layer_forward(
         layer.ref, _ptr(x), _xtype(x), q, _ptr(y), _ptr(ws), ws.numel(),
         _stream(stream)))
@@ -420,9 +436,9 @@ def moe_prefill_forward(layer: MoeLayer, x, y=None, ws=None, stream=None):
     _need_cuda(x)
     T = x.shape[0]
     if y is None:
-        y = torch.empty((T, layer.d), dtype=torch.float32, device=x.device)
+        y = _new(x, (T, layer.d), torch.float32, stream)
     if ws is None:
-        ws = workspace(layer, T, prefill=True)
+        ws = workspace(layer, T, prefill=True, stream=stream)
     _check("moe_prefill_forward", lib().moe_prefill_forward(
         layer.ref, _ptr(x), _xtype(x), T, _ptr(y), _ptr(ws), ws.numel(),
         _stream(stream)))
@@ -456,7 +472,7 @@ class DenseMatrix:
         n = lib().rfpx_dense_image_bytes(fmt, rows, cols)
         if n == 0:
             raise RfpxError("rfpx_dense_image_bytes", -2, f"unsupported {rows} x {cols}")
-        self.image = torch.empty(n, dtype=torch.uint8, device=canonical.device)
+        self.image = _new(canonical, n, torch.uint8, stream)
         _check("rfpx_dense_image_build", lib().rfpx_dense_image_build(
             fmt, _ptr(canonical), rows, cols, _ptr(self.image), n, _stream(stream)))
         self.fmt, self.rows, self.cols = fmt, rows, cols
@@ -464,18 +480,17 @@ class DenseMatrix:
     def unpack(self, out=None, stream=None):
         import torch
         if out is None:
-            out = torch.empty((self.rows, self.cols), dtype=torch.float32,
-                              device=self.image.device)
+            out = _new(self.image, (self.rows, self.cols), torch.float32, stream)
         _check("rfpx_dense_image_unpack", lib().rfpx_dense_image_unpack(
             self.fmt, _ptr(self.image), self.rows, self.cols, _ptr(out), _stream(stream)))
         return out
 
-    def workspace(self, q: int):
+    def workspace(self, q: int, stream=None):
         import torch
         n = lib().rfpx_dense_workspace_bytes(self.fmt, self.rows, self.cols, q)
         if n == 0:
             raise RfpxError("rfpx_dense_workspace_bytes", -2, "unsupported shape")
-        return torch.empty(n, dtype=torch.uint8, device=self.image.device)
+        return _new(self.image, n, torch.uint8, stream)
 
 
 def rfpx_dense_forward(m: DenseMatrix, x, y=None, ws=None, stream=None):
@@ -485,9 +500,9 @@ def rfpx_dense_forward(m: DenseMatrix, x, y=None, ws=None, stream=None):
     _need_cuda(x)
     q = x.shape[0]
     if y is None:
-        y = torch.empty((q, m.rows), dtype=torch.float32, device=x.device)
+        y = _new(x, (q, m.rows), torch.float32, stream)
     if ws is None:
-        ws = m.workspace(q)
+        ws = m.workspace(q, stream)
     _check("rfpx_dense_forward", lib().rfpx_dense_forward(
         m.fmt, _ptr(m.image), m.rows, m.cols, _ptr(x), _xtype(x), q, _ptr(y), _ptr(ws),
         ws.numel(), _stream(stream)))
@@ -516,9 +531,7 @@ def _rows(what: str, t):
 def _one_out(what, t, out, dtype, stream):
     """out, or a new tensor of t's shape and that dtype."""
     if out is None:
-        out = t.new_empty(t.shape, dtype=dtype)
-        if stream is not None:
-            _used_on(out, stream)
+        out = _new(t, t.shape, dtype, stream)
     elif out.shape != t.shape or out.dtype != dtype:
         raise ValueError(f"{what}_out must be a {dtype} tensor of {what}'s shape")
     return out
@@ -544,23 +557,6 @@ def _flat(what: str, t, dtype, shape):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
-
-
-def _scratch(n: int, like, stream):
-    """n bytes beside a tensor that live until the work on `stream` is done
-    with them."""
-    import torch
-    ws = like.new_empty(n, dtype=torch.uint8)
-    if stream is not None:
-        _used_on(ws, stream)
-    return ws
-
-
-def _used_on(t, stream):
-    """Tell the allocator that a tensor made here is used on `stream`."""
-    import torch
-    if stream is not None and stream != torch.cuda.current_stream():
-        t.record_stream(stream)
 
 
 class Rope:
@@ -689,13 +685,9 @@ def rfpx_kv_unpack(cache: KvCache, batch: KvBatch, rows: int, k=None, v=None, st
     import torch
     shape = (rows, cache.n_kv_heads, cache.head_dim)
     if k is None:
-        k = cache.pool.new_empty(shape, dtype=torch.float32)
-        if stream is not None:
-            _used_on(k, stream)
+        k = _new(cache.pool, shape, torch.float32, stream)
     if v is None:
-        v = cache.pool.new_empty(shape, dtype=k.dtype)
-        if stream is not None:
-            _used_on(v, stream)
+        v = _new(cache.pool, shape, k.dtype, stream)
     dev = _same_device(torch, cache.pool, batch.lens, k, v)
     _check("rfpx_kv_unpack", lib().rfpx_kv_unpack(
         cache.ref, batch.ref, rows, _flat("k", k, k.dtype, shape), _flat("v", v, k.dtype, shape),
@@ -717,16 +709,14 @@ def rfpx_attn_forward(cache: KvCache, batch: KvBatch, q, scale: Optional[float] 
         raise ValueError(f"q must be [rows][heads][{cache.head_dim}]")
     rows, heads, d = q.shape
     if out is None:
-        out = q.new_empty(q.shape)
-        if stream is not None:
-            _used_on(out, stream)
+        out = _new(q, q.shape, q.dtype, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
         n = rfpx_attn_workspace_bytes(cache, batch, heads, rows)
         if n == 0:
             raise RfpxError("rfpx_attn_workspace_bytes", -2, lib().rfpx_last_error().decode())
-        ws = _scratch(n, q, stream)
+        ws = _new(q, n, torch.uint8, stream)
     dev = _same_device(torch, cache.pool, batch.lens, q, out, lse, ws)
     qp, qs = _rows("q", q)
     op, os_ = _rows("out", out)
@@ -777,7 +767,7 @@ def rfpx_kv_evict(cache: KvCache, batch: KvBatch, keep: int, recent: int, acc, p
         n = rfpx_kv_evict_workspace_bytes(cache, batch, keep)
         if n == 0:
             raise RfpxError("rfpx_kv_evict_workspace_bytes", -2, lib().rfpx_last_error().decode())
-        ws = _scratch(n, cache.pool, stream)
+        ws = _new(cache.pool, n, torch.uint8, stream)
     dev = _same_device(torch, cache.pool, batch.lens, acc, pos, acc_out, pos_out, lens_out, ws)
     slots = _slots(cache, batch)
     _check("rfpx_kv_evict", lib().rfpx_kv_evict(
@@ -800,7 +790,9 @@ def rfpx_stream_read(buf, sink=None, stream=None):
     _need_cuda(buf)
     n = lib().rfpx_stream_read_sink_words()
     if sink is None:
-        sink = torch.zeros(n, dtype=torch.int32, device=buf.device)
+        sink = _new(buf, n, torch.int32, stream)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            sink.zero_()
     _check("rfpx_stream_read", lib().rfpx_stream_read(
         _ptr(buf), buf.numel() * buf.element_size(), _ptr(sink), _stream(stream)))
     return sink

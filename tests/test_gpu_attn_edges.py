@@ -142,3 +142,36 @@ def test_large_values_under_rising_scores(hk, heads, d, cols, plan, dtype):
     check_out(out[:, :h], ref, dt(dtype), slice(0, c.rows))
     check_lse(z[:, :h], ref, slice(0, c.rows))
     assert bool(t.isfinite(out).all())
+
+
+# ------------------------------------------------------------------ streams
+
+def test_side_stream_while_the_current_one_is_busy():
+    """Calls on a side stream while the current one still has writes queued to
+    blocks of memory that have gone back to the allocator: the calls' outputs
+    and workspaces are other memory."""
+    t = torch()
+    c = Case([3000, 700], [3, 2], 2, 128, 64, t.bfloat16)
+    q = t.randn((5, 8, 128), device="cuda").to(t.bfloat16)
+    pos = t.arange(5, dtype=t.int32, device="cuda")
+    rope = bqe.Rope(128)
+    x = t.randn((64, 256), device="cuda")
+    side = t.cuda.Stream()
+
+    def run(stream=None):
+        return (bqe.rfpx_attn_forward(c.cache, c.batch, q, stream=stream),
+                *bqe.rfpx_qk_norm_rope(q, q[:, :2], pos, rope=rope, stream=stream),
+                *bqe.rfpx_kv_unpack(c.cache, c.batch, 5, stream=stream), bqe.rfpx_pack(4, x, stream=stream))
+
+    want = run()
+    ws = bqe.rfpx_attn_workspace_bytes(c.cache, c.batch, 8, 5)
+    t.cuda.synchronize()
+    shapes = [(y.shape, y.dtype) for y in want] + [((ws,), t.uint8)]
+    for _ in range(3):
+        t.cuda._sleep(20_000_000)
+        for shape, dtype in shapes:
+            t.empty(shape, dtype=dtype, device="cuda").fill_(7)  # queued behind the sleep, and given back at once
+        got = run(side)
+        t.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert t.equal(a, b)
