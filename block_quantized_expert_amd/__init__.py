@@ -819,8 +819,8 @@ def upload_layer(lay, device="cuda", stream=None, validate: bool = True) -> MoeL
     L = MoeLayer(lay.d, lay.f, lay.E, lay.k, wr, image, lay.fmts,
                  getattr(lay, "routed_scale", 1.0))
     if validate:
-        check_image(L)  # waits for the stream, so the canonical bytes may go
+        check_image(L, stream)  # waits for the stream, so the canonical bytes may go
     else:
-        torch.cuda.current_stream().synchronize()
+        (stream or torch.cuda.current_stream()).synchronize()
     del blob, canon
     return L

@@ -128,3 +128,32 @@ def test_without_a_stream_the_current_one_is_used(world, name):
     here, made, noted = world
     CALLS[name](None)
     assert made and all(s is here for _, s in made) and not noted
+
+
+@pytest.mark.parametrize("validate", [True, False])
+def test_upload_waits_for_its_stream(world, monkeypatch, validate):
+    """The image is checked on the stream that builds it, and that stream is
+    waited for before the canonical bytes go."""
+    here, made, _ = world
+    waited, checked = [], []
+    side = Stream()
+    monkeypatch.setattr(Stream, "synchronize", lambda self: waited.append(self), raising=False)
+
+    def validate_on(l, report=None, stream=None):
+        checked.append(stream)
+        return torch.zeros(4, dtype=torch.int32)
+    monkeypatch.setattr(bqe, "moe_image_validate", validate_on)
+
+    class Synthetic:
+        import numpy as np
+        d = f = 32
+        E, k = 1, 1
+        fmts = [[4, 4, 4]] * 2
+        blob = np.zeros(6 * 544, np.uint8)
+        offsets = np.arange(6) * 544
+        wr = np.zeros((1, 32), np.float32)
+
+        def mat(self, e, m):
+            return self.blob[:544]
+    bqe.upload_layer(Synthetic(), device="cpu", stream=side, validate=validate)
+    assert waited == [side] and checked == ([side] if validate else [])
