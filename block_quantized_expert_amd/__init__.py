@@ -614,6 +614,9 @@ class KvBatch:
         _flat("page_table", page_table, torch.int32, (n, pages))
         _flat("lens", lens, torch.int32, (n,))
         _flat("starts", starts, torch.int32, (n + 1,))
+        # (a call looks at lens alone, for all three)
+        if page_table.device != lens.device or starts.device != lens.device:
+            raise ValueError("page_table, lens and starts must be on one device")
         self.page_table, self.lens, self.starts = page_table, lens, starts
         self.n_seqs, self.pages_per_seq = n, pages
         self.max_cols, self.max_len = max_cols, max_len

@@ -12,6 +12,7 @@ import block_quantized_expert_amd as bqe
 
 class Stream:
     cuda_stream = 1
+    device_index = -1  # where CPU tensors say they are
 
 
 class Lib:
@@ -47,7 +48,7 @@ def world(monkeypatch):
     monkeypatch.setattr(bqe, "_need_cuda", lambda *ts: None)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
     monkeypatch.setattr(torch.cuda, "stream", on)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)  # where CPU tensors say they are
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
     for name in ("empty", "zeros"):
         monkeypatch.setattr(torch, name, recorded(getattr(torch, name)))
@@ -157,3 +158,13 @@ def test_upload_waits_for_its_stream(world, monkeypatch, validate):
             return self.blob[:544]
     bqe.upload_layer(Synthetic(), device="cpu", stream=side, validate=validate)
     assert waited == [side] and checked == ([side] if validate else [])
+
+
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_a_batch_lies_on_one_device(world, at):
+    i = torch.int32
+    t = [tensor(1, 2, dtype=i), tensor(1, dtype=i), tensor(2, dtype=i)]
+    bqe.KvBatch(*t, 1, 32)
+    t[at] = t[at].to("meta")
+    with pytest.raises(ValueError, match="one device"):
+        bqe.KvBatch(*t, 1, 32)
