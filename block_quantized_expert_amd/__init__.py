@@ -546,7 +546,11 @@ def _same_device(torch, *ts):
 
 
 def _raw_stream(torch, dev, stream):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream must be one of the current device, cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _flat(what: str, t, dtype, shape):

@@ -168,3 +168,11 @@ def test_a_batch_lies_on_one_device(world, at):
     t[at] = t[at].to("meta")
     with pytest.raises(ValueError, match="one device"):
         bqe.KvBatch(*t, 1, 32)
+
+
+@pytest.mark.parametrize("name", ["rfpx_qk_norm_rope", "rfpx_kv_unpack", "rfpx_attn_forward", "rfpx_kv_evict"])
+def test_a_stream_of_another_device_is_refused(world, name):
+    other = Stream()
+    other.device_index = 1
+    with pytest.raises(ValueError, match="current device"):
+        CALLS[name](other)
