@@ -290,6 +290,8 @@ __global__ __launch_bounds__(kMoveThreads) void k_evict_move(EvictArgs a) {
     const int dst = a.holes[bh * a.list + i], src = a.late[bh * a.list + i];
     const uint8_t *from = kv_slab(a.v, seq, src, hd);
     uint8_t *to = kv_slab(a.v, seq, dst, hd);
+    // (also where a page is outside the pool, whose bytes cannot move: only a
+    // sequence that the caller must not hand in has such slots)
     if (r == 2) a.acc_out[bh * cap + dst] = a.acc[bh * cap + src];
     if (r == 3) a.pos_out[bh * cap + dst] = a.pos[bh * cap + src];
     if (!from || !to) continue;

@@ -176,9 +176,12 @@ size_t rfpx_kv_evict_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch
  * order: keys, values, acc and pos with them; every other kept slot stays
  * where it is.  lens_out[b] = min(lens[b], keep); acc_out and pos_out get
  * the slots below it.  acc_out, pos_out and lens_out may be acc, pos and
- * b->lens themselves (and overlap them no other way).  A move from or to a
- * page outside the pool is dropped.  0 <= recent, 1 <= keep.  Sequences must
- * not share pages. */
+ * b->lens themselves (and overlap them no other way).  0 <= recent, 1 <= keep.
+ * Sequences must not share pages, and every slot below lens[b] must have its
+ * page in the pool: the choice looks at acc and pos alone.  Of a sequence that
+ * breaks this nothing outside the pool is read or written and others are not
+ * touched, but its moves from or to such a page carry acc and pos only, keys
+ * and values stay, and its slots no longer belong together. */
 rfpx_status rfpx_kv_evict(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int keep, int recent,
                           const float *acc_dev, const int32_t *pos_dev, float *acc_out_dev,
                           int32_t *pos_out_dev, int32_t *lens_out_dev, void *ws_dev,

@@ -175,3 +175,34 @@ def test_side_stream_while_the_current_one_is_busy():
         t.cuda.synchronize()
         for a, b in zip(got, want):
             assert t.equal(a, b)
+
+
+# ----------------------------------------------------------------- eviction
+
+@pytest.mark.parametrize("bad", [-1, 2 ** 31 - 1, None])
+@pytest.mark.parametrize("at", [0, 2])
+def test_evict_beside_a_sequence_with_pages_outside(at, bad):
+    """The page that moves go to, or come from, lies outside the pool in one
+    sequence: its weights and positions move alone, no byte of the pool does,
+    and the other sequence is cut as ever."""
+    t = torch()
+    made = []
+    for broken in (False, True):
+        c = Case([96, 96], [96, 96], 2, 64, 32, t.float32, seed=5)
+        acc = t.arange(96, dtype=t.float32, device="cuda").expand(2, 2, 96).contiguous()
+        pos = t.arange(96, dtype=t.int32, device="cuda").expand(2, 2, 96).contiguous() + 7
+        mine = c.table[0].clone()
+        if broken:
+            c.table[0, at] = c.cache.n_pages if bad is None else bad
+        before = c.cache.pool.view(c.cache.n_pages, -1).clone()
+        ao, po, lo = bqe.rfpx_kv_evict(c.cache, c.fill, 32, 0, acc, pos)
+        assert lo.tolist() == [32, 32]
+        pool = c.cache.pool.view(c.cache.n_pages, -1)
+        # slots 64 .. 95 are the best 32, and go to 0 .. 31, in order
+        for b in range(2):
+            assert t.equal(ao[b, :, :32], t.arange(64.0, 96.0, device="cuda").expand(2, 32))
+            assert t.equal(po[b, :, :32], t.arange(71, 103, dtype=t.int32, device="cuda").expand(2, 32))
+        if broken:
+            assert t.equal(pool[mine.long()], before[mine.long()])
+        made.append(pool[c.table[1].long()].clone())
+    assert t.equal(*made)
