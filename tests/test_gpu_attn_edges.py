@@ -206,3 +206,203 @@ def test_evict_beside_a_sequence_with_pages_outside(at, bad):
             assert t.equal(pool[mine.long()], before[mine.long()])
         made.append(pool[c.table[1].long()].clone())
     assert t.equal(*made)
+
+
+# ------------------------------------------------------- plans and the data
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("hk,heads,d,cols,told,plan", [
+    (2, 16, 64, 100, 10, 65536), (2, 16, 128, 70, 9, 65536), (128, 128, 64, 300, 66, 1024), (2, 4, 128, 60, 1, 0),
+    (1, 3, 256, 40, 2, 300)])
+def test_more_columns_than_planned(hk, heads, d, cols, told, plan, dtype):
+    """A workgroup's second turn at row blocks, in both kernels: splits, whole
+    sequences, and the fewest row blocks."""
+    t = torch()
+    c = Case([330, 20], [cols, 3], hk, d, 64, dt(dtype), seed=d, capacity=max(plan, 330))
+    g = t.Generator(device="cuda").manual_seed(2)
+    q = (t.randn((c.rows, heads, d), generator=g, device="cuda") * 1.3).to(dt(dtype))
+    z = t.zeros((c.rows, heads), device="cuda")
+    small = bqe.KvBatch(c.table, c.batch.lens, c.batch.starts, told, max(plan, 1))
+    out = bqe.rfpx_attn_forward(c.cache, small, q, lse=z)
+    few = 1 if hk > 2 else hk  # kv heads: the plain form takes its time
+    values, h = [(k[:, :few], v[:, :few]) for k, v in c.values()], few * heads // hk
+    c.hk, c.values = few, lambda: values
+    ref = attend64(c, q[:, :h], d ** -0.5)
+    check_out(out[:, :h], ref, dt(dtype), slice(0, c.rows))
+    check_lse(z[:, :h], ref, slice(0, c.rows))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("d,heads,plan", [(64, 4, 0), (64, 20, 0), (256, 4, 0), (128, 20, 1500), (64, 40, 65536), (128, 40, 65536)])
+def test_nan_block_in_a_tile_that_all_rows_see(d, heads, plan, dtype):
+    """Far before the columns: every row of the head gets the values' NaN in its
+    block, and the keys' NaN everywhere."""
+    t = torch()
+    c = Case([400], [4], 2, d, 64, dt(dtype), seed=d, capacity=max(plan, 400))
+    k, v = c.k_in.clone(), c.v_in.clone()
+    v[17, 0, 33] = float("nan")
+    k[40, 1, d - 1] = float("inf")
+    bqe.rfpx_kv_append(c.cache, c.fill, k, v)
+    q = t.randn((4, heads, d), device="cuda").to(dt(dtype))
+    z = t.zeros((4, heads), device="cuda")
+    out = bqe.rfpx_attn_forward(c.cache, c.planned(plan), q, lse=z)
+    g = heads // 2
+    assert bool(out[:, :g, 32:64].isnan().all()) and bool(out[:, g:].isnan().all())
+    keep = [i for i in range(d) if not 32 <= i < 64]
+    assert bool(out[:, :g, keep].isfinite().all())
+    assert bool(z[:, :g].isfinite().all()) and bool(z[:, g:].isnan().all())
+
+
+# ------------------------------------------------------------------ weights
+
+def weights_batch(c, kernel, group, max_len=None):
+    """The batch as planned for k_attn_weights ("few") or k_attn_weights_chunk
+    ("many": 256 rows of a sequence and no more than 16 tokens to each)."""
+    cols = -(-256 // group) if kernel == "many" else max(1, min(c.cols))
+    return bqe.KvBatch(c.table, c.batch.lens, c.batch.starts, cols, max(c.lens) if max_len is None else max_len)
+
+
+def check_weights(c, got, start, decay, ref, heads=None):
+    """got = decay * start + the weights of ref (its scores' errors three times:
+    the score's own, lse's and the product's)."""
+    for b, n in enumerate(c.lens):
+        for h in range(c.hk) if heads is None else heads:
+            want = decay * f64(start)[b, h, :n] + ref["w"][b][h]
+            tol = 3 * ref["dw"][b][h] + 2.0 ** -20 * ref["w"][b][h] + 4 * U32 * want + 1e-30
+            err = np.abs(f64(got)[b, h, :n] - want)
+            assert (err <= tol).all(), (b, h, np.nanmax(err / tol))
+
+
+KERNELS = [(k, d, n) for k in ("few", "many") for d in (64, 128, 256) for n in ("bfloat16", "float32")]
+
+
+@pytest.mark.parametrize("kernel,d,dtype", KERNELS)
+@pytest.mark.parametrize("told", [None, 1, 64])
+def test_weights_rows_outside_strides_and_plans(kernel, d, dtype, told):
+    """Queries that are slices of wider rows, rows before the first sequence and
+    behind the last, sequences longer than planned."""
+    t = torch()
+    hk, group = 2, 3
+    c = Case([300, 0, 70, 161], [30, 2, 5, 7], hk, d, 32, dt(dtype), seed=d, gap=2)
+    g = t.Generator(device="cuda").manual_seed(6)
+    rows = c.rows + 3
+    wide = (t.randn((rows, 8, d), generator=g, device="cuda") * 1.3).to(dt(dtype))
+    q = wide[:, 1:1 + hk * group]
+    z = t.full((rows, hk * group), float("nan"), device="cuda")
+    wide[:2], wide[c.rows:] = float("nan"), float("nan")  # not read
+    bqe.rfpx_attn_forward(c.cache, c.batch, q, lse=z)
+    assert bool(z[:2].isnan().all()) and bool(z[c.rows:].isnan().all())
+    acc = t.rand((4, hk, c.per * 32), generator=g, device="cuda")
+    got = bqe.rfpx_attn_weights(c.cache, weights_batch(c, kernel, group, told), q, z, acc, 0.75,
+                                acc_out=t.full_like(acc, -3.0))
+    ref = attend64(c, q.nan_to_num(), d ** -0.5)
+    check_weights(c, got, acc, 0.75, ref)
+    for b, n in enumerate(c.lens):
+        assert bool((got[b, :, n:] == -3).all())
+
+
+@pytest.mark.parametrize("kernel,d,dtype", KERNELS)
+def test_weights_over_pages_outside(kernel, d, dtype):
+    """Slots without a page receive nothing: their weight only decays."""
+    t = torch()
+    hk, group = 2, 2
+    c = Case([200, 40], [9, 3], hk, d, 32, dt(dtype), seed=d)
+    vals = c.values()
+    c.table[0, 1], c.table[0, 4], c.table[1, 0] = -1, c.cache.n_pages, 2 ** 31 - 1
+    q = t.randn((12, 4, d), device="cuda").to(dt(dtype))
+    z = t.zeros((12, 4), device="cuda")
+    bqe.rfpx_attn_forward(c.cache, c.batch, q, lse=z)
+    acc = t.rand((2, hk, c.per * 32), device="cuda")
+    start = acc.clone()
+    bqe.rfpx_attn_weights(c.cache, weights_batch(c, kernel, group), q, z, acc, 0.5)
+    c.values = lambda: vals
+    ref = attend64(c, q, d ** -0.5, seen=lambda b, j: j // 32 not in ((1, 4) if b == 0 else (0,)))
+    check_weights(c, acc, start, 0.5, ref)
+    assert t.equal(acc[1, :, :32], start[1, :, :32] * 0.5) and t.equal(acc[0, :, 32:64], start[0, :, 32:64] * 0.5)
+
+
+@pytest.mark.parametrize("kernel,d,dtype", KERNELS)
+def test_weights_beside_nan(kernel, d, dtype):
+    """A NaN key reaches the head's slots through the rows that see it and no
+    others; a row of lse -inf gives nothing; NaN values give nothing either."""
+    t = torch()
+    hk, group, n = 2, 2, 200
+    c = Case([n, 50], [9, 3], hk, d, 64, dt(dtype), seed=d)
+    vals = c.values()
+    k, v = c.k_in[n - 9:n].clone(), c.v_in[n - 9:n].clone()
+    k[8, 1, 5], v[2, 0, 40] = float("nan"), float("inf")  # the last column's key of head 1
+    step = c.make([n, 50], [0, 9, 9], 9)
+    bqe.rfpx_kv_append(c.cache, step, k, v)
+    q = t.randn((12, 4, d), device="cuda").to(dt(dtype))
+    z = t.zeros((12, 4), device="cuda")
+    bqe.rfpx_attn_forward(c.cache, c.batch, q, lse=z)
+    assert bool(z[8, 2:].isnan().all()) and int(z.isnan().sum()) == 2
+    acc = t.rand((2, hk, c.per * 64), device="cuda")
+    b = weights_batch(c, kernel, group)
+    got = bqe.rfpx_attn_weights(c.cache, b, q, z, acc, 1.0, acc_out=t.zeros_like(acc))
+    c.values = lambda: vals
+    ref = attend64(c, q, d ** -0.5)
+    check_weights(c, got, acc, 1.0, ref, heads=[0])
+    assert bool(got[0, 1, :n].isnan().all()) and bool(got[1].isfinite().all())
+    # without the row that sees it
+    z[8, 2:] = -float("inf")
+    got = bqe.rfpx_attn_weights(c.cache, b, q, z, acc, 1.0, acc_out=t.zeros_like(acc))
+    ref["w"][0][1], ref["dw"][0][1] = 0, 0
+    kk = vals[0][0]
+    for i in range(8):
+        for h in (2, 3):
+            m = n - 9 + i + 1
+            s = d ** -0.5 * (kk[:m, 1] @ f64(q)[i, h])
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            ref["w"][0][1, :m] += p
+            ref["dw"][0][1, :m] += (2 * ref["ds"][i, h] + 2.0 ** -22) * p
+    check_weights(c, got, acc, 1.0, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_captured_weights_of_many_rows(dtype):
+    """A captured chunk with k_attn_weights_chunk, replayed with other lengths
+    and columns, against the eager calls and, each time, against 64 bits."""
+    t = torch()
+    hk, group, d, page, rows = 2, 8, 64, 32, 80
+    c = Case([300, 200], [40, 40], hk, d, page, dt(dtype), capacity=512)
+    batch = c.make(c.lens, c.starts, 40, 320)  # 320 rows a sequence, 320 tokens
+    g = t.Generator(device="cuda").manual_seed(9)
+    q = t.randn((rows, hk * group, d), generator=g, device="cuda").to(dt(dtype))
+    out, lse = t.zeros_like(q), t.zeros((rows, hk * group), device="cuda")
+    acc, acc_out = t.rand((2, hk, c.per * page), generator=g, device="cuda"), t.zeros((2, hk, c.per * page), device="cuda")
+    ws = t.empty(bqe.rfpx_attn_workspace_bytes(c.cache, batch, hk * group, rows), dtype=t.uint8, device="cuda")
+
+    def step(out, lse, acc_out, ws=None):
+        bqe.rfpx_attn_forward(c.cache, batch, q, out=out, lse=lse, ws=ws)
+        bqe.rfpx_attn_weights(c.cache, batch, q, lse, acc, 0.5, acc_out=acc_out)
+
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        step(out, lse, acc_out, ws)
+    t.cuda.current_stream().wait_stream(side)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        step(out, lse, acc_out, ws)
+    values = c.values()
+    for lens, starts in (([300, 200], [0, 40, 80]), ([250, 33], [0, 40, 73]), ([64, 80], [0, 3, 80]), ([31, 0], [0, 64, 64]),
+                         ([300, 200], [0, 40, 80])):
+        batch.lens.copy_(t.tensor(lens, dtype=t.int32))
+        batch.starts.copy_(t.tensor(starts, dtype=t.int32))
+        for x in (out, lse, acc_out):
+            x.fill_(3)
+        graph.replay()
+        o2, z2, a2 = t.full_like(out, 3), t.full_like(lse, 3), t.full_like(acc_out, 3)
+        step(o2, z2, a2)
+        t.cuda.synchronize()
+        assert t.equal(out, o2) and t.equal(lse, z2) and t.equal(acc_out, a2), lens
+        assert bool((out[starts[-1]:] == 3).all())
+        c.lens, c.starts, c.cols, c.rows = lens, starts, [b - a for a, b in zip(starts, starts[1:])], starts[-1]
+        c.values = lambda: [(k[:n], v[:n]) for (k, v), n in zip(values, lens)]
+        ref = attend64(c, q, d ** -0.5)
+        check_out(out, ref, dt(dtype), slice(0, c.rows))
+        check_lse(lse, ref, slice(0, c.rows))
+        check_weights(c, acc_out, acc, 0.5, ref)
+        _ = (q.float() @ q.float().transpose(1, 2)).sum().item()  # eager work between
