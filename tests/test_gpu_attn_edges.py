@@ -406,3 +406,86 @@ def test_captured_weights_of_many_rows(dtype):
         check_lse(lse, ref, slice(0, c.rows))
         check_weights(c, acc_out, acc, 0.5, ref)
         _ = (q.float() @ q.float().transpose(1, 2)).sum().item()  # eager work between
+
+
+# ------------------------------------------------------------- rows and data
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("plan", [0, 65536])
+def test_fewer_rows_than_the_batch_says(plan, dtype):
+    """starts tells of 40 + 30 columns, the tensors end after 50 rows: columns
+    keep their slots, the rest is neither read nor written."""
+    t = torch()
+    hk, heads, d = 2, 16, 64
+    c = Case([200, 90], [40, 30], hk, d, 32, dt(dtype), seed=1, capacity=max(plan, 200))
+    g = t.Generator(device="cuda").manual_seed(8)
+    batch = c.planned(plan)
+    q = (t.randn((70, heads, d), generator=g, device="cuda") * 1.3).to(dt(dtype))
+    whole, zw = t.zeros_like(q), t.zeros((70, heads), device="cuda")
+    bqe.rfpx_attn_forward(c.cache, batch, q, out=whole, lse=zw)
+    out, z = t.full_like(q, 7.0), t.full((70, heads), 7.0, device="cuda")
+    bqe.rfpx_attn_forward(c.cache, batch, q[:50], out=out[:50], lse=z[:50])
+    assert t.equal(out[:50], whole[:50]) and t.equal(z[:50], zw[:50])
+    assert bool((out[50:] == 7).all()) and bool((z[50:] == 7).all())
+    # weights of the rows that are there, by both kernels: the others' lse says that they see nothing
+    zw[50:] = -float("inf")
+    for kernel in ("few", "many"):
+        b = weights_batch(c, kernel, heads // hk)
+        acc = t.rand((2, hk, c.per * 32), generator=g, device="cuda")
+        a = bqe.rfpx_attn_weights(c.cache, b, q, zw, acc, acc_out=t.zeros_like(acc))
+        assert t.equal(bqe.rfpx_attn_weights(c.cache, b, q[:50], z[:50], acc, acc_out=t.zeros_like(acc)), a)
+    # append and unpack
+    k = t.randn((70, hk, d), generator=g, device="cuda").to(dt(dtype))
+    before, _ = bqe.rfpx_kv_unpack(c.cache, c.batch, 70)
+    bqe.rfpx_kv_append(c.cache, c.batch, k[:50], k[:50])
+    got, _ = bqe.rfpx_kv_unpack(c.cache, c.batch, 70)
+    want = bqe.rfpx_unpack(4, bqe.rfpx_pack(4, k[:50].float().reshape(-1, d)), 50 * hk, d).view(50, hk, d)
+    assert t.equal(got[:50], want) and t.equal(got[50:], before[50:])
+    short = t.full_like(got, 5.0)
+    bqe.rfpx_kv_unpack(c.cache, c.batch, 50, short[:50], short[:50].clone())
+    assert t.equal(short[:50], got[:50]) and bool((short[50:] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("hk,heads,d,cols,plan", PATHS)
+def test_bad_queries_reach_no_other_row(hk, heads, d, cols, plan, dtype):
+    """A query of NaN and one of infinities among ordinary ones: NaN for
+    themselves, and the rows beside them within their bounds."""
+    t = torch()
+    cols = max(cols, 3)
+    c = Case([300], [cols], hk, d, 64, dt(dtype), seed=d, capacity=max(plan, 300))
+    g = t.Generator(device="cuda").manual_seed(4)
+    q = (t.randn((cols, heads, d), generator=g, device="cuda") * 1.3).to(dt(dtype))
+    q[0, 0, 5], q[1, 1, :] = float("nan"), float("inf")
+    z = t.zeros((cols, heads), device="cuda")
+    out = bqe.rfpx_attn_forward(c.cache, c.planned(plan), q, lse=z)
+    assert bool(out[0, 0].isnan().all()) and bool(out[1, 1].isnan().all()) and bool(z[0, 0].isnan()) and bool(z[1, 1].isnan())
+    few = 2 if hk > 2 else hk  # kv heads: the plain form takes its time
+    (k, v), = c.values()
+    h = few * heads // hk
+    c.hk, c.values = few, lambda: [(k[:, :few], v[:, :few])]
+    clean = q[:, :h].clone()
+    clean[0, 0], clean[1, 1] = 0, 0
+    ref = attend64(c, clean, d ** -0.5)
+    out, z = out[:, :h].clone(), z[:, :h].clone()
+    for i in (0, 1):
+        out[i, i], z[i, i] = t.from_numpy(ref["out"][i, i]).to(out), float(ref["lse"][i, i])
+    check_out(out, ref, dt(dtype), slice(0, cols))
+    check_lse(z, ref, slice(0, cols))
+
+
+def test_negative_lengths_are_none():
+    t = torch()
+    c = Case([40, 33], [2, 2], 2, 64, 32, t.bfloat16)
+    b = c.make([-5, -2 ** 31], c.starts, 2, 40)
+    q = t.randn((4, 4, 64), device="cuda").to(t.bfloat16)
+    z = t.zeros((4, 4), device="cuda")
+    before = c.cache.pool.clone()
+    bqe.rfpx_kv_append(c.cache, b, q[:, :2], q[:, :2])
+    assert t.equal(c.cache.pool, before)
+    assert bool((bqe.rfpx_attn_forward(c.cache, b, q, lse=z) == 0).all()) and bool((z == -float("inf")).all())
+    acc = t.rand((2, 2, 64), device="cuda")
+    start, pos = acc.clone(), t.zeros((2, 2, 64), dtype=t.int32, device="cuda")
+    bqe.rfpx_attn_weights(c.cache, b, q, z, acc, 0.5)
+    _, _, lens = bqe.rfpx_kv_evict(c.cache, b, 1, 0, acc, pos)
+    assert t.equal(acc, start) and lens.tolist() == [0, 0] and t.equal(c.cache.pool, before)
