@@ -412,7 +412,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
     floatx4 acc[RT][NB][2], l[RT];
     Offsets<NB, RT> offs;
     // l is the sum of the numerators as they enter the second product, the
-    // output's denominator; exact the one before bf16 rounding, for lse
+    // output's denominator (so that rounding them to bf16 cancels where one
+    // token has the weight); exact the one before bf16 rounding, for lse
     // mx: raw maximum; a score above thr moves it; numerators are 2^(s sc -
     // base), with a wide base against 0 and mx taken off s before
     float mx[RT], thr[RT], base[RT], exact[RT];
@@ -750,8 +751,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
 // waves, 32 rows each, decodes 64 tokens at a time to exact bf16 values in
 // LDS, in the order in which the 32x32x16 matrix instruction's operands are
 // read (16 bytes a lane, adjacent lanes adjacent), while it computes the 64
-// before.  The offset comes off in the decoding (one dot instruction a value:
-// word * 1 + other * 0 - offset), so no product is spent on it.  Lane (row m
+// before.  The offset comes off in the decoding (one mixed-precision fma a
+// value, exact_pair), so no product is spent on it.  Lane (row m
 // = lane & 31, h = lane >> 5) holds of its row the scores of tokens 8 j + 4 h
 // + i (i < 4, j < 4) of 32, and the second product takes j = 2 s and 2 s + 1
 // as its step s from that very lane.
@@ -927,7 +928,10 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[b][i] = 0.f;
-    float mx = kNegInf, base = 0.f, thr = kNegInf, sum = 0.f;  // as in k_attn
+    // as in k_attn; sum is of the numerators before bf16 rounding, the output's
+    // denominator and lse's: one of the rounded ones besides would cost a
+    // vector instruction a score more
+    float mx = kNegInf, base = 0.f, thr = kNegInf, sum = 0.f;
     const float room = fminf(kChunkRoom / a.sc, 3.0e38f);  // finite, as in k_attn
     uint32_t poison = 0;
 
@@ -1418,7 +1422,7 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightA
       const uint32_t u = __float_as_uint(v1[0]);
       const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
       const int i = ms_index<16>(m & 15);
-      wave_fence();
+      wave_fence();  // the sums lie over the stage, which lanes of this wave have just read
       if (m < 16)
         red(wave)[8 * (i >> 2) + 4 * h + (i & 3)] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
     }

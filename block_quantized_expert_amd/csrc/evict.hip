@@ -6,10 +6,11 @@
 // no slot is both read and written, so that all moves run at once, in place.
 //
 // Two launches.  k_evict_select, a workgroup for each (sequence, kv head):
-// every slot's worth becomes one whole number (32 bits, larger is better;
-// in registers up to 32768 slots), a radix selection finds the number of the keep-th best (eight bits a pass,
-// a histogram in LDS), and one ordered pass over the slots lists the slots
-// that go and the slots that move.  k_evict_move: sixteen lanes a move.
+// every slot's worth becomes one whole number (32 bits, larger is better; in
+// registers up to 32768 slots), a radix selection finds the number of the
+// keep-th best (eight bits a pass, a histogram in LDS), and one ordered pass
+// over the slots lists the slots that go and the slots that move.
+// k_evict_move: sixteen lanes a move.
 #include "rfpx_attn.hpp"
 
 namespace rfpx {

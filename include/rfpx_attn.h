@@ -100,7 +100,8 @@ size_t rfpx_kv_pool_bytes(int n_kv_heads, int head_dim, int page_tokens, int n_p
  *   z = x / sqrt(mean(x^2) + eps) * weight        (weight NULL: z = x)
  *   (z_a, z_b) -> (z_a cos t - z_b sin t, z_a sin t + z_b cos t)
  * for the pairs of rope, t = positions[row] * inv_freq, the angle reduced in
- * 64 bits (rope NULL: none).  All in fp32, rounded once into q_out and k_out
+ * 64 bits (rope NULL: none).  All in fp32 (the sum of the squares too: values
+ * past 2^60 are out of its range), rounded once into q_out and k_out
  * (fp32 or bf16 per otype), which may be q and k themselves with the same
  * stride and type.  A row of negative position is padding: left as it was.
  * q or k may be absent (NULL with 0 heads).  head_dim 64, 128 or 256;
@@ -145,10 +146,14 @@ size_t rfpx_attn_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b,
  * q_stride and out_stride elements apart; lse_dev NULL or fp32 [n_rows]
  * [n_heads].  A column that sees nothing gets out = 0, lse = -inf.  The
  * cache's values enter the products exactly.  bf16 q enters as it is, and its
- * softmax numerators as bf16; fp32 q and its numerators enter as three bf16
- * terms, which lose nothing.  Sums and statistics are fp32, in a fixed order:
- * out is the same bit for bit from run to run (of one plan: max_cols and
- * max_len decide how a sequence is split).  scale > 0, finite.  out may not overlap q. */
+ * softmax numerators rounded to bf16 (2^-8 of each at most); they are divided
+ * by the sum of the rounded ones, or in plans of many rows of the unrounded
+ * ones, so that out differs within that bound from plan to plan.  fp32 q and
+ * its numerators enter as three bf16 terms, 24 bits: what is lost is lost in
+ * the fp32 sums, of terms up to four times their result.  Sums and statistics
+ * are fp32, in a fixed order: out is the same bit for bit from run to run (of
+ * one plan: max_cols and max_len decide how a sequence is split).  Scores may
+ * be of any finite size.  scale > 0, below 1e30.  out may not overlap q. */
 rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q_dev,
                               long long q_stride, int xtype, int n_heads, int n_rows, float scale,
                               void *out_dev, long long out_stride, float *lse_dev, void *ws_dev,
@@ -158,8 +163,9 @@ rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, co
  * step's columns that see the slot and the query heads of the kv head, for
  * the slots below lens[b]; others are left as they were.  acc and acc_out
  * [n_seqs][n_kv_heads][pages_per_seq * page_tokens] fp32, may be the same.
- * q, scale and lse as rfpx_attn_forward was given and gave them.  Sums in a
- * fixed order. */
+ * q, scale and lse as rfpx_attn_forward was given and gave them.  lse is an
+ * fp32 number: a weight is off by about 2^-22 |lse| of itself, and from |lse|
+ * = 2^20 on says little.  Sums in a fixed order. */
 rfpx_status rfpx_attn_weights(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q_dev,
                               long long q_stride, int xtype, int n_heads, int n_rows, float scale,
                               const float *lse_dev, float decay, const float *acc_dev,
