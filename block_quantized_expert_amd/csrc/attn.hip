@@ -23,13 +23,13 @@
 //
 // Bases.  Maxima are kept as the products give them (raw), so that comparing
 // them rounds nothing.  What a row's numerators stand against is base =
-// fl(maximum * sc): 2^(s sc - base) is one fma a score, and what base was
-// rounded by (half a step of it at most) is a factor that the sums, the joins
-// and lse share.  At a base of 2^31 that factor can be 2^64, so from |base| =
-// kWide on numerators are 2^((s - maximum) sc) instead, 1 at the maximum
-// itself, and joins take the same difference.  A wave with such a row has a
-// threshold of -inf, so that all its tiles come by the block where maxima move,
-// and other waves pay nothing for it.
+// fl(maximum * sc): 2^(s sc - base) is one fma a score.  What base was rounded
+// by (half a step of it at most) is a factor that their sums share; a wave
+// takes it out of them at its end, so that joins and lse see sums against the
+// maximum itself.  At a base of 2^31 that factor can be 2^64, so from |base| =
+// kWide on numerators are 2^((s - maximum) sc) to begin with.  A wave with such
+// a row has a threshold of -inf, so that all its tiles come by the block where
+// maxima move, and other waves pay nothing for it.
 #include "rfpx_attn.hpp"
 
 namespace rfpx {
@@ -93,12 +93,19 @@ __device__ __forceinline__ float base_step(float from, float to, float sc) {
   const float base = to * sc, was = from * sc;
   return fabsf(base) < kWide ? was - base : (from - to) * sc;
 }
-
+// What base was rounded by; 0 where numerators stand against the maximum
+// itself, for which base is 0.
+__device__ __forceinline__ float rounded_by(float top, float base, float sc) {
+  return base == 0.f ? 0.f : -fmaf(top, sc, -base);
+}
+// From one raw maximum to another, no smaller, as a power of two (to 0 while
+// nothing has been seen).
+__device__ __forceinline__ float down_to(float from, float to, float sc) {
+  return (from - (to == kNegInf ? 0.f : to)) * sc;
+}
 // Log of a row's sum `ex` of numerators against its raw maximum.
 __device__ __forceinline__ float lse_of(float top, float ex, float sc) {
-#pragma clang fp contract(off)
-  const float base = top * sc;
-  return (base + log2f(ex)) * 0.69314718055994531f;
+  return fmaf(top, sc, log2f(ex)) * 0.69314718055994531f;
 }
 
 // N dwords from p (aligned to their size, at most 16 bytes a load).
@@ -586,12 +593,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
     for (int t = 0; t < RT; ++t) {
       poison[t] |= __shfl_xor(poison[t], 16);
       poison[t] |= __shfl_xor(poison[t], 32);
-      const float z = VX == 1 ? cross_row_sum(exact[t]) : l[t][0];
-      if (g == 0) {
-        sh_ml[wave][16 * t + m][0] = mx[t];
-        sh_ml[wave][16 * t + m][1] = l[t][0];
-        sh_ml[wave][16 * t + m][2] = z;
-      }
+      if (VX == 1) exact[t] = cross_row_sum(exact[t]);
+      if (g == 0) sh_ml[wave][16 * t + m][0] = mx[t];
     }
     __syncthreads();
 #pragma unroll
@@ -599,7 +602,12 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       float top = kNegInf;
 #pragma unroll
       for (int w = 0; w < W; ++w) top = fmaxf(top, sh_ml[w][16 * t + m][0]);
-      const float f = __builtin_amdgcn_exp2f(base_step(mx[t], top, a.sc));
+      const float f = __builtin_amdgcn_exp2f(down_to(mx[t], top, a.sc) +
+                                             rounded_by(mx[t], base[t], a.sc));
+      if (g == 0) {
+        sh_ml[wave][16 * t + m][1] = l[t][0] * f;
+        sh_ml[wave][16 * t + m][2] = (VX == 1 ? exact[t] : l[t][0]) * f;
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float h = (poison[t] >> b) & 1 ? __builtin_nanf("") : f;
@@ -620,9 +628,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
           floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            const float f = __builtin_amdgcn_exp2f(base_step(sh_ml[w][16 * t + row][0], rt, a.sc));
-            sum += sh_ml[w][16 * t + row][1] * f;
-            ex += sh_ml[w][16 * t + row][2] * f;
+            sum += sh_ml[w][16 * t + row][1];
+            ex += sh_ml[w][16 * t + row][2];
             o += *reinterpret_cast<const floatx4 *>(&sh_o[w][row][d]);
           }
           const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
@@ -686,7 +693,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
     for (int s = g; s < a.splits; s += NG) {
       const float4 w = ml[s];
       if (w.x == kNegInf && w.y == 0.f) continue;  // no tokens: its numerators were not written
-      const float f = __builtin_amdgcn_exp2f(base_step(w.x, top, a.sc));
+      const float f = __builtin_amdgcn_exp2f(down_to(w.x, top, a.sc));
       sum += w.y * f;
       ex += w.z * f;
       o += *reinterpret_cast<const floatx4 *>(a.part + (rh * a.splits + s) * D + d) * f;
@@ -735,7 +742,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join_few(AttnArgs a) {
       const float4 w = ml[s];
       floatx4 v = *reinterpret_cast<const floatx4 *>(a.part + (rh * a.splits + s) * D + d);
       const bool none = w.x == kNegInf && w.y == 0.f;
-      const float f = none ? 0.f : __builtin_amdgcn_exp2f(base_step(w.x, top, a.sc));
+      const float f = none ? 0.f : __builtin_amdgcn_exp2f(down_to(w.x, top, a.sc));
       if (none) v = floatx4{0.f, 0.f, 0.f, 0.f};
       sum += w.y * f;
       ex += w.z * f;
@@ -1116,7 +1123,9 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     if (live) {
       const size_t rh = (size_t)(s0 + col) * a.heads + hd;
       const bool empty = mx == kNegInf && sum == 0.f;
-      const float inv = a.splits > 1 ? 1.f : empty ? 0.f : 16.f / sum;
+      const float whole = __builtin_amdgcn_exp2f(rounded_by(mx, base, a.sc));
+      const float inv = a.splits > 1 ? whole : empty ? 0.f : 16.f / sum;
+      sum *= whole;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float f = (poison >> b) & 1 ? __builtin_nanf("") : inv;
