@@ -352,7 +352,7 @@ __device__ __forceinline__ void add_values(const VTile<NB> &v, const u32x4v (&p)
 // What bounds it: instruction issue, then HBM.  A wave's 32-token tile of a
 // head of 128 is 4352 bytes, about 290 vector instructions (two thirds of
 // them the two decodes) and, at 32 rows, 40 matrix instructions.  Measured on
-// an MI355X: 5 columns of 32 heads over 131071 tokens (143 MB) 38 us, 3.8
+// an MI355X: 5 columns of 32 heads over 131071 tokens (143 MB) 37 us, 3.8
 // TB/s, 79% of a large copy's rate; 64 sequences of up to 4096 tokens 4.0
 // TB/s; one column over 1021 tokens 11.7 us, a chain of loads.  Tried and not
 // kept: 256, 768, 1024 and 2048 workgroups instead of 512 (22, 15, 12 and 33%
@@ -871,11 +871,12 @@ __device__ __forceinline__ void chunk_decode(const ChunkRaw<NB> &r, int wave, in
 // next is decoded into the other.
 //
 // Measured on an MI355X: 2048 columns of 32 heads of 128 at the end of 8192
-// tokens 271 us, 889 TFLOP/s, 77% of a library's 8192^3 bf16 product (1158);
-// matrix units a third busy, vector units 45%.  Tried and not kept, all
-// within 3%: operands read six products ahead, both halves' score chains in
-// turn, pages read three tiles ahead, rows written through LDS; the scores of
-// a tile beside the exps of the tile before it spills (355 us).
+// tokens 276 us, 871 TFLOP/s, 77% of a library's 8192^3 bf16 product (1126); by
+// its counters matrix units 41% busy, vector instructions issuing 56% of the
+// time.  Tried and not kept, all within 3%: operands read six products ahead,
+// both halves' score chains in turn, pages read three tiles ahead, rows written
+// through LDS; the scores of a tile beside the exps of the tile before it
+// spills (355 us).
 template <int NB>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   constexpr int D = 32 * NB;
@@ -1178,7 +1179,7 @@ __device__ __forceinline__ float row_sums(const float (&v)[8], int lane) {
 // Workgroup (x, y, z): kv head x of sequence z, 32-token tiles shared out over
 // the waves of all y.  The rows' operands stand in LDS, QB tiles of 16 at a
 // time, while the keys pass, the next tile's loads in flight.  Measured: 4
-// sequences of up to 16384 tokens, 4 columns of 32 heads, 13.7 us.
+// sequences of up to 16384 tokens, 4 columns of 32 heads, 14.1 us.
 template <int NB, int VX>
 __global__ __launch_bounds__(kThreads) void k_attn_weights(WeightArgs a) {
   constexpr int D = 32 * NB, QB = VX == 1 ? 4 : 2;
@@ -1285,7 +1286,7 @@ __device__ __forceinline__ void wave_fence() {
 // LDS (pieces of 16 bytes, a row's exchanged by its number, so that both sides
 // are free of bank conflicts).  Each lane reading its own row from memory was
 // bound by a cache line a lane: 64 us.  The waves' sums meet in LDS.
-// Measured: 2048 columns of 32 heads of 128 over their own 2048 tokens 48 us.
+// Measured: 2048 columns of 32 heads of 128 over their own 2048 tokens 47 us.
 template <int NB, int VX>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_weights_chunk(WeightArgs a) {
   constexpr int D = 32 * NB, KS = 2 * NB;
