@@ -1,5 +1,5 @@
-"""Python binding of librfpx (include/rfpx.h and include/rfpx_attn.h):
-argument marshalling only.
+"""Python binding of librfpx (include/rfpx.h, include/rfpx_attn.h and
+include/rfpx_verify.h): argument marshalling only.
 
 Every computation runs in the HIP kernels of librfpx.so; PyTorch supplies
 device memory and the current stream.  The functions carry the C names and
@@ -49,6 +49,13 @@ ATTN_SYMBOLS = (
     "rfpx_kv_evict_workspace_bytes", "rfpx_kv_evict",
 )
 RFPX_ROPE_HALF, RFPX_ROPE_PAIRS = 0, 1
+
+# ... and include/rfpx_verify.h
+VERIFY_SYMBOLS = (
+    "rfpx_tree_masks", "rfpx_attn_tree_forward", "rfpx_sample_workspace_bytes", "rfpx_sample",
+    "rfpx_tree_accept", "rfpx_kv_commit",
+)
+TREE_COLS_MAX = 1024
 
 
 class RfpxError(RuntimeError):
@@ -149,6 +156,12 @@ def lib():
             "rfpx_attn_weights": (I, [KP, BP, P, L, I, I, I, F, P, F, P, P, P]),
             "rfpx_kv_evict_workspace_bytes": (S, [KP, BP, I]),
             "rfpx_kv_evict": (I, [KP, BP, I, I, P, P, P, P, P, P, S, P]),
+            "rfpx_tree_masks": (I, [BP, I, P, P, I, P, P, P]),
+            "rfpx_attn_tree_forward": (I, [KP, BP, P, L, I, I, I, F, P, I, P, L, P, P, S, P]),
+            "rfpx_sample_workspace_bytes": (S, [I, I, I]),
+            "rfpx_sample": (I, [P, L, I, I, I, P, P, P, P, P, P, P, P, S, P]),
+            "rfpx_tree_accept": (I, [BP, I, P, P, P, I, P, P, P, P, P]),
+            "rfpx_kv_commit": (I, [KP, BP, I, P, P, P, P, P]),
         })
         for name, (res, args) in sig.items():
             fn = getattr(l, name)
@@ -784,6 +797,147 @@ def rfpx_kv_evict(cache: KvCache, batch: KvBatch, keep: int, recent: int, acc, p
         _flat("lens_out", lens_out, torch.int32, (batch.n_seqs,)), ws.data_ptr(),
         ws.numel() * ws.element_size(), _raw_stream(torch, dev, stream)))
     return acc_out, pos_out, lens_out
+
+
+# ----------------------------------------------- verification of drafts
+#
+# A step whose columns are a tree of drafted tokens (include/rfpx_verify.h):
+# masks and positions from parents, attention over the context and a column's
+# own ancestors, tokens drawn from the logits, the drafts that they confirm,
+# and the cache made a plain sequence of those again.
+
+def rfpx_tree_masks(batch: KvBatch, parents, base=None, mask_words: Optional[int] = None, masks=None,
+                    positions=None, stream=None):
+    """Ancestor bits (int32 [rows][mask_words], as many words as max_cols
+    needs) and positions (int32 [rows]) of a tree's columns from parents (int32
+    [rows], a column of the same sequence or -1).  base: int32 [seqs], the
+    position of column 0 (None: its slot).  Returns (masks, positions)."""
+    import torch
+    rows = parents.shape[0]
+    if masks is not None:
+        mask_words = masks.shape[1]
+    elif mask_words is None:
+        mask_words = max(1, (batch.max_cols + 31) // 32)
+    if masks is None:
+        masks = _new(parents, (rows, mask_words), torch.int32, stream)
+    if positions is None:
+        positions = _new(parents, (rows,), torch.int32, stream)
+    dev = _same_device(torch, batch.lens, parents, base, masks, positions)
+    i32 = torch.int32
+    _check("rfpx_tree_masks", lib().rfpx_tree_masks(
+        batch.ref, rows, _flat("parents", parents, i32, (rows,)),
+        _flat("base", base, i32, (batch.n_seqs,)), mask_words,
+        _flat("masks", masks, i32, (rows, mask_words)),
+        _flat("positions", positions, i32, (rows,)), _raw_stream(torch, dev, stream)))
+    return masks, positions
+
+
+def rfpx_attn_tree_forward(cache: KvCache, batch: KvBatch, q, masks, scale: Optional[float] = None,
+                           out=None, lse=None, ws=None, stream=None):
+    """rfpx_attn_forward for a tree: every column sees the context and those of
+    the step's columns that its masks (int32 [rows][words], bit j: column j)
+    name."""
+    import torch
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [rows][heads][{cache.head_dim}]")
+    rows, heads, d = q.shape
+    if masks.dim() != 2:
+        raise ValueError("masks must be [rows][words]")
+    words = masks.shape[1]
+    if out is None:
+        out = _new(q, q.shape, q.dtype, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if ws is None:
+        n = rfpx_attn_workspace_bytes(cache, batch, heads, rows)
+        if n == 0:
+            raise RfpxError("rfpx_attn_workspace_bytes", -2, lib().rfpx_last_error().decode())
+        ws = _new(q, n, torch.uint8, stream)
+    dev = _same_device(torch, cache.pool, batch.lens, q, masks, out, lse, ws)
+    qp, qs = _rows("q", q)
+    op, os_ = _rows("out", out)
+    _check("rfpx_attn_tree_forward", lib().rfpx_attn_tree_forward(
+        cache.ref, batch.ref, qp, qs, _xtype(q), heads, rows,
+        d ** -0.5 if scale is None else scale, _flat("masks", masks, torch.int32, (rows, words)),
+        words, op, os_, _flat("lse", lse, torch.float32, (rows, heads)), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(torch, dev, stream)))
+    return out
+
+
+def rfpx_sample_workspace_bytes(rows: int, vocab: int, dtype) -> int:
+    import torch
+    return lib().rfpx_sample_workspace_bytes(
+        rows, vocab, RFPX_X_BF16 if dtype == torch.bfloat16 else RFPX_X_F32)
+
+
+def rfpx_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
+                probs=None, ws=None, stream=None):
+    """A token (int32 [rows]) of every row of logits [rows][vocab] (fp32 or
+    bf16, tokens adjacent, rows any distance apart), drawn by u (fp32 [rows], in
+    [0, 1)) from what temperature, top_p, min_p (fp32) and top_k (int32), each
+    [rows] or None, leave of it.  probs (fp32 [rows]), if given, gets the
+    probabilities that they were drawn with."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows][vocab]")
+    rows, vocab = logits.shape
+    if logits.stride(1) != 1 and vocab > 1:
+        raise ValueError("logits: tokens must be adjacent")
+    stride = logits.stride(0) if rows > 1 else vocab
+    if tokens is None:
+        tokens = _new(logits, (rows,), torch.int32, stream)
+    if ws is None:
+        n = rfpx_sample_workspace_bytes(rows, vocab, logits.dtype)
+        if n == 0:
+            raise RfpxError("rfpx_sample_workspace_bytes", -2, lib().rfpx_last_error().decode())
+        ws = _new(logits, n, torch.uint8, stream)
+    dev = _same_device(torch, logits, u, temperature, top_k, top_p, min_p, tokens, probs, ws)
+    f32, i32, shape = torch.float32, torch.int32, (rows,)
+    _check("rfpx_sample", lib().rfpx_sample(
+        logits.data_ptr(), stride, _xtype(logits), rows, vocab, _flat("u", u, f32, shape),
+        _flat("temperature", temperature, f32, shape), _flat("top_k", top_k, i32, shape),
+        _flat("top_p", top_p, f32, shape), _flat("min_p", min_p, f32, shape),
+        _flat("tokens", tokens, i32, shape), _flat("probs", probs, f32, shape), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(torch, dev, stream)))
+    return tokens
+
+
+def rfpx_tree_accept(batch: KvBatch, parents, tokens, drawn, path=None, counts=None,
+                     next_tokens=None, lens_out=None, stream=None):
+    """The drafts that the drawn tokens confirm: path (int32 [seqs][path_cols],
+    columns, then -1; path_cols is max_cols unless path is given), counts, the
+    token drawn at the last of them, and the lengths that the sequences then
+    have.  parents, tokens and drawn are int32 [rows].  Returns (path, counts,
+    next_tokens, lens_out)."""
+    import torch
+    rows, n, i32 = parents.shape[0], batch.n_seqs, torch.int32
+    if path is None:
+        path = _new(parents, (n, max(1, batch.max_cols)), i32, stream)
+    counts = _new(parents, (n,), i32, stream) if counts is None else counts
+    next_tokens = _new(parents, (n,), i32, stream) if next_tokens is None else next_tokens
+    lens_out = _new(parents, (n,), i32, stream) if lens_out is None else lens_out
+    cols = path.shape[1]
+    dev = _same_device(torch, batch.lens, parents, tokens, drawn, path, counts, next_tokens, lens_out)
+    _check("rfpx_tree_accept", lib().rfpx_tree_accept(
+        batch.ref, rows, _flat("parents", parents, i32, (rows,)), _flat("tokens", tokens, i32, (rows,)),
+        _flat("drawn", drawn, i32, (rows,)), cols, _flat("path", path, i32, (n, cols)),
+        _flat("counts", counts, i32, (n,)), _flat("next_tokens", next_tokens, i32, (n,)),
+        _flat("lens_out", lens_out, i32, (n,)), _raw_stream(torch, dev, stream)))
+    return path, counts, next_tokens, lens_out
+
+
+def rfpx_kv_commit(cache: KvCache, batch: KvBatch, path, counts, acc=None, pos=None, stream=None) -> None:
+    """Move the columns that rfpx_tree_accept found (path, counts) to the first
+    slots of the step, keys and values and, where given, acc (fp32) and pos
+    (int32), [seqs][kv heads][slots]; lens is still that of the step."""
+    import torch
+    n, cols = batch.n_seqs, path.shape[1]
+    dev = _same_device(torch, cache.pool, batch.lens, path, counts, acc, pos)
+    slots = _slots(cache, batch)
+    _check("rfpx_kv_commit", lib().rfpx_kv_commit(
+        cache.ref, batch.ref, cols, _flat("path", path, torch.int32, (n, cols)),
+        _flat("counts", counts, torch.int32, (n,)), _flat("acc", acc, torch.float32, slots),
+        _flat("pos", pos, torch.int32, slots), _raw_stream(torch, dev, stream)))
 
 
 # ------------------------------------------------------------ measurement

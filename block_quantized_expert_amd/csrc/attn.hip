@@ -30,6 +30,11 @@
 // kWide on numerators are 2^((s - maximum) sc) to begin with.  A wave with such
 // a row has a threshold of -inf, so that all its tiles come by the block where
 // maxima move, and other waves pay nothing for it.
+//
+// A tree's columns see the context and, of the step's own slots, those that
+// bits name (TREE): in the tiles behind the context a row's 32 tokens are one
+// word, shifted out of its mask; everywhere else the two are one code.
+#include "../../include/rfpx_verify.h"
 #include "rfpx_attn.hpp"
 
 namespace rfpx {
@@ -59,7 +64,28 @@ struct AttnArgs {
   long long q_stride, out_stride;
   int xtype, heads, group, n_rows, splits, row_blocks;
   float sc;       // 16 * scale * log2(e)
+  const uint32_t *masks;  // [rows][mask_words]; null: every column sees those before it
+  int mask_words;
 };
+
+// The slots t0 .. t0 + 31 that a tree's column sees, a bit each: those before
+// `context`, and behind it those that its mask names, below `end`.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *mask, int words, int context, int t0,
+                                              int end) {
+  const int off = t0 - context;
+  uint32_t bits = 0;
+  if (off <= -32) {
+    bits = 0xFFFFFFFFu;
+  } else if (off < 0) {
+    bits = (words > 0 ? mask[0] << -off : 0u) | ((1u << -off) - 1u);
+  } else {
+    const int w = off >> 5, sh = off & 31;
+    if (w < words) bits = mask[w] >> sh;
+    if (sh && w + 1 < words) bits |= mask[w + 1] << (32 - sh);
+  }
+  const int seen = end - t0;
+  return seen >= 32 ? bits : seen <= 0 ? 0u : bits & ((1u << seen) - 1u);
+}
 
 __device__ __forceinline__ floatx4 mfma(const u32x4v &a, const u32x4v &b, const floatx4 &c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -362,7 +388,7 @@ __device__ __forceinline__ void add_values(const VTile<NB> &v, const u32x4v (&p)
 // Workgroup (x, y, z): kv head and row block x, split y, sequence z.  A row
 // block is 16 RT of the sequence's rows (column, head of the group); its W waves
 // share out the split's 32-token tiles and join their sums in LDS.
-template <int NB, int VX, int RT, int W>
+template <int NB, int VX, int RT, int W, bool TREE>
 __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   constexpr int D = 32 * NB;
   constexpr int LD = D + 4;
@@ -385,9 +411,12 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   const int32_t *table = a.v.table + (size_t)seq * a.v.pages_per_seq;
 
   for (long long r0 = (long long)rb0 * (16 * RT); r0 < rows; r0 += (long long)a.row_blocks * (16 * RT)) {
-    int vis[RT];
+    int vis[RT];  // (TREE: a column's row, -1 where its slot is negative)
     int first_vis, last_vis;
-    {
+    if constexpr (TREE) {
+      first_vis = max(0, len - n_all);
+      last_vis = len;
+    } else {
       const int c0 = (int)(r0 / a.group);
       long long e = r0 + 16 * RT - 1;
       if (e >= rows) e = rows - 1;
@@ -401,7 +430,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       const bool live = r < rows;
       if (!live) r = rows - 1;
       const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
-      vis[t] = min(len, max(0, len - n_all + col + 1));
+      vis[t] = TREE ? (len - n_all + col < 0 ? -1 : s0 + col)
+                    : min(len, max(0, len - n_all + col + 1));
       if (wave == t) {
         QTile<NB, VX> q;
         load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q);
@@ -499,13 +529,25 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
         // some row does not see some token: its score is -inf, and what its
         // scale says must not reach any row
         const int lim = held ? len : 0;
+        uint32_t bits[RT];  // what each row sees of the lane's tokens 16 u + i
+        if constexpr (TREE) {
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            bits[t] = vis[t] < 0 ? 0u
+                                 : tree_bits(a.masks + (size_t)vis[t] * a.mask_words, a.mask_words,
+                                             len - n_all, t0, lim) >> (4 * g);
+        }
+        const auto hidden = [&](int t, int u, int i) {
+          if constexpr (TREE) return !((bits[t] >> (16 * u + i)) & 1u);
+          else return t0 + 16 * u + 4 * g + i >= min(vis[t], lim);
+        };
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (t0 + 16 * u + 4 * g + i >= min(vis[t], lim)) s[t][u][i] = kNegInf;
+              if (hidden(t, u, i)) s[t][u][i] = kNegInf;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -520,7 +562,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
                 v.s[u][at >> 2] &= ~(0xFFu << (8 * (at & 3)));
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                  if (bad && slot < min(vis[t], lim)) poison[t] |= 1u << b;
+                  if (bad && !hidden(t, u, i)) poison[t] |= 1u << b;
               }
             }
           }
@@ -877,7 +919,7 @@ __device__ __forceinline__ void chunk_decode(const ChunkRaw<NB> &r, int wave, in
 // both halves' score chains in turn, pages read three tiles ahead, rows written
 // through LDS; the scores of a tile beside the exps of the tile before it
 // spills (355 us).
-template <int NB>
+template <int NB, bool TREE>
 __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   constexpr int D = 32 * NB;
   extern __shared__ __align__(16) uint8_t lds[];
@@ -901,16 +943,18 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
 
   for (long long r0 = (long long)rb0 * kChunkRows; r0 < rows;
        r0 += (long long)a.row_blocks * kChunkRows) {
-    const auto sees = [&](long long r) {  // slots that a row sees
+    const auto sees = [&](long long r) {  // slots that a row sees (TREE: may see)
+      if constexpr (TREE) return len;
       if (r >= rows) r = rows - 1;
       return min(len, max(0, len - n_all + (int)(r / a.group) + 1));
     };
-    const int first_vis = sees(r0), last_vis = sees(r0 + kChunkRows - 1);
+    const int first_vis = TREE ? max(0, len - n_all) : sees(r0);
+    const int last_vis = sees(r0 + kChunkRows - 1);
     long long r = r0 + 32 * wave + m;
     const bool live = r < rows;
     if (!live) r = rows - 1;
     const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
-    const int vis = sees(r);
+    const int vis = TREE && len - n_all + col < 0 ? 0 : sees(r);
     u32x4v q[2 * NB];
     {
       const uint16_t *p = static_cast<const uint16_t *>(a.q) + (size_t)(s0 + col) * a.q_stride +
@@ -998,11 +1042,20 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     const auto hide = [&](int tile, int u, int at, floatx16 &o) {
       const int t0 = tile * kChunkTile + 32 * u;
       const int lim = is_page(page_at(t0)) ? vis : 0;
+      uint32_t in;
+      if constexpr (TREE) {
+        in = tree_bits(a.masks + (size_t)(s0 + col) * a.mask_words, a.mask_words, len - n_all, t0, lim);
+        const uint32_t mine = in >> (4 * h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (t0 + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) o[i] = kNegInf;
-      const int seen = lim - t0;
-      const uint32_t in = seen <= 0 ? 0u : seen >= 32 ? 0xFFFFFFFFu : (1u << seen) - 1u;
+        for (int i = 0; i < 16; ++i)
+          if (!((mine >> (8 * (i >> 2) + (i & 3))) & 1u)) o[i] = kNegInf;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (t0 + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) o[i] = kNegInf;
+        const int seen = lim - t0;
+        in = seen <= 0 ? 0u : seen >= 32 ? 0xFFFFFFFFu : (1u << seen) - 1u;
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         if (*reinterpret_cast<const uint32_t *>(&bad[(at * NB + b) * kChunkWaves + 4 * u]) & in)
@@ -1526,17 +1579,17 @@ rfpx_status check_heads(const char *fn, const rfpx_kv_cache *c, int heads, int n
   return RFPX_OK;
 }
 
-template <int NB>
+template <int NB, bool TREE>
 hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
   const dim3 grid(a.v.hk * p.row_blocks, p.splits, a.v.n_seqs), block(64 * p.waves);
   constexpr int RT = NB == 8 ? 1 : 2;
   constexpr int W1 = NB == 8 ? kWaves : kWavesOne;  // heads of 256 leave no registers for more
   const bool one = p.waves == kWavesOne;
   void (*k)(AttnArgs) =
-      p.chunk               ? k_attn_chunk<NB == 8 ? 4 : NB>
-      : a.xtype == RFPX_X_F32 ? (one ? k_attn<NB, 3, 1, W1> : k_attn<NB, 3, 1, kWaves>)
-      : p.rt == 1           ? (one ? k_attn<NB, 1, 1, W1> : k_attn<NB, 1, 1, kWaves>)
-                            : (one ? k_attn<NB, 1, RT, W1> : k_attn<NB, 1, RT, kWaves>);
+      p.chunk               ? k_attn_chunk<NB == 8 ? 4 : NB, TREE>
+      : a.xtype == RFPX_X_F32 ? (one ? k_attn<NB, 3, 1, W1, TREE> : k_attn<NB, 3, 1, kWaves, TREE>)
+      : p.rt == 1           ? (one ? k_attn<NB, 1, 1, W1, TREE> : k_attn<NB, 1, 1, kWaves, TREE>)
+                            : (one ? k_attn<NB, 1, RT, W1, TREE> : k_attn<NB, 1, RT, kWaves, TREE>);
   const size_t lds =
       p.chunk ? 2 * sizeof(ChunkK<NB>) + 2 * sizeof(ChunkV<NB>) + 2 * NB * kChunkWaves : 0;
   const hipError_t e = launch_k(k, grid, block, lds, s, a);
@@ -1552,29 +1605,13 @@ hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
   return launch_k(j, jg, dim3(kThreads), 0, s, a);
 }
 
-}  // namespace
-}  // namespace rfpx
-
-using namespace rfpx;
-
-extern "C" {
-
-size_t rfpx_attn_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int n_heads,
-                                 int n_rows) {
-  const char *fn = "rfpx_attn_workspace_bytes";
-  if (check_kv(fn, c, b, false) || check_heads(fn, c, n_heads, n_rows, RFPX_X_F32, 1.f)) return 0;
-  const size_t f = attn_plan(c, b, n_heads, n_rows, RFPX_X_F32).total;
-  const size_t h = attn_plan(c, b, n_heads, n_rows, RFPX_X_BF16).total;
-  return f > h ? f : h;
-}
-
-rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,
-                              long long q_stride, int xtype, int n_heads, int n_rows, float scale,
-                              void *out, long long out_stride, float *lse, void *ws,
-                              size_t ws_bytes, void *stream) {
-  const char *fn = "rfpx_attn_forward";
-  rfpx_status st = check_kv(fn, c, b, true);
-  if (st) return st;
+// rfpx_attn_forward, and with masks rfpx_attn_tree_forward.
+rfpx_status attn_forward(const char *fn, const rfpx_kv_cache *c, const rfpx_kv_batch *b,
+                         const void *q, long long q_stride, int xtype, int n_heads, int n_rows,
+                         float scale, const uint32_t *masks, int mask_words, void *out,
+                         long long out_stride, float *lse, void *ws, size_t ws_bytes,
+                         void *stream) {
+  rfpx_status st;
   if ((st = check_heads(fn, c, n_heads, n_rows, xtype, scale))) return st;
   if (n_rows == 0) return RFPX_OK;
   if ((st = check_rows(fn, "q", q, q_stride, n_heads, c->head_dim, xtype))) return st;
@@ -1602,11 +1639,62 @@ rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, co
   a.splits = p.splits;
   a.row_blocks = p.row_blocks;
   a.sc = 16.f * scale * 1.4426950408889634f;
+  a.masks = masks;
+  a.mask_words = mask_words;
   hipStream_t s = (hipStream_t)stream;
-  hipError_t e = c->head_dim == 64    ? launch_attn<2>(p, a, s)
-                 : c->head_dim == 128 ? launch_attn<4>(p, a, s)
-                                      : launch_attn<8>(p, a, s);
+  const int d = c->head_dim;
+  const hipError_t e =
+      masks ? (d == 64    ? launch_attn<2, true>(p, a, s)
+               : d == 128 ? launch_attn<4, true>(p, a, s)
+                          : launch_attn<8, true>(p, a, s))
+            : (d == 64    ? launch_attn<2, false>(p, a, s)
+               : d == 128 ? launch_attn<4, false>(p, a, s)
+                          : launch_attn<8, false>(p, a, s));
   return e == hipSuccess ? RFPX_OK : fail(RFPX_E_HIP, "%s: %s", fn, hipGetErrorString(e));
+}
+
+}  // namespace
+}  // namespace rfpx
+
+using namespace rfpx;
+
+extern "C" {
+
+size_t rfpx_attn_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int n_heads,
+                                 int n_rows) {
+  const char *fn = "rfpx_attn_workspace_bytes";
+  if (check_kv(fn, c, b, false) || check_heads(fn, c, n_heads, n_rows, RFPX_X_F32, 1.f)) return 0;
+  const size_t f = attn_plan(c, b, n_heads, n_rows, RFPX_X_F32).total;
+  const size_t h = attn_plan(c, b, n_heads, n_rows, RFPX_X_BF16).total;
+  return f > h ? f : h;
+}
+
+rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,
+                              long long q_stride, int xtype, int n_heads, int n_rows, float scale,
+                              void *out, long long out_stride, float *lse, void *ws,
+                              size_t ws_bytes, void *stream) {
+  const char *fn = "rfpx_attn_forward";
+  rfpx_status st = check_kv(fn, c, b, true);
+  if (st) return st;
+  return attn_forward(fn, c, b, q, q_stride, xtype, n_heads, n_rows, scale, nullptr, 0, out,
+                      out_stride, lse, ws, ws_bytes, stream);
+}
+
+rfpx_status rfpx_attn_tree_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,
+                                   long long q_stride, int xtype, int n_heads, int n_rows,
+                                   float scale, const uint32_t *masks, int mask_words, void *out,
+                                   long long out_stride, float *lse, void *ws, size_t ws_bytes,
+                                   void *stream) {
+  const char *fn = "rfpx_attn_tree_forward";
+  rfpx_status st = check_kv(fn, c, b, true);
+  if (st) return st;
+  if (mask_words < 1 || mask_words > RFPX_TREE_COLS_MAX / 32)
+    return fail(RFPX_E_SHAPE, "%s: mask_words=%d: must be in [1, %d]", fn, mask_words,
+                RFPX_TREE_COLS_MAX / 32);
+  if (n_rows && !masks) return fail(RFPX_E_ARG, "%s: masks is null", fn);
+  if ((uintptr_t)masks % 4) return fail(RFPX_E_ALIGN, "%s: masks not 4-byte aligned", fn);
+  return attn_forward(fn, c, b, q, q_stride, xtype, n_heads, n_rows, scale, masks, mask_words, out,
+                      out_stride, lse, ws, ws_bytes, stream);
 }
 
 rfpx_status rfpx_attn_weights(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,
