@@ -16,13 +16,22 @@
 // a choice, LDS atomics may have any, and tokens of equal logits weigh the
 // same, so that a place among them is a division.
 //
-// find() narrows: a histogram over 256 bins of the distance from the largest
-// logit, 5 an octave of weight (the row is read for the largest, for the
-// histogram, and once more for the tokens of the bins that the three
-// questions fall into, which go into a list in LDS), then digits of the keys
-// in the list, until at most 64 tokens are left, which one wave ranks, or
-// tokens of one logit.  A list that is too short for its bins (flat rows) is
-// replaced by the row itself.
+// find() narrows: bins of the distance from the largest logit, 10 an octave of
+// weight, then digits of the keys in one bin, until at most 64 tokens are left,
+// which one wave ranks, or tokens of one logit.
+//
+// Rows of up to 32768 logits are a workgroup's each, in registers
+// (k_sample_row).  Longer ones are cut into slices:
+//   k_sample_slices   a workgroup holds its slice in registers: its largest
+//                     logit; and, if the row keeps the first of few, or tokens
+//                     of some weight, all of the slice that can be among them,
+//                     a list; or else the slice's weights by bin
+//   k_sample_decide   a workgroup a row: rows of lists are done; of the others
+//                     the bins that the questions fall into
+//   k_sample_collect  the tokens of those bins (these rows are read once more)
+//   k_sample_pick     a workgroup a row: the questions
+// A slice's weights are relative to its own largest logit, and scaled where
+// the slices of a row come together.
 #include "../../include/rfpx_verify.h"
 #include "rfpx_impl.hpp"
 
@@ -31,15 +40,55 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 256;
-constexpr int kCopies = 4;   // of a histogram, by lane: neighbours often share a bin
-constexpr int kList = 4096;
+constexpr int kWide = 1024;    // threads of a workgroup that has a row's logits
+constexpr int kNarrow = 256;   // ... a slice's
+constexpr int kMiddle = 512;   // ... or what is left of a row
+constexpr int kMostWaves = 16;
+constexpr int kBins = 512;
+constexpr int kLaneBins = kBins / 64;
+constexpr int kCopies = 2;   // of a histogram, by lane: neighbours often share a bin
+constexpr int kList = 6144;  // tokens that answer() has in LDS
 constexpr int kSmall = 64;   // tokens that one wave ranks
-constexpr float kBinsPerOctave = 5.f;
+constexpr float kBinsPerOctave = 10.f;  // 51 octaves, which is all that weighs anything
 constexpr uint32_t kNoToken = 0x007FFFFFu;  // key of -inf, which NaN gets too
 constexpr float kNegInf = -__builtin_inff();
+constexpr int kRowMost = 32 * kWide;  // logits of a row that is not cut into slices
+constexpr int kSlice = 32 * kNarrow;  // logits of a slice
+constexpr int kSliceList = 512;       // tokens that a slice may list
+constexpr int kMostSlices = RFPX_VOCAB_MAX / kSlice + 1;
+constexpr int kTopMost = 256;     // top_k of rows whose slices list their tokens
+constexpr int kRowsAtOnce = 512;  // rows of one set of launches, which bounds the workspace
+
+// What k_sample_slices says of a slice.
+struct SliceHead {
+  float largest;
+  int first;   // its first place
+  float base;  // of its bins
+  bool binned; // its weights stand by bin
+  u64 total;   // ... and this is their sum
+  int listed;  // tokens that had to be listed (more than kSliceList: the list is not whole)
+  int last;    // the first top_k are in bins up to this one
+  int collected;  // ... by k_sample_collect
+};
+
+// Bins whose tokens the questions need one by one: of min_p's and top_k's, and
+// ranges for the two that depend on an answer that is known to its bin.
+struct Need {
+  int m0, m1, k0, k1, p0, p1, r0, r1;
+};
+
+struct Sums {  // of a bin and those before it
+  u64 mass[kBins];
+  uint32_t count[kBins];
+};
+
+// What k_sample_decide says of a row that is not done.
+struct RowState {
+  float largest;
+  int first;
+  Need need;
+  Sums bins;
+};
 
 struct SampleArgs {
   const void *logits;
@@ -49,6 +98,13 @@ struct SampleArgs {
   float *probs;
   long long stride;
   int n_rows, vocab, bits;  // weights are multiples of 2^-bits
+  int row0, rows, slices;
+  int *active;       // [1 + rows]: how many rows are not done, and which
+  RowState *state;   // [rows]
+  SliceHead *heads;  // [rows][slices]
+  u64 *mass;         // [rows][slices][kBins]
+  uint32_t *count;   // [rows][slices][kBins]
+  uint2 *list;       // [rows][slices][kSliceList]: key, index
 };
 
 // Keys order as floats do.
@@ -62,25 +118,34 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // NaN is no token, and -0 is 0.
 __device__ __forceinline__ float logit_of(float x) { return x > kNegInf ? x + 0.0f : kNegInf; }
 
-// A row's settings.
+// What weights and bins of a row, or a slice of it, are relative to.
 struct Row {
   float largest;
-  double rate;    // log2(e) / temperature
-  float bin_rate; // bins a logit
+  double rate;     // log2(e) / temperature
+  float bin_rate;  // bins a logit
+  float base;      // the largest logit's bin, counted from 0
   int bits;
 };
 
-__device__ __forceinline__ double below(const Row &r, float v) {  // 0 or less
-  return v == r.largest ? 0.0 : (double)v - (double)r.largest;
+__device__ __forceinline__ Row row_of(float largest, float temperature, int bits) {
+  Row r;
+  r.largest = largest;
+  r.rate = 1.4426950408889634 / (double)temperature;
+  r.bin_rate = fminf((float)r.rate * kBinsPerOctave, 3.0e38f);
+  r.base = floorf(largest * r.bin_rate);
+  r.bits = bits;
+  return r;
 }
 
-// exp(below / temperature) in units of 2^-bits, rounded to the nearest: 2^f by
-// its Taylor series to f^11 (|f| <= 1/2: 7e-15), the rounding by adding 2^52.
+// exp((v - largest) / temperature) in units of 2^-bits, rounded to the nearest:
+// 2^f by its Taylor series to f^11 (|f| <= 1/2: 7e-15).  Whole numbers are
+// had by adding 1.5 * 2^52 and 2^52, which leaves them in the low bits.
 __device__ __forceinline__ u64 weight(const Row &r, float v) {
 #pragma clang fp contract(off)
-  const double x = below(r, v) * r.rate;
+  const double x = (v == r.largest ? 0.0 : (double)v - (double)r.largest) * r.rate;
   if (!(x > -64.0)) return 0;  // (also 0 times an infinite distance)
-  const double n = __builtin_rint(x), f = x - n;
+  const double t = x + 6755399441055744.0;
+  const double f = x - (t - 6755399441055744.0);
   double p = 4.4455382718708100e-10;                     // ln2^11 / 11!
   p = __builtin_fma(p, f, 7.0549116208011208e-09);
   p = __builtin_fma(p, f, 1.0178086009239700e-07);
@@ -93,14 +158,18 @@ __device__ __forceinline__ u64 weight(const Row &r, float v) {
   p = __builtin_fma(p, f, 2.4022650695910069e-01);
   p = __builtin_fma(p, f, 6.9314718055994529e-01);
   p = __builtin_fma(p, f, 1.0);
-  const double y = __builtin_ldexp(p, (int)n + r.bits) + 4503599627370496.0;
-  return __builtin_bit_cast(u64, y) & 0xFFFFFFFFFFFFFull;
+  // times 2^(n + bits), by the exponent: p is within [0.7, 1.5], n + bits
+  // above -64
+  const u64 n = (u64)((int)__builtin_bit_cast(u64, t) + r.bits);
+  const double y = __builtin_bit_cast(double, __builtin_bit_cast(u64, p) + (n << 52));
+  return __builtin_bit_cast(u64, y + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
 }
 
-// The bin of a logit: no larger for a larger one.
+// The bin of a logit: no larger for a larger one.  Whole numbers of the logit
+// itself, so that bins of slices differ by a whole number too.
 __device__ __forceinline__ int bin_of(const Row &r, float v) {
-  const float y = v == r.largest ? 0.f : (r.largest - v) * r.bin_rate;
-  return y < (float)(kBins - 1) ? (int)y : kBins - 1;
+  const float b = r.base - floorf(v * r.bin_rate);
+  return v == r.largest ? 0 : (int)fminf(b, (float)(kBins - 1));
 }
 
 // x as a fraction of 2^64, below 1.
@@ -122,22 +191,20 @@ __device__ __forceinline__ u64 shfl_up_u64(u64 v, int off) {
   return ((u64)(uint32_t)__shfl_up((int)(v >> 32), off) << 32) | (uint32_t)__shfl_up((int)v, off);
 }
 
-struct Sums {  // of a bin and those before it
-  u64 mass[kBins];
-  uint32_t count[kBins];
-};
-
-// What a workgroup shares.
-struct Shared {
+struct Hist {
   u64 mass[kBins * kCopies];
   uint32_t count[kBins * kCopies];
-  Sums bins;                // of the row
-  Sums digits;              // of what find() is narrowing
+};
+// What a workgroup that answers a row's questions shares.
+struct Shared {
+  Hist hist;
+  Sums bins;    // of the row
+  Sums digits;  // of what find() is narrowing
   uint32_t key[kList];
   int32_t index[kList];
-  u64 sum[kWaves];
-  uint32_t best[kWaves];
-  int32_t first[kWaves];
+  u64 sum[kMostWaves];
+  float best[kMostWaves];
+  int32_t first[kMostWaves];
   uint32_t small_key[kSmall];
   int32_t small_index[kSmall];
   // answers of wave 0
@@ -148,40 +215,77 @@ struct Shared {
 
 // -------------------------------------------------------- sources of tokens
 
-// The logits of a row, 16 bytes a lane: f(logit, index) for each.
+// 16 bytes of a row's logits as floats, -inf outside of it.
 template <typename T>
 struct RowSource {
+  static constexpr int E = 16 / sizeof(T);
   const T *p;
   int n;
+  // The row in pieces of 16 aligned bytes: how many, and where piece c begins.
+  __device__ __forceinline__ int skip() const { return (int)(((uintptr_t)p & 15) / sizeof(T)); }
+  __device__ __forceinline__ int pieces() const { return (n + skip() + E - 1) / E; }
+  __device__ __forceinline__ int begin(int c) const { return c * E - skip(); }
+  __device__ __forceinline__ void load(int c, float (&v)[E]) const {
+    const int at = begin(c);
+    if (at >= 0 && at + E <= n) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(p + at);
+      const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        v[j] = sizeof(T) == 4 ? __uint_as_float(d[j * sizeof(T) / 4])
+               : j & 1        ? __uint_as_float(d[j / 2] & 0xFFFF0000u)
+                              : __uint_as_float(d[j / 2] << 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const bool in = at + j >= 0 && at + j < n;
+        const T x = in ? p[at + j] : T(0);
+        v[j] = !in              ? kNegInf
+               : sizeof(T) == 4 ? __builtin_bit_cast(float, (uint32_t)x)
+                                : __uint_as_float((uint32_t)x << 16);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = logit_of(v[j]);
+  }
+  // f(logit, index) for each; also for -inf.
   template <typename F>
   __device__ __forceinline__ void each(F &&f) const {
-    constexpr int E = 16 / sizeof(T);
-    const int skip = (int)(((uintptr_t)p & 15) / sizeof(T));
-    const int chunks = (n + skip + E - 1) / E;
-    for (int c = threadIdx.x; c < chunks; c += kThreads) {
-      const int at = c * E - skip;
+    for (int c = threadIdx.x; c < pieces(); c += blockDim.x) {
       float v[E];
-      if (at >= 0 && at + E <= n) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p + at);
-        const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+      load(c, v);
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-          v[j] = sizeof(T) == 4 ? __uint_as_float(d[j * sizeof(T) / 4])
-                 : j & 1        ? __uint_as_float(d[j / 2] & 0xFFFF0000u)
-                                : __uint_as_float(d[j / 2] << 16);
+      for (int j = 0; j < E; ++j) f(v[j], begin(c) + j);
+    }
+  }
+};
+
+// Logits in registers: pieces first + N threads' ones of a row.
+template <typename T, int N>
+struct HeldSource {
+  static constexpr int E = RowSource<T>::E;
+  float v[N][E];
+  int at;  // of the first
+  __device__ __forceinline__ void load(const RowSource<T> &src, int slice) {
+    const int c0 = slice * N * (int)blockDim.x + threadIdx.x, pieces = src.pieces();
+    at = src.begin(c0);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c = c0 + j * (int)blockDim.x;
+      if (c < pieces) {
+        src.load(c, v[j]);
       } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const bool in = at + j >= 0 && at + j < n;
-          const T x = in ? p[at + j] : T(0);
-          v[j] = !in ? kNegInf
-                 : sizeof(T) == 4 ? __builtin_bit_cast(float, (uint32_t)x)
-                                  : __uint_as_float((uint32_t)x << 16);
-        }
+        for (int i = 0; i < E; ++i) v[j][i] = kNegInf;
       }
-#pragma unroll
-      for (int j = 0; j < E; ++j) f(logit_of(v[j]), at + j);
     }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F &&f) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) f(v[j][i], at + j * (int)blockDim.x * E + i);
   }
 };
 
@@ -190,33 +294,53 @@ struct ListSource {
   int n;
   template <typename F>
   __device__ __forceinline__ void each(F &&f) const {
-    for (int i = threadIdx.x; i < n; i += kThreads) f(value_of(sh.key[i]), sh.index[i]);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) f(value_of(sh.key[i]), sh.index[i]);
+  }
+};
+
+// The lists of a row's slices.
+struct GatherSource {
+  const SliceHead *heads;
+  const uint2 *list;
+  int slices;
+  bool collected;
+  template <typename F>
+  __device__ __forceinline__ void each(F &&f) const {
+    // a wave a slice
+    const int lane = threadIdx.x & 63;
+    for (int s = threadIdx.x >> 6; s < slices; s += blockDim.x >> 6) {
+      const int n = collected ? heads[s].collected : heads[s].listed;
+      for (int i = lane; i < n; i += 64) {
+        const uint2 e = list[(size_t)s * kSliceList + i];
+        f(value_of(e.x), (int)e.y);
+      }
+    }
   }
 };
 
 // --------------------------------------------------------------- histograms
 
-__device__ __forceinline__ void clear_histogram(Shared &sh) {
-  for (int i = threadIdx.x; i < kBins * kCopies; i += kThreads) {
-    sh.mass[i] = 0;
-    sh.count[i] = 0;
+__device__ __forceinline__ void clear_histogram(Hist &h) {
+  for (int i = threadIdx.x; i < kBins * kCopies; i += blockDim.x) {
+    h.mass[i] = 0;
+    h.count[i] = 0;
   }
 }
-__device__ __forceinline__ void add_to_bin(Shared &sh, int bin, u64 w, bool counts) {
+__device__ __forceinline__ void add_to_bin(Hist &h, int bin, u64 w, uint32_t n) {
   const int at = bin * kCopies + (threadIdx.x & (kCopies - 1));
-  if (w) atomicAdd(&sh.mass[at], w);
-  if (counts) atomicAdd(&sh.count[at], 1u);
+  if (w) atomicAdd(&h.mass[at], w);
+  if (n) atomicAdd(&h.count[at], n);
 }
 // Running sums over the histogram's bins (between barriers of its own).
-__device__ __forceinline__ void sum_histogram(const Shared &sh, Sums &to) {
+__device__ __forceinline__ void sum_histogram(const Hist &h, Sums &to) {
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+  for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
     u64 m = 0;
     uint32_t c = 0;
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) {
-      m += sh.mass[i * kCopies + k];
-      c += sh.count[i * kCopies + k];
+      m += h.mass[i * kCopies + k];
+      c += h.count[i * kCopies + k];
     }
     to.mass[i] = m;
     to.count[i] = c;
@@ -224,15 +348,15 @@ __device__ __forceinline__ void sum_histogram(const Shared &sh, Sums &to) {
   __syncthreads();
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
-    u64 m[4];
-    uint32_t c[4];
+    u64 m[kLaneBins];
+    uint32_t c[kLaneBins];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = to.mass[4 * lane + i] + (i ? m[i - 1] : 0);
-      c[i] = to.count[4 * lane + i] + (i ? c[i - 1] : 0);
+    for (int i = 0; i < kLaneBins; ++i) {
+      m[i] = to.mass[kLaneBins * lane + i] + (i ? m[i - 1] : 0);
+      c[i] = to.count[kLaneBins * lane + i] + (i ? c[i - 1] : 0);
     }
-    u64 ms = m[3];
-    uint32_t cs = c[3];
+    u64 ms = m[kLaneBins - 1];
+    uint32_t cs = c[kLaneBins - 1];
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const u64 mo = shfl_up_u64(ms, off);
@@ -243,9 +367,9 @@ __device__ __forceinline__ void sum_histogram(const Shared &sh, Sums &to) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      to.mass[4 * lane + i] = ms - m[3] + m[i];
-      to.count[4 * lane + i] = cs - c[3] + c[i];
+    for (int i = 0; i < kLaneBins; ++i) {
+      to.mass[kLaneBins * lane + i] = ms - m[kLaneBins - 1] + m[i];
+      to.count[kLaneBins * lane + i] = cs - c[kLaneBins - 1] + c[i];
     }
   }
   __syncthreads();
@@ -254,14 +378,12 @@ __device__ __forceinline__ void sum_histogram(const Shared &sh, Sums &to) {
 // wave finds it for itself.
 __device__ __forceinline__ int bin_over(const Sums &to, u64 r, bool by_count) {
   const int lane = threadIdx.x & 63;
-  int over = kBins;
-#pragma unroll
-  for (int i = 3; i >= 0; --i) {
-    const int b = 4 * lane + i;
-    if ((by_count ? (u64)to.count[b] : to.mass[b]) > r) over = b;
-  }
-  const uint64_t lanes = __ballot(over < kBins);
-  return lanes ? __shfl(over, __builtin_ctzll(lanes)) : kBins - 1;
+  const auto over = [&](int b) { return (by_count ? (u64)to.count[b] : to.mass[b]) > r; };
+  const uint64_t lanes = __ballot(over(kLaneBins * lane + kLaneBins - 1));
+  if (!lanes) return kBins - 1;
+  const int first = kLaneBins * __builtin_ctzll(lanes);
+  const uint64_t bins = __ballot(lane < kLaneBins && over(first + (lane & (kLaneBins - 1))));
+  return uniform(first + __builtin_ctzll(bins));
 }
 
 // ------------------------------------------------------------------- find()
@@ -271,6 +393,10 @@ struct Found {
   u64 own;    // its weight
   int token;  // its index, if that was asked for
 };
+
+// A place in a sum: the last one, if it is past that (sums of slices that came
+// together are off by their rounding).
+__device__ __forceinline__ u64 within(u64 r, u64 sum) { return r < sum ? r : sum ? sum - 1 : 0; }
 
 // Among the tokens of bin `bin`, before which the order has weights `above`:
 // the first one at which the running sum (of weights, or of ones) within the
@@ -320,7 +446,7 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
       // are summed
       const u64 w = weight(row, value_of(lo));
       if (!by_count && w) {
-        const u64 place = r / w;
+        const u64 place = within(r / w, n);
         above += place * w;
         r = place;
       } else {
@@ -331,17 +457,18 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
       last = RFPX_VOCAB_MAX - 1;
     }
     const uint32_t span = keys ? hi - lo : (uint32_t)(last - first);
-    const int shift = max(0, 24 - __builtin_clz(span));
+    const int shift = max(0, 23 - __builtin_clz(span));
     __syncthreads();
-    clear_histogram(sh);
+    clear_histogram(sh.hist);
     __syncthreads();
     src.each([&](float v, int i) {
       const uint32_t k = key_of(v);
       if (k < lo || k > hi || i < first || i > last) return;
-      if (keys) add_to_bin(sh, (hi - k) >> shift, weight(row, v), true);
-      else add_to_bin(sh, (i - first) >> shift, 0, true);
+      if (keys) add_to_bin(sh.hist, (hi - k) >> shift, weight(row, v), 1);
+      else add_to_bin(sh.hist, (i - first) >> shift, 0, 1);
     });
-    sum_histogram(sh, sh.digits);
+    sum_histogram(sh.hist, sh.digits);
+    r = within(r, by_count ? (u64)sh.digits.count[kBins - 1] : sh.digits.mass[kBins - 1]);
     const int d = bin_over(sh.digits, r, by_count);
     const u64 m0 = d ? sh.digits.mass[d - 1] : 0;
     const uint32_t c0 = d ? sh.digits.count[d - 1] : 0;
@@ -360,7 +487,7 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
   if (n > kSmall) {  // many of one logit, and no index asked for
     const u64 w = weight(row, value_of(lo));
     f.own = w;
-    f.upto = above + ((by_count ? r : w ? r / w : 0) + 1) * w;
+    f.upto = above + (within(by_count ? r : w ? r / w : 0, n) + 1) * w;
     return f;
   }
   // One wave ranks what is left.  (Where indices were counted, the weights
@@ -396,6 +523,8 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
       }
     }
     const u64 sum = by_count ? (u64)rank : upto, own = by_count ? 1 : w;
+    const uint64_t last_one = __ballot(lane < m && rank == (uint32_t)m);
+    r = within(r, last_one ? shfl_u64(sum, __builtin_ctzll(last_one)) : 0);
     const bool it = lane < m && sum > r && sum - own <= r;
     const uint64_t lanes = __ballot(it);
     if (lanes ? lane == __builtin_ctzll(lanes) : lane == 0) {
@@ -415,14 +544,26 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
 
 // What a row asks for.
 struct Ask {
+  float temperature;
   int top_k;         // 0: no cut
   bool nucleus;      // a cut by top_p
   u64 top_p, u;      // fractions of 2^64
-  u64 least;         // weights of min_p
+  float min_p;       // 0: no cut
+  u64 least;         // its weight
+  __device__ __forceinline__ bool greedy() const { return !(temperature > 0.f) || top_k == 1; }
+  // Slices list their tokens: the first top_k, or those of min_p
+  __device__ __forceinline__ bool few() const { return top_k > 0 && top_k <= kTopMost; }
+  // (with a longer top_k and top_p besides, tokens that min_p cuts count too)
+  __device__ __forceinline__ bool listed() const {
+    return few() || (min_p > 0.f && !(top_k > 0 && nucleus));
+  }
+  // The sum of all tokens counts
+  __device__ __forceinline__ bool all() const { return !few() && (nucleus || !(min_p > 0.f)); }
 };
 
-__device__ __forceinline__ Ask ask_of(const SampleArgs &a, int at, int bits) {
+__device__ __forceinline__ Ask ask_of(const SampleArgs &a, int at) {
   Ask q;
+  q.temperature = a.temperature ? a.temperature[at] : 1.f;
   const int k = a.top_k ? a.top_k[at] : 0;
   q.top_k = k > 0 && k < a.vocab ? k : 0;
   const float p = a.top_p ? a.top_p[at] : 1.f;
@@ -430,30 +571,49 @@ __device__ __forceinline__ Ask ask_of(const SampleArgs &a, int at, int bits) {
   q.top_p = fraction(p);
   q.u = fraction(a.u[at]);
   const float m = a.min_p ? a.min_p[at] : 0.f;
-  q.least = !(m > 0.f) ? 0
-            : m >= 1.f ? 1ull << bits
-                       : (u64)__builtin_ceil(__builtin_ldexp((double)m, bits));
+  q.min_p = !(m > 0.f) ? 0.f : fminf(m, 1.f);
+  q.least = (u64)__builtin_ceil(__builtin_ldexp((double)q.min_p, a.bits));
   return q;
 }
 
-// Bins of whose tokens a question may need each by itself: of top_k's, and
-// ranges for the two that depend on an answer that is known to its bin.
-struct Need {
-  int k, p0, p1, r0, r1;
-  __device__ __forceinline__ bool operator()(int b) const {
-    return b == k || (b >= p0 && b <= p1) || (b >= r0 && b <= r1);
+__device__ __forceinline__ u64 before(const Sums &s, int bin) { return bin ? s.mass[bin - 1] : 0; }
+
+// Whether a logit is in one of the bins of a Need.  A bin is b or less just
+// where logit * bin_rate >= base - b, which most logits are not for any.
+struct Needed {
+  Row row;
+  Need n;
+  float least;
+  __device__ __forceinline__ Needed(const Row &r, const Need &need) : row(r), n(need) {
+    const int last = max(max(n.m1, n.k1), max(n.p1, n.r1));
+    least = last == kBins - 1 ? kNegInf : r.base - (float)last;
+  }
+  __device__ __forceinline__ bool operator()(float v) const {
+    if (v * row.bin_rate < least) return false;
+    const int b = bin_of(row, v);
+    return v > kNegInf && ((b >= n.m0 && b <= n.m1) || (b >= n.k0 && b <= n.k1) ||
+                           (b >= n.p0 && b <= n.p1) || (b >= n.r0 && b <= n.r1));
   }
 };
 
-__device__ __forceinline__ u64 before(const Sums &s, int bin) { return bin ? s.mass[bin - 1] : 0; }
-
-__device__ __forceinline__ Need need_of(const Sums &s, const Ask &q, u64 mass_min) {
-  Need n{-1, 0, -1, 0, -1};
-  u64 lo = s.mass[kBins - 1], hi = lo;
+// mass_min: the weights that min_p leaves, where they are known (else those
+// of the bins up to its own, in which it then has to be found out).
+__device__ __forceinline__ Need need_of(const Sums &s, const Row &row, const Ask &q, u64 all,
+                                        u64 mass_min, bool known) {
+  Need n{0, -1, 0, -1, 0, -1, 0, -1};
+  u64 min_lo = mass_min, min_hi = mass_min;
+  if (!known && q.min_p > 0.f) {
+    const int b = bin_of(row, (float)((double)row.largest + log((double)q.min_p) * q.temperature));
+    n.m0 = max(0, b - 1);
+    n.m1 = min(kBins - 1, b + 1);
+    min_lo = before(s, n.m0);
+    min_hi = s.mass[n.m1];
+  }
+  u64 lo = all, hi = all;
   if (q.top_k && s.count[kBins - 1] > (uint32_t)q.top_k) {
-    n.k = bin_over(s, (u64)(q.top_k - 1), true);
-    lo = before(s, n.k);
-    hi = s.mass[n.k];
+    n.k0 = n.k1 = bin_over(s, (u64)(q.top_k - 1), true);
+    lo = before(s, n.k0);
+    hi = s.mass[n.k0];
   }
   if (q.nucleus) {
     n.p0 = bin_over(s, just_below(lo, q.top_p), false);
@@ -461,128 +621,583 @@ __device__ __forceinline__ Need need_of(const Sums &s, const Ask &q, u64 mass_mi
     lo = min(lo, before(s, n.p0));
     hi = min(hi, s.mass[n.p1]);
   }
-  n.r0 = bin_over(s, __umul64hi(min(lo, mass_min), q.u), false);
-  n.r1 = bin_over(s, __umul64hi(min(hi, mass_min), q.u), false);
+  n.r0 = bin_over(s, __umul64hi(min(lo, min_lo), q.u), false);
+  n.r1 = bin_over(s, __umul64hi(min(hi, min_hi), q.u), false);
   return n;
 }
 
-// The questions in turn; `whole` gets the weight of all that stays.
+// The questions in turn: of top_k, of top_p, and of u.  `all` is the sum of the
+// row's weights, `whole` gets the sum of those that stay.
 template <typename S>
 __device__ __forceinline__ Found answer(const S &src, Shared &sh, const Row &row, const Ask &q,
-                                        u64 mass_min, u64 *whole) {
+                                        u64 all, u64 mass_min, u64 *whole) {
   const Sums &s = sh.bins;
-  u64 m = s.mass[kBins - 1];
-  if (q.top_k && s.count[kBins - 1] > (uint32_t)q.top_k) {
-    const int b = bin_over(s, (u64)(q.top_k - 1), true);
+  u64 m = all;
+  Found f{0, 0, -1};
+  for (int turn = 0; turn < 3; ++turn) {
+    u64 r = (u64)(q.top_k - 1);
+    if (turn == 0 && !(q.top_k && s.count[kBins - 1] > (uint32_t)q.top_k)) continue;
+    if (turn == 1) {
+      r = just_below(m, q.top_p);
+      if (!q.nucleus || r >= s.mass[kBins - 1]) continue;
+    }
+    if (turn == 2) {
+      m = min(m, mass_min);
+      *whole = m;
+      r = __umul64hi(m, q.u);
+    }
+    const int b = bin_over(s, r, turn == 0);
     const u64 m0 = before(s, b);
-    m = s.mass[b] == m0 ? m0
-                        : find(src, sh, row, b, true,
-                               (u64)(q.top_k - 1) - (b ? s.count[b - 1] : 0), m0, false).upto;
+    // no weight in the bin; or min_p leaves no more than the bins before, and
+    // nothing else is to be taken of the sum
+    if (turn < 2 && (s.mass[b] == m0 || (m0 >= mass_min && (turn == 1 || !q.nucleus)))) {
+      m = min(m, m0);
+      continue;
+    }
+    f = find(src, sh, row, b, turn == 0, r - (turn ? m0 : b ? s.count[b - 1] : 0), m0, turn == 2);
+    if (turn < 2) m = min(m, min(f.upto, s.mass[b]));
   }
-  if (q.nucleus) {
-    const u64 r = just_below(m, q.top_p);
-    const int b = bin_over(s, r, false);
-    const u64 m0 = before(s, b);
-    // (where min_p leaves less than the bins before, it alone counts)
-    if (m0 < mass_min) m = min(m, find(src, sh, row, b, false, r - m0, m0, false).upto);
-  }
-  m = min(m, mass_min);
-  *whole = m;
-  const u64 r = __umul64hi(m, q.u);
-  const int b = bin_over(s, r, false);
-  const u64 m0 = before(s, b);
-  return find(src, sh, row, b, false, r - m0, m0, true);
+  return f;
 }
 
-// A workgroup a row.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_sample_row(SampleArgs a) {
-  __shared__ Shared sh;
-  const int at = blockIdx.x, lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const RowSource<T> src{static_cast<const T *>(a.logits) + (size_t)at * a.stride, a.vocab};
+// The tokens of a source that `in` picks, into the list.  Their number: where
+// it is more than kList, the list is of no use.
+template <typename S, typename F>
+__device__ __forceinline__ int list_tokens(const S &src, Shared &sh, F &&in) {
+  __syncthreads();
+  if (threadIdx.x == 0) sh.n_list = 0;
+  __syncthreads();
+  src.each([&](float v, int i) {
+    if (!in(v)) return;
+    const int j = atomicAdd(&sh.n_list, 1);
+    if (j < kList) {
+      sh.key[j] = key_of(v);
+      sh.index[j] = i;
+    }
+  });
+  __syncthreads();
+  return sh.n_list;
+}
 
-  // the largest logit and its first place
-  float best = kNegInf;
-  int first = 0x7FFFFFFF;
+// The bins of all that may stay, from a source that has it; and what min_p
+// leaves of it.
+template <typename S>
+__device__ __forceinline__ u64 bins_of(const S &src, Shared &sh, const Row &row, const Ask &q) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  clear_histogram(sh.hist);
+  __syncthreads();
+  u64 mass_min = 0;
+  src.each([&](float v, int) {
+    if (!(v > kNegInf)) return;
+    const u64 w = weight(row, v);
+    add_to_bin(sh.hist, bin_of(row, v), w, q.top_k != 0);
+    if (w >= q.least) mass_min += w;
+  });
+#pragma unroll
+  for (int off = 32; off; off >>= 1) mass_min += shfl_u64(mass_min, lane ^ off);
+  if (lane == 0) sh.sum[wave] = mass_min;
+  sum_histogram(sh.hist, sh.bins);
+  mass_min = 0;
+  for (int w = 0; w < waves; ++w) mass_min += sh.sum[w];
+  return mass_min;
+}
+
+// A row of which all that may stay is in the list.
+__device__ __forceinline__ Found listed_row(Shared &sh, int n, const Row &row, const Ask &q,
+                                            bool all_here, u64 all, u64 *whole) {
+  const ListSource list{sh, n};
+  const u64 mass_min = bins_of(list, sh, row, q);
+  return answer(list, sh, row, q, all_here ? sh.bins.mass[kBins - 1] : all, mass_min, whole);
+}
+
+// Any row, from a source that has all of it (or all that may stay).
+// `long_way` has the same tokens, and need not be fast.
+template <typename S, typename L>
+__device__ __forceinline__ Found whole_row(const S &src, const L &long_way, Shared &sh,
+                                           const Row &row, const Ask &q, bool all_here, u64 all,
+                                           u64 *whole) {
+  const u64 mass_min = bins_of(src, sh, row, q);
+  if (all_here) all = sh.bins.mass[kBins - 1];
+  const int n = list_tokens(src, sh, Needed(row, need_of(sh.bins, row, q, all, mass_min, true)));
+  return n <= kList ? answer(ListSource{sh, n}, sh, row, q, all, mass_min, whole)
+                    : answer(long_way, sh, row, q, all, mass_min, whole);
+}
+
+// What can be among the first top_k, or weigh min_p: logits from `least` on, in
+// bins to `last`.  Of the first top_k of a row its part in this workgroup has
+// at most its own first top_k, and where so many of its threads' largest
+// logits (of each half of what a thread holds) lie in the bins to one, they
+// do.  (min_p is taken a little lower than it is, by far more than anything is
+// rounded.)
+struct Limits {
+  float least;
+  int last;
+  __device__ __forceinline__ bool operator()(const Row &row, float v) const {
+    return v > kNegInf && v >= least && bin_of(row, v) <= last;
+  }
+};
+__device__ __forceinline__ float least_of(const Row &row, const Ask &q) {
+  const double t = (double)q.temperature;
+  return __double2float_rd((double)row.largest + log((double)q.min_p) * t * (1.0 + 1e-6) - 1e-6 * t);
+}
+template <typename T, int N>
+__device__ __forceinline__ Limits limits_of(const HeldSource<T, N> &src, const Row &row,
+                                            const Ask &q, Hist &hist, Sums &sums) {
+  Limits l{kNegInf, kBins - 1};
+  if (q.few()) {
+    clear_histogram(hist);
+    __syncthreads();
+    constexpr int E = RowSource<T>::E;
+    float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int h = N > 1 ? 2 * j / N : 2 * i / E;
+        top[h] = fmaxf(top[h], src.v[j][i]);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (top[h] > kNegInf) add_to_bin(hist, bin_of(row, top[h]), 0, 1);
+    sum_histogram(hist, sums);
+    l.last = bin_over(sums, (u64)(q.top_k - 1), true);
+  } else if (q.min_p > 0.f) {
+    l.least = least_of(row, q);
+  }
+  return l;
+}
+
+__device__ __forceinline__ void write(const SampleArgs &a, int at, int token, float prob) {
+  if (threadIdx.x) return;
+  a.tokens[at] = token;
+  if (a.probs) a.probs[at] = prob;
+}
+
+// The largest of (v, i) over the workgroup, the smallest i among equals.
+__device__ __forceinline__ void first_largest(float (&best)[kMostWaves], int32_t (&first)[kMostWaves],
+                                              float &v, int &i) {
+  const auto join = [&](float x, int j) {
+    if (x > v || (x == v && j < i)) {
+      v = x;
+      i = j;
+    }
+  };
+#pragma unroll
+  for (int off = 32; off; off >>= 1) join(__shfl_xor(v, off), __shfl_xor(i, off));
+  if ((threadIdx.x & 63) == 0) {
+    best[threadIdx.x >> 6] = v;
+    first[threadIdx.x >> 6] = i;
+  }
+  __syncthreads();
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) join(best[w], first[w]);
+}
+template <typename T, int N>
+__device__ __forceinline__ void first_of(const HeldSource<T, N> &src, float &best, int &first) {
+  best = kNegInf;
+  first = 0x7FFFFFFF;
   src.each([&](float v, int i) {
     if (v > best) {
       best = v;
       first = i;
     }
   });
-  const auto join = [&](float v, int i) {
-    if (v > best || (v == best && i < first)) {
-      best = v;
-      first = i;
-    }
-  };
-#pragma unroll
-  for (int off = 32; off; off >>= 1) join(__shfl_xor(best, off), __shfl_xor(first, off));
-  if (lane == 0) {
-    sh.best[wave] = __float_as_uint(best);
-    sh.first[wave] = first;
+}
+
+template <typename T>
+__device__ __forceinline__ RowSource<T> logits_of(const SampleArgs &a, int at) {
+  return RowSource<T>{static_cast<const T *>(a.logits) + (size_t)at * a.stride, a.vocab};
+}
+
+// A workgroup a row, whose logits it holds.
+template <typename T, int N>
+__global__ __launch_bounds__(kWide) void k_sample_row(SampleArgs a) {
+  __shared__ Shared sh;
+  const int at = blockIdx.x;
+  const RowSource<T> src = logits_of<T>(a, at);
+  HeldSource<T, N> held;
+  held.load(src, 0);
+  float best;
+  int first;
+  first_of(held, best, first);
+  first_largest(sh.best, sh.first, best, first);
+  const Ask q = ask_of(a, at);
+  if (best == kNegInf) return write(a, at, -1, 0.f);
+  if (q.greedy()) return write(a, at, first, 1.f);
+  const Row row = row_of(best, q.temperature, a.bits);
+  u64 whole;
+  Found f;
+  // (where one is +inf, what the others are told by is no number)
+  if (!q.all() && q.listed() && best < -kNegInf) {
+    const Limits l = limits_of(held, row, q, sh.hist, sh.digits);
+    const int n = list_tokens(held, sh, [&](float v) { return l(row, v); });
+    f = n <= kList ? listed_row(sh, n, row, q, true, 0, &whole)
+                   : whole_row(src, src, sh, row, q, true, 0, &whole);
+  } else {
+    f = whole_row(held, src, sh, row, q, true, 0, &whole);
   }
-  clear_histogram(sh);
-  if (threadIdx.x == 0) sh.n_list = 0;
-  __syncthreads();
-  for (int w = 0; w < kWaves; ++w) join(__uint_as_float(sh.best[w]), sh.first[w]);
-  const float t = a.temperature ? a.temperature[at] : 1.f;
-  const Ask q = ask_of(a, at, a.bits);
-  if (best == kNegInf || !(t > 0.f) || q.top_k == 1) {
-    if (threadIdx.x == 0) {
-      a.tokens[at] = best == kNegInf ? -1 : first;
-      if (a.probs) a.probs[at] = best == kNegInf ? 0.f : 1.f;
-    }
+  write(a, at, f.token, (float)((double)f.own / (double)whole));
+}
+
+// ------------------------------------------------------------------- slices
+
+template <typename T>
+constexpr int kPieces = kSlice / (kNarrow * RowSource<T>::E);
+
+template <typename T>
+__global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
+  __shared__ Hist hist;
+  __shared__ Sums sums;
+  __shared__ float sh_best[kMostWaves];
+  __shared__ int32_t sh_first[kMostWaves];
+  __shared__ u64 sh_sum[kMostWaves];
+  __shared__ int sh_listed;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int slice = blockIdx.x, at = a.row0 + blockIdx.y;
+  const size_t rs = (size_t)blockIdx.y * a.slices + slice;
+  if (slice == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.active[0] = 0;
+  HeldSource<T, kPieces<T>> held;
+  held.load(logits_of<T>(a, at), slice);
+  const Ask q = ask_of(a, at);
+  float best;
+  int first;
+  first_of(held, best, first);
+  if (threadIdx.x == 0) sh_listed = 0;
+  first_largest(sh_best, sh_first, best, first);
+  SliceHead head{best, first, 0.f, false, 0, 0, kBins - 1, 0};
+  if (best == kNegInf || best == -kNegInf || q.greedy()) {
+    if (threadIdx.x == 0) a.heads[rs] = head;
     return;
   }
-  Row row;
-  row.largest = best;
-  row.rate = 1.4426950408889634 / (double)t;
-  row.bin_rate = fminf((float)row.rate * kBinsPerOctave, 3.0e38f);
-  row.bits = a.bits;
-
-  // weights by bin, and of those that min_p leaves
-  u64 mass_min = 0;
-  src.each([&](float v, int) {
-    if (v > kNegInf) {
-      const u64 w = weight(row, v);
-      add_to_bin(sh, bin_of(row, v), w, q.top_k != 0);
-      if (w >= q.least) mass_min += w;
+  const Row row = row_of(best, q.temperature, a.bits);
+  head.base = row.base;
+  const bool listed = q.listed(), all = q.all();
+  if (listed) {
+    const Limits l = limits_of(held, row, q, hist, sums);
+    head.last = l.last;
+    held.each([&](float v, int i) {
+      if (!l(row, v)) return;
+      const int n = atomicAdd(&sh_listed, 1);
+      if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key_of(v), (uint32_t)i);
+    });
+    __syncthreads();
+    head.listed = sh_listed;
+    if (!all && head.listed <= kSliceList) {
+      if (threadIdx.x == 0) a.heads[rs] = head;
+      return;
     }
+  }
+  head.binned = true;
+  clear_histogram(hist);
+  __syncthreads();
+  u64 total = 0;
+  held.each([&](float v, int) {
+    if (!(v > kNegInf)) return;
+    const u64 w = weight(row, v);
+    total += w;
+    add_to_bin(hist, bin_of(row, v), w, q.top_k != 0);
   });
 #pragma unroll
-  for (int off = 32; off; off >>= 1) mass_min += shfl_u64(mass_min, lane ^ off);
-  if (lane == 0) sh.sum[wave] = mass_min;
-  sum_histogram(sh, sh.bins);
-  mass_min = 0;
-  for (int w = 0; w < kWaves; ++w) mass_min += sh.sum[w];
-
-  // the tokens of the bins in question
-  const Need need = need_of(sh.bins, q, mass_min);
-  src.each([&](float v, int i) {
-    if (v > kNegInf && need(bin_of(row, v))) {
-      const int j = atomicAdd(&sh.n_list, 1);
-      if (j < kList) {
-        sh.key[j] = key_of(v);
-        sh.index[j] = i;
-      }
-    }
-  });
+  for (int off = 32; off; off >>= 1) total += shfl_u64(total, lane ^ off);
+  if (lane == 0) sh_sum[wave] = total;
   __syncthreads();
-  u64 whole;
-  const Found f = sh.n_list <= kList
-                      ? answer(ListSource{sh, sh.n_list}, sh, row, q, mass_min, &whole)
-                      : answer(src, sh, row, q, mass_min, &whole);
   if (threadIdx.x == 0) {
-    a.tokens[at] = f.token;
-    if (a.probs) a.probs[at] = (float)((double)f.own / (double)whole);
+    for (int w = 0; w < kNarrow / 64; ++w) head.total += sh_sum[w];
+    a.heads[rs] = head;
+  }
+  for (int i = threadIdx.x; i < kBins; i += kNarrow) {
+    u64 m = 0;
+    uint32_t c = 0;
+#pragma unroll
+    for (int k = 0; k < kCopies; ++k) {
+      m += hist.mass[i * kCopies + k];
+      c += hist.count[i * kCopies + k];
+    }
+    a.mass[rs * kBins + i] = m;
+    a.count[rs * kBins + i] = c;
   }
 }
+
+// A row's slices together.
+struct Joined {
+  float largest;
+  int first;
+  bool whole;  // every slice has listed all that may stay of it
+};
+__device__ __forceinline__ Joined join_heads(const SliceHead *heads, int slices, const Ask &q) {
+  const int lane = threadIdx.x & 63;  // slices dealt out over the lanes of each wave
+  Joined r{kNegInf, -1, false};
+  int at = 0x7FFFFFFF;
+  bool more = false;
+  for (int s = lane; s < slices; s += 64) {
+    const SliceHead h = heads[s];
+    if (h.largest > r.largest) {
+      r.largest = h.largest;
+      at = h.first;
+    }
+    more = more || h.listed > kSliceList;
+  }
+#pragma unroll
+  for (int off = 32; off; off >>= 1) {
+    const float x = __shfl_xor(r.largest, off);
+    const int i = __shfl_xor(at, off);
+    if (x > r.largest || (x == r.largest && i < at)) {
+      r.largest = x;
+      at = i;
+    }
+  }
+  r.first = at;
+  r.whole = q.listed() && !__any(more);
+  return r;
+}
+// What a slice's weights are multiplied by, as a fraction of 2^64 (0: by one).
+__device__ __forceinline__ u64 slice_factor(const Row &row, float largest) {
+  if (largest == row.largest) return 0;
+  const double f = exp2(((double)largest - (double)row.largest) * row.rate);
+  const u64 part = (u64)__builtin_ldexp(f, 64);
+  return f < 1.0 ? part ? part : 1 : 0;
+}
+__device__ __forceinline__ u64 scaled(u64 m, u64 factor) { return factor ? __umul64hi(m, factor) : m; }
+
+// Weights and counts by bin of all slices, as running sums: a wave a slice.
+// Of a slice that has listed all that may stay, that.
+__device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row &row, const Ask &q,
+                                          Hist &hist, Sums &to) {
+  clear_histogram(hist);
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  for (int s = threadIdx.x >> 6; s < a.slices; s += blockDim.x >> 6) {
+    const size_t rs = (size_t)r * a.slices + s;
+    const SliceHead h = a.heads[rs];
+    if (!(h.largest > kNegInf)) continue;
+    if (!h.binned) {
+      for (int i = lane; i < h.listed; i += 64) {
+        const float v = value_of(a.list[rs * kSliceList + i].x);
+        add_to_bin(hist, bin_of(row, v), weight(row, v), q.top_k != 0);
+      }
+      continue;
+    }
+    const u64 factor = slice_factor(row, h.largest);
+    for (int i = lane; i < kBins; i += 64) {
+      const u64 m = a.mass[rs * kBins + i];
+      const uint32_t c = a.count[rs * kBins + i];
+      // (bases that are no numbers: the last bin, as bin_of has it)
+      const float b = (float)i + (row.base - h.base);
+      if (m | c)
+        add_to_bin(hist, h.largest == row.largest ? i : (int)fminf(b, (float)(kBins - 1)),
+                   scaled(m, factor), c);
+    }
+  }
+  sum_histogram(hist, to);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 63;
+  const int r = blockIdx.x, at = a.row0 + r;
+  const SliceHead *heads = a.heads + (size_t)r * a.slices;
+  const Ask q = ask_of(a, at);
+  const Joined joined = join_heads(heads, a.slices, q);
+  if (joined.largest == kNegInf) return write(a, at, -1, 0.f);
+  if (q.greedy()) return write(a, at, joined.first, 1.f);
+  const Row row = row_of(joined.largest, q.temperature, a.bits);
+  u64 whole;
+  if (joined.largest == -kNegInf || joined.whole) {
+    Found f;
+    const RowSource<T> src = logits_of<T>(a, at);
+    if (joined.whole && joined.largest < -kNegInf) {
+      // all weights, and what the slices' own first top_k leave for the row's
+      u64 all = 0;
+      float last = kBins - 1;
+      for (int s = lane; s < a.slices; s += 64) {
+        const SliceHead h = heads[s];
+        if (!(h.largest > kNegInf)) continue;
+        all += scaled(h.total, slice_factor(row, h.largest));
+        last = fminf(last, h.largest == row.largest ? (float)h.last
+                                                    : (float)h.last + (row.base - h.base));
+      }
+#pragma unroll
+      for (int off = 32; off; off >>= 1) {
+        all += shfl_u64(all, lane ^ off);
+        last = fminf(last, __shfl_xor(last, off));
+      }
+      const Limits l{q.few() || !(q.min_p > 0.f) ? kNegInf : least_of(row, q),
+                     q.few() ? (int)last : kBins - 1};
+      const GatherSource gather{heads, a.list + (size_t)r * a.slices * kSliceList, a.slices, false};
+      const int n = list_tokens(gather, sh, [&](float v) { return l(row, v); });
+      f = n <= kList ? listed_row(sh, n, row, q, !q.all(), all, &whole)
+                     : whole_row(gather, gather, sh, row, q, !q.all(), all, &whole);
+    } else {
+      f = whole_row(src, src, sh, row, q, true, 0, &whole);
+    }
+    return write(a, at, f.token, (float)((double)f.own / (double)whole));
+  }
+  join_bins(a, r, row, q, sh.hist, sh.bins);
+  const u64 all = sh.bins.mass[kBins - 1];
+  const Need need = need_of(sh.bins, row, q, all, all, false);
+  RowState &state = a.state[r];
+  for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
+    state.bins.mass[i] = sh.bins.mass[i];
+    state.bins.count[i] = sh.bins.count[i];
+  }
+  if (threadIdx.x == 0) {
+    state.largest = joined.largest;
+    state.first = joined.first;
+    state.need = need;
+    a.active[1 + atomicAdd(a.active, 1)] = r;
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kNarrow) void k_sample_collect(SampleArgs a) {
+  __shared__ int sh_n;
+  const int tasks = a.active[0] * a.slices;
+  for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int r = a.active[1 + task / a.slices], slice = task % a.slices, at = a.row0 + r;
+    const size_t rs = (size_t)r * a.slices + slice;
+    HeldSource<T, kPieces<T>> held;
+    held.load(logits_of<T>(a, at), slice);
+    if (threadIdx.x == 0) sh_n = 0;
+    __syncthreads();
+    const Needed needed(row_of(a.state[r].largest, a.temperature ? a.temperature[at] : 1.f, a.bits),
+                        a.state[r].need);
+    held.each([&](float v, int i) {
+      if (needed(v)) {
+        const int n = atomicAdd(&sh_n, 1);
+        if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key_of(v), (uint32_t)i);
+      }
+    });
+    __syncthreads();
+    if (threadIdx.x == 0) a.heads[rs].collected = sh_n;
+    __syncthreads();
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
+  __shared__ Shared sh;
+  if ((int)blockIdx.x >= a.active[0]) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r = a.active[1 + blockIdx.x], at = a.row0 + r;
+  const SliceHead *heads = a.heads + (size_t)r * a.slices;
+  const Ask q = ask_of(a, at);
+  const RowState &state = a.state[r];
+  const Row row = row_of(state.largest, q.temperature, a.bits);
+  const Need need = state.need;
+  for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
+    sh.bins.mass[i] = state.bins.mass[i];
+    sh.bins.count[i] = state.bins.count[i];
+  }
+  if (threadIdx.x == 0) sh.n_list = 0;
+  bool more = false;
+  for (int s = lane; s < a.slices; s += 64) more = more || heads[s].collected > kSliceList;
+  const bool fits = !__any(more);
+  __syncthreads();
+  const u64 all = sh.bins.mass[kBins - 1];
+  // the tokens in question, and of min_p's bins the weights that it leaves
+  u64 part = 0;
+  const auto look = [&](float v, int i, bool keep) {
+    if (!(v > kNegInf)) return;
+    const int b = bin_of(row, v);
+    if (b >= need.m0 && b <= need.m1) {
+      const u64 w = weight(row, v);
+      if (w >= q.least) part += w;
+    }
+    if (!keep) return;
+    const int j = atomicAdd(&sh.n_list, 1);
+    if (j < kList) {
+      sh.key[j] = key_of(v);
+      sh.index[j] = i;
+    }
+  };
+  const RowSource<T> src = logits_of<T>(a, at);
+  const GatherSource gather{heads, a.list + (size_t)r * a.slices * kSliceList, a.slices, true};
+  if (fits) gather.each([&](float v, int i) { look(v, i, true); });
+  else if (need.m1 >= need.m0) src.each([&](float v, int i) { look(v, i, false); });
+#pragma unroll
+  for (int off = 32; off; off >>= 1) part += shfl_u64(part, lane ^ off);
+  if (lane == 0) sh.sum[wave] = part;
+  __syncthreads();
+  u64 mass_min = all;
+  if (need.m1 >= need.m0) {
+    mass_min = before(sh.bins, need.m0);
+    for (int w = 0; w < kMiddle / 64; ++w) mass_min += sh.sum[w];
+    mass_min = min(mass_min, sh.bins.mass[need.m1]);
+  }
+  u64 whole;
+  const Found f = !fits ? answer(src, sh, row, q, all, mass_min, &whole)
+                  : sh.n_list <= kList
+                      ? answer(ListSource{sh, sh.n_list}, sh, row, q, all, mass_min, &whole)
+                      : answer(gather, sh, row, q, all, mass_min, &whole);
+  write(a, at, f.token, (float)((double)f.own / (double)whole));
+}
+
+// ---------------------------------------------------------------- host side
 
 int weight_bits(int vocab) {
   int log = 12;
   while (1 << log < vocab) ++log;
   return 62 - log;
+}
+
+// Slices of a row (none: a row is a workgroup's), and the workspace of the
+// rows that are done at once.
+struct SamplePlan {
+  int pieces, slices, rows;
+  size_t active, state, heads, mass, count, list, total;
+};
+
+SamplePlan sample_plan(int n_rows, int vocab, int xtype) {
+  SamplePlan p{};
+  p.total = 256;
+  const int e = xtype == RFPX_X_BF16 ? 8 : 4;
+  const int pieces = (vocab + 2 * (e - 1)) / e;  // wherever the row begins
+  const int most = kRowMost / (kWide * e);
+  for (p.pieces = 1; p.pieces < most && p.pieces * kWide < pieces;) p.pieces *= 2;
+  if (p.pieces * kWide >= pieces) return p;
+  p.rows = n_rows < kRowsAtOnce ? n_rows : kRowsAtOnce;
+  p.slices = (pieces * e + kSlice - 1) / kSlice;
+  const size_t rs = (size_t)p.rows * p.slices;
+  p.active = 0;
+  p.state = p.active + align_up(((size_t)p.rows + 1) * 4, 256);
+  p.heads = p.state + align_up(p.rows * sizeof(RowState), 256);
+  p.mass = p.heads + align_up(rs * sizeof(SliceHead), 256);
+  p.count = p.mass + align_up(rs * kBins * 8, 256);
+  p.list = p.count + align_up(rs * kBins * 4, 256);
+  p.total = p.list + align_up(rs * kSliceList * 8, 256);
+  if (p.total < 256) p.total = 256;
+  return p;
+}
+
+template <typename T>
+hipError_t launch_sample(const SamplePlan &p, SampleArgs a, uint8_t *w, hipStream_t s) {
+  constexpr int most = kRowMost / (kWide * RowSource<T>::E);
+  if (!p.slices) {
+    void (*row)(SampleArgs) = p.pieces == 1   ? k_sample_row<T, 1>
+                              : p.pieces == 2 ? k_sample_row<T, 2>
+                              : p.pieces == 4 ? k_sample_row<T, 4>
+                                              : k_sample_row<T, most>;
+    return launch_k(row, dim3(a.n_rows), dim3(kWide), 0, s, a);
+  }
+  a.slices = p.slices;
+  a.active = reinterpret_cast<int *>(w + p.active);
+  a.state = reinterpret_cast<RowState *>(w + p.state);
+  a.heads = reinterpret_cast<SliceHead *>(w + p.heads);
+  a.mass = reinterpret_cast<u64 *>(w + p.mass);
+  a.count = reinterpret_cast<uint32_t *>(w + p.count);
+  a.list = reinterpret_cast<uint2 *>(w + p.list);
+  hipError_t e = hipSuccess;
+  for (a.row0 = 0; a.row0 < a.n_rows && e == hipSuccess; a.row0 += p.rows) {
+    a.rows = a.n_rows - a.row0 < p.rows ? a.n_rows - a.row0 : p.rows;
+    const int all = a.rows * a.slices;
+    e = launch_k(k_sample_slices<T>, dim3(a.slices, a.rows), dim3(kNarrow), 0, s, a);
+    if (e == hipSuccess) e = launch_k(k_sample_decide<T>, dim3(a.rows), dim3(kMiddle), 0, s, a);
+    if (e == hipSuccess)
+      e = launch_k(k_sample_collect<T>, dim3(all < 2048 ? all : 2048), dim3(kNarrow), 0, s, a);
+    if (e == hipSuccess) e = launch_k(k_sample_pick<T>, dim3(a.rows), dim3(kMiddle), 0, s, a);
+  }
+  return e;
 }
 
 rfpx_status check_sample(const char *fn, int n_rows, int vocab, int xtype) {
@@ -604,7 +1219,7 @@ extern "C" {
 
 size_t rfpx_sample_workspace_bytes(int n_rows, int vocab, int xtype) {
   if (check_sample("rfpx_sample_workspace_bytes", n_rows, vocab, xtype)) return 0;
-  return 256;
+  return sample_plan(n_rows, vocab, xtype).total;
 }
 
 rfpx_status rfpx_sample(const void *logits, long long stride, int xtype, int n_rows, int vocab,
@@ -625,9 +1240,9 @@ rfpx_status rfpx_sample(const void *logits, long long stride, int xtype, int n_r
     return fail(RFPX_E_ALIGN, "%s: logits must be aligned to an element, the others to 4 bytes", fn);
   if (!ws) return fail(RFPX_E_ARG, "%s: workspace is null", fn);
   if ((uintptr_t)ws % 256) return fail(RFPX_E_ALIGN, "%s: workspace not 256-byte aligned", fn);
-  const size_t need = rfpx_sample_workspace_bytes(n_rows, vocab, xtype);
-  if (ws_bytes < need)
-    return fail(RFPX_E_WORKSPACE, "%s: workspace holds %zu bytes, needs %zu", fn, ws_bytes, need);
+  const SamplePlan p = sample_plan(n_rows, vocab, xtype);
+  if (ws_bytes < p.total)
+    return fail(RFPX_E_WORKSPACE, "%s: workspace holds %zu bytes, needs %zu", fn, ws_bytes, p.total);
   SampleArgs a{};
   a.logits = logits;
   a.u = u;
@@ -641,9 +1256,10 @@ rfpx_status rfpx_sample(const void *logits, long long stride, int xtype, int n_r
   a.n_rows = n_rows;
   a.vocab = vocab;
   a.bits = weight_bits(vocab);
-  const hipError_t e =
-      launch_k(xtype == RFPX_X_BF16 ? k_sample_row<uint16_t> : k_sample_row<uint32_t>,
-               dim3(n_rows), dim3(kThreads), 0, (hipStream_t)stream, a);
+  const hipStream_t s = (hipStream_t)stream;
+  const hipError_t e = xtype == RFPX_X_BF16
+                           ? launch_sample<uint16_t>(p, a, static_cast<uint8_t *>(ws), s)
+                           : launch_sample<uint32_t>(p, a, static_cast<uint8_t *>(ws), s);
   return e == hipSuccess ? RFPX_OK : fail(RFPX_E_HIP, "%s: %s", fn, hipGetErrorString(e));
 }
 
