@@ -46,6 +46,8 @@ constexpr int kMiddle = 512;   // ... or what is left of a row
 constexpr int kMostWaves = 16;
 constexpr int kBins = 512;
 constexpr int kLaneBins = kBins / 64;
+constexpr int kSumWaves = 4;  // that sum up a histogram, two bins a lane
+static_assert(kBins == 2 * 64 * kSumWaves, "two bins a lane");
 constexpr int kCopies = 2;   // of a histogram, by lane: neighbours often share a bin
 constexpr int kList = 6144;  // tokens that answer() has in LDS
 constexpr int kSmall = 64;   // tokens that one wave ranks
@@ -107,16 +109,19 @@ struct SampleArgs {
   uint2 *list;       // [rows][slices][kSliceList]: key, index
 };
 
-// Keys order as floats do.
+// Keys order as floats do, and -0 is 0.
 __device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t u = __float_as_uint(v);
+  const uint32_t u = __float_as_uint(v + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
-// NaN is no token, and -0 is 0.
-__device__ __forceinline__ float logit_of(float x) { return x > kNegInf ? x + 0.0f : kNegInf; }
+// NaN is no token, as -inf; +inf counts as the largest number, so that all
+// that is computed of tokens is one.
+__device__ __forceinline__ float logit_of(float x) {
+  return x > kNegInf ? fminf(x, 3.402823466e38f) : kNegInf;
+}
 
 // What weights and bins of a row, or a slice of it, are relative to.
 struct Row {
@@ -138,38 +143,42 @@ __device__ __forceinline__ Row row_of(float largest, float temperature, int bits
 }
 
 // exp((v - largest) / temperature) in units of 2^-bits, rounded to the nearest:
-// 2^f by its Taylor series to f^11 (|f| <= 1/2: 7e-15).  Whole numbers are
-// had by adding 1.5 * 2^52 and 2^52, which leaves them in the low bits.
+// 2^f, |f| <= 1/2, by the polynomial 1 + f q(f) of degree 10 of least relative
+// error (3e-16, by Remez' exchange).  Whole numbers are had by adding 1.5 * 2^52
+// and 2^52, which leaves them in the low bits; 2^n goes into the exponent.  A
+// logit of -inf weighs 0.
 __device__ __forceinline__ u64 weight(const Row &r, float v) {
 #pragma clang fp contract(off)
-  const double x = (v == r.largest ? 0.0 : (double)v - (double)r.largest) * r.rate;
-  if (!(x > -64.0)) return 0;  // (also 0 times an infinite distance)
-  const double t = x + 6755399441055744.0;
-  const double f = x - (t - 6755399441055744.0);
-  double p = 4.4455382718708100e-10;                     // ln2^11 / 11!
-  p = __builtin_fma(p, f, 7.0549116208011208e-09);
-  p = __builtin_fma(p, f, 1.0178086009239700e-07);
-  p = __builtin_fma(p, f, 1.3215486790144307e-06);
-  p = __builtin_fma(p, f, 1.5252733804059841e-05);
-  p = __builtin_fma(p, f, 1.5403530393381610e-04);
-  p = __builtin_fma(p, f, 1.3333558146428441e-03);
-  p = __builtin_fma(p, f, 9.6181291076284769e-03);
-  p = __builtin_fma(p, f, 5.5504108664821580e-02);
-  p = __builtin_fma(p, f, 2.4022650695910069e-01);
-  p = __builtin_fma(p, f, 6.9314718055994529e-01);
+  const double x = __builtin_fmax(((double)v - (double)r.largest) * r.rate, -64.0);
+  const double whole = 6755399441055744.0 + (double)r.bits;
+  const double t = x + whole, f = x - (t - whole);
+  double p = 7.11174936174289645e-09;
+  p = __builtin_fma(p, f, 1.02105059849407951e-07);
+  p = __builtin_fma(p, f, 1.32152356871880181e-06);
+  p = __builtin_fma(p, f, 1.52526477502981718e-05);
+  p = __builtin_fma(p, f, 1.54035308007198697e-04);
+  p = __builtin_fma(p, f, 1.33335582464760177e-03);
+  p = __builtin_fma(p, f, 9.61812910738078439e-03);
+  p = __builtin_fma(p, f, 5.55041086643466158e-02);
+  p = __builtin_fma(p, f, 2.40226506959104719e-01);
+  p = __builtin_fma(p, f, 6.93147180559951614e-01);
   p = __builtin_fma(p, f, 1.0);
-  // times 2^(n + bits), by the exponent: p is within [0.7, 1.5], n + bits
-  // above -64
-  const u64 n = (u64)((int)__builtin_bit_cast(u64, t) + r.bits);
-  const double y = __builtin_bit_cast(double, __builtin_bit_cast(u64, p) + (n << 52));
-  return __builtin_bit_cast(u64, y + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
+  const u64 u = __builtin_bit_cast(u64, p);
+  const uint32_t hi = (uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(u64, t) << 20);
+  const double y = __builtin_bit_cast(double, (u64)hi << 32 | (uint32_t)u) + 4503599627370496.0;
+  return __builtin_bit_cast(u64, y) & 0xFFFFFFFFFFFFFull;
 }
 
 // The bin of a logit: no larger for a larger one.  Whole numbers of the logit
-// itself, so that bins of slices differ by a whole number too.
+// itself, so that bins of slices differ by a whole number too.  Where products
+// overflow, and what is left of two of them is no number, it is the first.
 __device__ __forceinline__ int bin_of(const Row &r, float v) {
   const float b = r.base - floorf(v * r.bin_rate);
-  return v == r.largest ? 0 : (int)fminf(b, (float)(kBins - 1));
+  return (int)fminf(fmaxf(b, 0.f), (float)(kBins - 1));
+}
+// Bin `i` of a slice, among the row's.
+__device__ __forceinline__ int row_bin(const Row &r, float slice_base, int i) {
+  return slice_base == r.base ? i : (int)fminf((float)i + (r.base - slice_base), (float)(kBins - 1));
 }
 
 // x as a fraction of 2^64, below 1.
@@ -187,13 +196,33 @@ __device__ __forceinline__ u64 just_below(u64 whole, u64 part) {
 __device__ __forceinline__ u64 shfl_u64(u64 v, int lane) {
   return ((u64)(uint32_t)__shfl((int)(v >> 32), lane) << 32) | (uint32_t)__shfl((int)v, lane);
 }
-__device__ __forceinline__ u64 shfl_up_u64(u64 v, int off) {
-  return ((u64)(uint32_t)__shfl_up((int)(v >> 32), off) << 32) | (uint32_t)__shfl_up((int)v, off);
+
+// Running sums over the lanes of a wave, by data-parallel moves: within rows of
+// 16 lanes, then from row to row.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 moved(u64 v) {
+  return ((u64)moved<CTRL, ROWS>((uint32_t)(v >> 32)) << 32) | moved<CTRL, ROWS>((uint32_t)v);
+}
+template <typename U>
+__device__ __forceinline__ U running_sum(U v) {
+  v += moved<0x111, 0xF>(v);  // from 1, 2, 4, 8 lanes below
+  v += moved<0x112, 0xF>(v);
+  v += moved<0x114, 0xF>(v);
+  v += moved<0x118, 0xF>(v);
+  v += moved<0x142, 0xA>(v);  // the last lane of row 0 to row 1, of 2 to 3
+  v += moved<0x143, 0xC>(v);  // the last lane of row 1 to rows 2 and 3
+  return v;
 }
 
 struct Hist {
   u64 mass[kBins * kCopies];
   uint32_t count[kBins * kCopies];
+  u64 wave_mass[kSumWaves];
+  uint32_t wave_count[kSumWaves];
 };
 // What a workgroup that answers a row's questions shares.
 struct Shared {
@@ -225,6 +254,10 @@ struct RowSource {
   __device__ __forceinline__ int skip() const { return (int)(((uintptr_t)p & 15) / sizeof(T)); }
   __device__ __forceinline__ int pieces() const { return (n + skip() + E - 1) / E; }
   __device__ __forceinline__ int begin(int c) const { return c * E - skip(); }
+  __device__ __forceinline__ float one(int i) const {
+    return sizeof(T) == 4 ? __builtin_bit_cast(float, (uint32_t)p[i])
+                          : __uint_as_float((uint32_t)p[i] << 16);
+  }
   __device__ __forceinline__ void load(int c, float (&v)[E]) const {
     const int at = begin(c);
     if (at >= 0 && at + E <= n) {
@@ -239,10 +272,7 @@ struct RowSource {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const bool in = at + j >= 0 && at + j < n;
-        const T x = in ? p[at + j] : T(0);
-        v[j] = !in              ? kNegInf
-               : sizeof(T) == 4 ? __builtin_bit_cast(float, (uint32_t)x)
-                                : __uint_as_float((uint32_t)x << 16);
+        v[j] = in ? one(at + j) : kNegInf;
       }
     }
 #pragma unroll
@@ -286,6 +316,27 @@ struct HeldSource {
     for (int j = 0; j < N; ++j)
 #pragma unroll
       for (int i = 0; i < E; ++i) f(v[j][i], at + j * (int)blockDim.x * E + i);
+  }
+  // f(place, logit, index) for those that `in` picks: a wave takes its places
+  // from `counter` at once.  They are few, and read again.
+  template <typename In, typename F>
+  __device__ __forceinline__ void pick(const RowSource<T> &src, int *counter, In &&in, F &&f) const {
+    static_assert(N * E <= 32, "a bit each");
+    uint32_t mask = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) mask |= in(v[j][i]) ? 1u << (j * E + i) : 0u;
+    if (!__any(mask != 0)) return;
+    const uint32_t mine = __popc(mask), upto = running_sum(mine);
+    int place = 0;
+    if ((threadIdx.x & 63) == 63) place = atomicAdd(counter, (int)upto);
+    place = __builtin_amdgcn_readlane(place, 63) + (int)(upto - mine);
+    for (; mask; mask &= mask - 1, ++place) {
+      const int bit = __builtin_ctz(mask);
+      const int index = at + bit / E * (int)blockDim.x * E + bit % E;
+      f(place, logit_of(src.one(index)), index);
+    }
   }
 };
 
@@ -332,45 +383,36 @@ __device__ __forceinline__ void add_to_bin(Hist &h, int bin, u64 w, uint32_t n) 
   if (n) atomicAdd(&h.count[at], n);
 }
 // Running sums over the histogram's bins (between barriers of its own).
-__device__ __forceinline__ void sum_histogram(const Hist &h, Sums &to) {
+__device__ __forceinline__ void sum_histogram(Hist &h, Sums &to) {
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
-    u64 m = 0;
-    uint32_t c = 0;
+  const int t = threadIdx.x, wave = uniform(t >> 6);
+  u64 m0 = 0, m1 = 0, m = 0;
+  uint32_t c0 = 0, c1 = 0, c = 0;
+  if (wave < kSumWaves) {
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) {
-      m += h.mass[i * kCopies + k];
-      c += h.count[i * kCopies + k];
+      m0 += h.mass[2 * t * kCopies + k];
+      m1 += h.mass[(2 * t + 1) * kCopies + k];
+      c0 += h.count[2 * t * kCopies + k];
+      c1 += h.count[(2 * t + 1) * kCopies + k];
     }
-    to.mass[i] = m;
-    to.count[i] = c;
+    m = running_sum(m0 + m1);
+    c = running_sum(c0 + c1);
+    if ((t & 63) == 63) {
+      h.wave_mass[wave] = m;
+      h.wave_count[wave] = c;
+    }
   }
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    u64 m[kLaneBins];
-    uint32_t c[kLaneBins];
-#pragma unroll
-    for (int i = 0; i < kLaneBins; ++i) {
-      m[i] = to.mass[kLaneBins * lane + i] + (i ? m[i - 1] : 0);
-      c[i] = to.count[kLaneBins * lane + i] + (i ? c[i - 1] : 0);
+  if (wave < kSumWaves) {
+    for (int w = 0; w < wave; ++w) {
+      m += h.wave_mass[w];
+      c += h.wave_count[w];
     }
-    u64 ms = m[kLaneBins - 1];
-    uint32_t cs = c[kLaneBins - 1];
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 mo = shfl_up_u64(ms, off);
-      const uint32_t co = (uint32_t)__shfl_up((int)cs, off);
-      if (lane >= off) {
-        ms += mo;
-        cs += co;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kLaneBins; ++i) {
-      to.mass[kLaneBins * lane + i] = ms - m[kLaneBins - 1] + m[i];
-      to.count[kLaneBins * lane + i] = cs - c[kLaneBins - 1] + c[i];
-    }
+    to.mass[2 * t] = m - m1;
+    to.mass[2 * t + 1] = m;
+    to.count[2 * t] = c - c1;
+    to.count[2 * t + 1] = c;
   }
   __syncthreads();
 }
@@ -562,15 +604,19 @@ struct Ask {
 };
 
 __device__ __forceinline__ Ask ask_of(const SampleArgs &a, int at) {
+  // all loads at once, u's in place of one that is not given
+  const auto given = [&](const float *x) { return (x ? x : a.u)[at]; };
+  const float u = a.u[at], t = given(a.temperature), p0 = given(a.top_p), m0 = given(a.min_p);
+  const int k0 = __float_as_int(given(reinterpret_cast<const float *>(a.top_k)));
   Ask q;
-  q.temperature = a.temperature ? a.temperature[at] : 1.f;
-  const int k = a.top_k ? a.top_k[at] : 0;
+  q.temperature = a.temperature ? t : 1.f;
+  const int k = a.top_k ? k0 : 0;
   q.top_k = k > 0 && k < a.vocab ? k : 0;
-  const float p = a.top_p ? a.top_p[at] : 1.f;
+  const float p = a.top_p ? p0 : 1.f;
   q.nucleus = p < 1.f;
   q.top_p = fraction(p);
-  q.u = fraction(a.u[at]);
-  const float m = a.min_p ? a.min_p[at] : 0.f;
+  q.u = fraction(u);
+  const float m = a.min_p ? m0 : 0.f;
   q.min_p = !(m > 0.f) ? 0.f : fminf(m, 1.f);
   q.least = (u64)__builtin_ceil(__builtin_ldexp((double)q.min_p, a.bits));
   return q;
@@ -660,16 +706,27 @@ __device__ __forceinline__ Found answer(const S &src, Shared &sh, const Row &row
   return f;
 }
 
-// The tokens of a source that `in` picks, into the list.  Their number: where
-// it is more than kList, the list is of no use.
-template <typename S, typename F>
-__device__ __forceinline__ int list_tokens(const S &src, Shared &sh, F &&in) {
+// f(place, logit, index) for the tokens of a source that `in` picks.
+template <typename T, int N, typename In, typename F>
+__device__ __forceinline__ void pick(const HeldSource<T, N> &src, const RowSource<T> &again, int *counter,
+                                     In &&in, F &&f) {
+  src.pick(again, counter, in, f);
+}
+template <typename S, typename L, typename In, typename F>
+__device__ __forceinline__ void pick(const S &src, const L &, int *counter, In &&in, F &&f) {
+  src.each([&](float v, int i) {
+    if (in(v)) f(atomicAdd(counter, 1), v, i);
+  });
+}
+
+// Those tokens into the list.  Their number: where it is more than kList, the
+// list is of no use.
+template <typename S, typename L, typename In>
+__device__ __forceinline__ int list_tokens(const S &src, const L &again, Shared &sh, In &&in) {
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
-  src.each([&](float v, int i) {
-    if (!in(v)) return;
-    const int j = atomicAdd(&sh.n_list, 1);
+  pick(src, again, &sh.n_list, in, [&](int j, float v, int i) {
     if (j < kList) {
       sh.key[j] = key_of(v);
       sh.index[j] = i;
@@ -688,10 +745,10 @@ __device__ __forceinline__ u64 bins_of(const S &src, Shared &sh, const Row &row,
   clear_histogram(sh.hist);
   __syncthreads();
   u64 mass_min = 0;
+  const bool counts = q.top_k != 0;
   src.each([&](float v, int) {
-    if (!(v > kNegInf)) return;
     const u64 w = weight(row, v);
-    add_to_bin(sh.hist, bin_of(row, v), w, q.top_k != 0);
+    add_to_bin(sh.hist, bin_of(row, v), w, counts && v > kNegInf);
     if (w >= q.least) mass_min += w;
   });
 #pragma unroll
@@ -703,9 +760,70 @@ __device__ __forceinline__ u64 bins_of(const S &src, Shared &sh, const Row &row,
   return mass_min;
 }
 
+// The same where the list is no longer than a workgroup: a thread a token finds
+// its rank by comparing with all of them, and with weights and running sums in
+// that order every question is one comparison a thread.
+__device__ __forceinline__ Found sorted_row(Shared &sh, int n, const Row &row, const Ask &q,
+                                            bool all_here, u64 all, u64 *whole) {
+  const int t = threadIdx.x, wave = uniform(t >> 6);
+  u64 *const code = sh.hist.mass;   // logit, then the lower index
+  u64 *const upto = sh.bins.mass;   // (both sums' arrays: 1024 of them)
+  static_assert(kBins * kCopies >= kWide && 2 * sizeof(Sums) >= 8 * kWide, "a token a thread");
+  __syncthreads();
+  const uint32_t key = t < n ? sh.key[t] : 0;
+  const int index = t < n ? sh.index[t] : 0;
+  const u64 mine = (u64)key << 32 | (uint32_t)~index;
+  code[t] = t < n ? mine : 0;
+  if (t == 0) sh.upto = 0;
+  __syncthreads();
+  int rank = 0;
+  if (wave * 64 < n) {
+    for (int i = 0; i < n; i += 8) {  // (codes behind the list are 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) rank += code[i + j] > mine;
+    }
+  }
+  if (t < n) {
+    sh.key[rank] = key;
+    sh.index[rank] = index;
+  }
+  __syncthreads();
+  const u64 w = t < n ? weight(row, value_of(sh.key[t])) : 0;
+  const int place = t < n ? sh.index[t] : 0;
+  u64 sum = running_sum(w);
+  if ((t & 63) == 63) sh.sum[wave] = sum;
+  __syncthreads();
+  for (int i = 0; i < wave; ++i) sum += sh.sum[i];
+  upto[t] = sum;
+  // the last that weighs min_p (weights fall with the order, but for their rounding)
+  const uint64_t heavy = __ballot(t < n && w >= q.least);
+  if (heavy && (t & 63) == 63 - __builtin_clzll(heavy)) atomicMax(&sh.upto, sum);
+  __syncthreads();
+  const u64 here = upto[n - 1], mass_min = sh.upto;
+  u64 m = all_here ? here : all;
+  if (q.top_k && n > q.top_k) m = upto[q.top_k - 1];
+  if (q.nucleus) {
+    const u64 r = just_below(m, q.top_p);
+    if (sum > r && sum - w <= r) sh.own = sum;
+    __syncthreads();
+    m = min(m, r < here ? sh.own : here);
+  }
+  m = min(m, mass_min);
+  *whole = m;
+  const u64 r = __umul64hi(m, q.u);
+  __syncthreads();
+  if (sum > r && sum - w <= r) {
+    sh.own = w;
+    sh.token = place;
+  }
+  __syncthreads();
+  return Found{0, sh.own, sh.token};
+}
+
 // A row of which all that may stay is in the list.
 __device__ __forceinline__ Found listed_row(Shared &sh, int n, const Row &row, const Ask &q,
                                             bool all_here, u64 all, u64 *whole) {
+  if (n <= (int)blockDim.x) return sorted_row(sh, n, row, q, all_here, all, whole);
   const ListSource list{sh, n};
   const u64 mass_min = bins_of(list, sh, row, q);
   return answer(list, sh, row, q, all_here ? sh.bins.mass[kBins - 1] : all, mass_min, whole);
@@ -719,53 +837,52 @@ __device__ __forceinline__ Found whole_row(const S &src, const L &long_way, Shar
                                            u64 *whole) {
   const u64 mass_min = bins_of(src, sh, row, q);
   if (all_here) all = sh.bins.mass[kBins - 1];
-  const int n = list_tokens(src, sh, Needed(row, need_of(sh.bins, row, q, all, mass_min, true)));
+  const int n = list_tokens(src, long_way, sh, Needed(row, need_of(sh.bins, row, q, all, mass_min, true)));
   return n <= kList ? answer(ListSource{sh, n}, sh, row, q, all, mass_min, whole)
                     : answer(long_way, sh, row, q, all, mass_min, whole);
 }
 
-// What can be among the first top_k, or weigh min_p: logits from `least` on, in
-// bins to `last`.  Of the first top_k of a row its part in this workgroup has
-// at most its own first top_k, and where so many of its threads' largest
-// logits (of each half of what a thread holds) lie in the bins to one, they
+// What can be among the first top_k, or weigh min_p: logits of which `scale`
+// times is `least` or more.  Of the first top_k of a row its part in this workgroup
+// has at most its own first top_k, and where so many of its threads' largest
+// logits (of each half of what a thread holds) lie in the bins to `last`, they
 // do.  (min_p is taken a little lower than it is, by far more than anything is
 // rounded.)
 struct Limits {
-  float least;
+  float scale, least;
   int last;
-  __device__ __forceinline__ bool operator()(const Row &row, float v) const {
-    return v > kNegInf && v >= least && bin_of(row, v) <= last;
+  __device__ __forceinline__ bool operator()(float v) const {
+    return v > kNegInf && v * scale >= least;
   }
 };
-__device__ __forceinline__ float least_of(const Row &row, const Ask &q) {
+__device__ __forceinline__ Limits limits_of(const Row &row, const Ask &q, int last) {
+  if (q.few()) return {row.bin_rate, last == kBins - 1 ? kNegInf : row.base - (float)last, last};
+  if (!(q.min_p > 0.f)) return {1.f, kNegInf, kBins - 1};
   const double t = (double)q.temperature;
-  return __double2float_rd((double)row.largest + log((double)q.min_p) * t * (1.0 + 1e-6) - 1e-6 * t);
+  return {1.f,
+          __double2float_rd((double)row.largest + log((double)q.min_p) * t * (1.0 + 1e-6) - 1e-6 * t),
+          kBins - 1};
 }
 template <typename T, int N>
 __device__ __forceinline__ Limits limits_of(const HeldSource<T, N> &src, const Row &row,
                                             const Ask &q, Hist &hist, Sums &sums) {
-  Limits l{kNegInf, kBins - 1};
-  if (q.few()) {
-    clear_histogram(hist);
-    __syncthreads();
-    constexpr int E = RowSource<T>::E;
-    float top[2] = {kNegInf, kNegInf};
+  if (!q.few()) return limits_of(row, q, kBins - 1);
+  clear_histogram(hist);
+  __syncthreads();
+  constexpr int E = RowSource<T>::E;
+  float top[2] = {kNegInf, kNegInf};
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+  for (int j = 0; j < N; ++j)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int h = N > 1 ? 2 * j / N : 2 * i / E;
-        top[h] = fmaxf(top[h], src.v[j][i]);
-      }
+    for (int i = 0; i < E; ++i) {
+      const int h = N > 1 ? 2 * j / N : 2 * i / E;
+      top[h] = fmaxf(top[h], src.v[j][i]);
+    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (top[h] > kNegInf) add_to_bin(hist, bin_of(row, top[h]), 0, 1);
-    sum_histogram(hist, sums);
-    l.last = bin_over(sums, (u64)(q.top_k - 1), true);
-  } else if (q.min_p > 0.f) {
-    l.least = least_of(row, q);
-  }
-  return l;
+  for (int h = 0; h < 2; ++h)
+    if (top[h] > kNegInf) add_to_bin(hist, bin_of(row, top[h]), 0, 1);
+  sum_histogram(hist, sums);
+  return limits_of(row, q, bin_over(sums, (u64)(q.top_k - 1), true));
 }
 
 __device__ __forceinline__ void write(const SampleArgs &a, int at, int token, float prob) {
@@ -827,10 +944,8 @@ __global__ __launch_bounds__(kWide) void k_sample_row(SampleArgs a) {
   const Row row = row_of(best, q.temperature, a.bits);
   u64 whole;
   Found f;
-  // (where one is +inf, what the others are told by is no number)
-  if (!q.all() && q.listed() && best < -kNegInf) {
-    const Limits l = limits_of(held, row, q, sh.hist, sh.digits);
-    const int n = list_tokens(held, sh, [&](float v) { return l(row, v); });
+  if (!q.all() && q.listed()) {
+    const int n = list_tokens(held, src, sh, limits_of(held, row, q, sh.hist, sh.digits));
     f = n <= kList ? listed_row(sh, n, row, q, true, 0, &whole)
                    : whole_row(src, src, sh, row, q, true, 0, &whole);
   } else {
@@ -856,8 +971,9 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   const int slice = blockIdx.x, at = a.row0 + blockIdx.y;
   const size_t rs = (size_t)blockIdx.y * a.slices + slice;
   if (slice == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.active[0] = 0;
+  const RowSource<T> src = logits_of<T>(a, at);
   HeldSource<T, kPieces<T>> held;
-  held.load(logits_of<T>(a, at), slice);
+  held.load(src, slice);
   const Ask q = ask_of(a, at);
   float best;
   int first;
@@ -865,7 +981,7 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   if (threadIdx.x == 0) sh_listed = 0;
   first_largest(sh_best, sh_first, best, first);
   SliceHead head{best, first, 0.f, false, 0, 0, kBins - 1, 0};
-  if (best == kNegInf || best == -kNegInf || q.greedy()) {
+  if (best == kNegInf || q.greedy()) {
     if (threadIdx.x == 0) a.heads[rs] = head;
     return;
   }
@@ -875,9 +991,7 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   if (listed) {
     const Limits l = limits_of(held, row, q, hist, sums);
     head.last = l.last;
-    held.each([&](float v, int i) {
-      if (!l(row, v)) return;
-      const int n = atomicAdd(&sh_listed, 1);
+    held.pick(src, &sh_listed, l, [&](int n, float v, int i) {
       if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key_of(v), (uint32_t)i);
     });
     __syncthreads();
@@ -890,21 +1004,12 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   head.binned = true;
   clear_histogram(hist);
   __syncthreads();
-  u64 total = 0;
+  const bool counts = q.top_k != 0;
   held.each([&](float v, int) {
-    if (!(v > kNegInf)) return;
-    const u64 w = weight(row, v);
-    total += w;
-    add_to_bin(hist, bin_of(row, v), w, q.top_k != 0);
+    add_to_bin(hist, bin_of(row, v), weight(row, v), counts && v > kNegInf);
   });
-#pragma unroll
-  for (int off = 32; off; off >>= 1) total += shfl_u64(total, lane ^ off);
-  if (lane == 0) sh_sum[wave] = total;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kNarrow / 64; ++w) head.total += sh_sum[w];
-    a.heads[rs] = head;
-  }
+  u64 total = 0;
   for (int i = threadIdx.x; i < kBins; i += kNarrow) {
     u64 m = 0;
     uint32_t c = 0;
@@ -915,6 +1020,14 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
     }
     a.mass[rs * kBins + i] = m;
     a.count[rs * kBins + i] = c;
+    total += m;
+  }
+  total = running_sum(total);
+  if (lane == 63) sh_sum[wave] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kNarrow / 64; ++w) head.total += sh_sum[w];
+    a.heads[rs] = head;
   }
 }
 
@@ -981,11 +1094,7 @@ __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row 
     for (int i = lane; i < kBins; i += 64) {
       const u64 m = a.mass[rs * kBins + i];
       const uint32_t c = a.count[rs * kBins + i];
-      // (bases that are no numbers: the last bin, as bin_of has it)
-      const float b = (float)i + (row.base - h.base);
-      if (m | c)
-        add_to_bin(hist, h.largest == row.largest ? i : (int)fminf(b, (float)(kBins - 1)),
-                   scaled(m, factor), c);
+      if (m | c) add_to_bin(hist, row_bin(row, h.base, i), scaled(m, factor), c);
     }
   }
   sum_histogram(hist, to);
@@ -1003,34 +1112,25 @@ __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   if (q.greedy()) return write(a, at, joined.first, 1.f);
   const Row row = row_of(joined.largest, q.temperature, a.bits);
   u64 whole;
-  if (joined.largest == -kNegInf || joined.whole) {
-    Found f;
-    const RowSource<T> src = logits_of<T>(a, at);
-    if (joined.whole && joined.largest < -kNegInf) {
-      // all weights, and what the slices' own first top_k leave for the row's
-      u64 all = 0;
-      float last = kBins - 1;
-      for (int s = lane; s < a.slices; s += 64) {
-        const SliceHead h = heads[s];
-        if (!(h.largest > kNegInf)) continue;
-        all += scaled(h.total, slice_factor(row, h.largest));
-        last = fminf(last, h.largest == row.largest ? (float)h.last
-                                                    : (float)h.last + (row.base - h.base));
-      }
-#pragma unroll
-      for (int off = 32; off; off >>= 1) {
-        all += shfl_u64(all, lane ^ off);
-        last = fminf(last, __shfl_xor(last, off));
-      }
-      const Limits l{q.few() || !(q.min_p > 0.f) ? kNegInf : least_of(row, q),
-                     q.few() ? (int)last : kBins - 1};
-      const GatherSource gather{heads, a.list + (size_t)r * a.slices * kSliceList, a.slices, false};
-      const int n = list_tokens(gather, sh, [&](float v) { return l(row, v); });
-      f = n <= kList ? listed_row(sh, n, row, q, !q.all(), all, &whole)
-                     : whole_row(gather, gather, sh, row, q, !q.all(), all, &whole);
-    } else {
-      f = whole_row(src, src, sh, row, q, true, 0, &whole);
+  if (joined.whole) {
+    // all weights, and what the slices' own first top_k leave for the row's
+    u64 all = 0;
+    int last = kBins - 1;
+    for (int s = lane; s < a.slices; s += 64) {
+      const SliceHead h = heads[s];
+      if (!(h.largest > kNegInf)) continue;
+      if (q.all()) all += scaled(h.total, slice_factor(row, h.largest));
+      last = min(last, row_bin(row, h.base, h.last));
     }
+#pragma unroll
+    for (int off = 32; off; off >>= 1) {
+      if (q.all()) all += shfl_u64(all, lane ^ off);
+      last = min(last, __shfl_xor(last, off));
+    }
+    const GatherSource gather{heads, a.list + (size_t)r * a.slices * kSliceList, a.slices, false};
+    const int n = list_tokens(gather, gather, sh, limits_of(row, q, last));
+    const Found f = n <= kList ? listed_row(sh, n, row, q, !q.all(), all, &whole)
+                               : whole_row(gather, gather, sh, row, q, !q.all(), all, &whole);
     return write(a, at, f.token, (float)((double)f.own / (double)whole));
   }
   join_bins(a, r, row, q, sh.hist, sh.bins);
@@ -1056,17 +1156,15 @@ __global__ __launch_bounds__(kNarrow) void k_sample_collect(SampleArgs a) {
   for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
     const int r = a.active[1 + task / a.slices], slice = task % a.slices, at = a.row0 + r;
     const size_t rs = (size_t)r * a.slices + slice;
+    const RowSource<T> src = logits_of<T>(a, at);
     HeldSource<T, kPieces<T>> held;
-    held.load(logits_of<T>(a, at), slice);
+    held.load(src, slice);
     if (threadIdx.x == 0) sh_n = 0;
     __syncthreads();
     const Needed needed(row_of(a.state[r].largest, a.temperature ? a.temperature[at] : 1.f, a.bits),
                         a.state[r].need);
-    held.each([&](float v, int i) {
-      if (needed(v)) {
-        const int n = atomicAdd(&sh_n, 1);
-        if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key_of(v), (uint32_t)i);
-      }
+    held.pick(src, &sh_n, needed, [&](int n, float v, int i) {
+      if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key_of(v), (uint32_t)i);
     });
     __syncthreads();
     if (threadIdx.x == 0) a.heads[rs].collected = sh_n;
