@@ -30,7 +30,7 @@
 //                     the bins that the questions fall into
 //   k_sample_collect  the tokens of those bins (these rows are read once more)
 //   k_sample_pick     a workgroup a row: the questions
-// A slice's weights are relative to its own largest logit, and scaled where
+// A slice's weights are relative to a power of two of its own, and shifted where
 // the slices of a row come together.
 #include "../../include/rfpx_verify.h"
 #include "rfpx_impl.hpp"
@@ -56,21 +56,24 @@ constexpr uint32_t kNoToken = 0x007FFFFFu;  // key of -inf, which NaN gets too
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kRowMost = 32 * kWide;  // logits of a row that is not cut into slices
 constexpr int kSlice = 32 * kNarrow;  // logits of a slice
-constexpr int kSliceList = 512;       // tokens that a slice may list
+constexpr int kSliceList = kMiddle;   // tokens that a slice may list
+static_assert(kBins == kMiddle, "a thread a bin");
 constexpr int kMostSlices = RFPX_VOCAB_MAX / kSlice + 1;
 constexpr int kTopMost = 256;     // top_k of rows whose slices list their tokens
 constexpr int kRowsAtOnce = 512;  // rows of one set of launches, which bounds the workspace
 
 // What k_sample_slices says of a slice.
 struct SliceHead {
+  double ref;  // of its weights
+  u64 total;   // their sum, where they stand by bin
   float largest;
   int first;   // its first place
   float base;  // of its bins
-  bool binned; // its weights stand by bin
-  u64 total;   // ... and this is their sum
+  int binned;  // its weights stand by bin
   int listed;  // tokens that had to be listed (more than kSliceList: the list is not whole)
   int last;    // the first top_k are in bins up to this one
-  int collected;  // ... by k_sample_collect
+  int collected;  // tokens that k_sample_collect had to list
+  int none;
 };
 
 // Bins whose tokens the questions need one by one: of min_p's and top_k's, and
@@ -126,47 +129,26 @@ __device__ __forceinline__ float logit_of(float x) {
 // What weights and bins of a row, or a slice of it, are relative to.
 struct Row {
   float largest;
-  double rate;     // log2(e) / temperature
   float bin_rate;  // bins a logit
   float base;      // the largest logit's bin, counted from 0
   int bits;
+  bool far;        // nothing but the largest logit weighs anything
+  double rate;     // log2(e) / temperature
+  double ref;      // a whole number, the largest logit times rate or above
 };
 
 __device__ __forceinline__ Row row_of(float largest, float temperature, int bits) {
   Row r;
   r.largest = largest;
   r.rate = 1.4426950408889634 / (double)temperature;
-  r.bin_rate = fminf((float)r.rate * kBinsPerOctave, 3.0e38f);
+  // (above 0, so that -inf is in the last bin at any temperature)
+  r.bin_rate = fmaxf(fminf((float)r.rate * kBinsPerOctave, 3.0e38f), 1.17549435e-38f);
   r.base = floorf(largest * r.bin_rate);
   r.bits = bits;
+  r.ref = __builtin_ceil((double)largest * r.rate);
+  // (from 2^40 on the next smaller logit is more than 2^15 octaves below)
+  r.far = !(__builtin_fabs(r.ref) < 1099511627776.0) || !(r.rate < 1.2676506002282294e30);
   return r;
-}
-
-// exp((v - largest) / temperature) in units of 2^-bits, rounded to the nearest:
-// 2^f, |f| <= 1/2, by the polynomial 1 + f q(f) of degree 10 of least relative
-// error (3e-16, by Remez' exchange).  Whole numbers are had by adding 1.5 * 2^52
-// and 2^52, which leaves them in the low bits; 2^n goes into the exponent.  A
-// logit of -inf weighs 0.
-__device__ __forceinline__ u64 weight(const Row &r, float v) {
-#pragma clang fp contract(off)
-  const double x = __builtin_fmax(((double)v - (double)r.largest) * r.rate, -64.0);
-  const double whole = 6755399441055744.0 + (double)r.bits;
-  const double t = x + whole, f = x - (t - whole);
-  double p = 7.11174936174289645e-09;
-  p = __builtin_fma(p, f, 1.02105059849407951e-07);
-  p = __builtin_fma(p, f, 1.32152356871880181e-06);
-  p = __builtin_fma(p, f, 1.52526477502981718e-05);
-  p = __builtin_fma(p, f, 1.54035308007198697e-04);
-  p = __builtin_fma(p, f, 1.33335582464760177e-03);
-  p = __builtin_fma(p, f, 9.61812910738078439e-03);
-  p = __builtin_fma(p, f, 5.55041086643466158e-02);
-  p = __builtin_fma(p, f, 2.40226506959104719e-01);
-  p = __builtin_fma(p, f, 6.93147180559951614e-01);
-  p = __builtin_fma(p, f, 1.0);
-  const u64 u = __builtin_bit_cast(u64, p);
-  const uint32_t hi = (uint32_t)(u >> 32) + ((uint32_t)__builtin_bit_cast(u64, t) << 20);
-  const double y = __builtin_bit_cast(double, (u64)hi << 32 | (uint32_t)u) + 4503599627370496.0;
-  return __builtin_bit_cast(u64, y) & 0xFFFFFFFFFFFFFull;
 }
 
 // The bin of a logit: no larger for a larger one.  Whole numbers of the logit
@@ -181,6 +163,41 @@ __device__ __forceinline__ int row_bin(const Row &r, float slice_base, int i) {
   return slice_base == r.base ? i : (int)fminf((float)i + (r.base - slice_base), (float)(kBins - 1));
 }
 
+// 2^(v rate - ref) in units of 2^-bits, rounded to the nearest, of a logit that
+// is not in the last bin (what is weighs less than half a unit).  With v rate = m
+// + f, m whole and |f| <= 1/2, 2^f is the polynomial 1 + f q(f) of degree 10 of
+// least relative error (3e-16, by Remez' exchange); the product is never rounded.
+// Adding 1.5 * 2^52, less ref and plus bits, leaves the exponent in the low bits;
+// adding 2^52 leaves the result there.
+__device__ __forceinline__ u64 near_weight(const Row &r, float v) {
+#pragma clang fp contract(off)
+  const double whole = 6755399441055744.0 + ((double)r.bits - r.ref);
+  const double t = __builtin_fma((double)v, r.rate, whole);
+  const double f = __builtin_fma((double)v, r.rate, -(t - whole));
+  double p = 7.11174936174289645e-09;
+  p = __builtin_fma(p, f, 1.02105059849407951e-07);
+  p = __builtin_fma(p, f, 1.32152356871880181e-06);
+  p = __builtin_fma(p, f, 1.52526477502981718e-05);
+  p = __builtin_fma(p, f, 1.54035308007198697e-04);
+  p = __builtin_fma(p, f, 1.33335582464760177e-03);
+  p = __builtin_fma(p, f, 9.61812910738078439e-03);
+  p = __builtin_fma(p, f, 5.55041086643466158e-02);
+  p = __builtin_fma(p, f, 2.40226506959104719e-01);
+  p = __builtin_fma(p, f, 6.93147180559951614e-01);
+  p = __builtin_fma(p, f, 1.0);
+  typedef uint32_t words_t __attribute__((ext_vector_type(2)));
+  words_t u = __builtin_bit_cast(words_t, p);
+  u[1] += __builtin_bit_cast(words_t, t)[0] << 20;
+  words_t y = __builtin_bit_cast(words_t, __builtin_bit_cast(double, u) + 4503599627370496.0);
+  y[1] &= 0xFFFFFu;
+  return __builtin_bit_cast(u64, y);
+}
+__device__ __forceinline__ u64 weight(const Row &r, float v, int bin) {
+  if (r.far) return v == r.largest ? 1ull << r.bits : 0;
+  return bin < kBins - 1 ? near_weight(r, v) : 0;
+}
+__device__ __forceinline__ u64 weight(const Row &r, float v) { return weight(r, v, bin_of(r, v)); }
+
 // x as a fraction of 2^64, below 1.
 __device__ __forceinline__ u64 fraction(float x) {
   if (!(x > 0.f)) return 0;
@@ -193,33 +210,52 @@ __device__ __forceinline__ u64 just_below(u64 whole, u64 part) {
   return whole * part ? hi : hi ? hi - 1 : 0;
 }
 
-__device__ __forceinline__ u64 shfl_u64(u64 v, int lane) {
-  return ((u64)(uint32_t)__shfl((int)(v >> 32), lane) << 32) | (uint32_t)__shfl((int)v, lane);
-}
-
-// Running sums over the lanes of a wave, by data-parallel moves: within rows of
-// 16 lanes, then from row to row.
+// Over the lanes of a wave by data-parallel moves, within rows of 16 lanes and
+// then from row to row: the last lane has seen all of them.
 template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t moved(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+__device__ __forceinline__ uint32_t moved(uint32_t v, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
 }
 template <int CTRL, int ROWS>
-__device__ __forceinline__ u64 moved(u64 v) {
-  return ((u64)moved<CTRL, ROWS>((uint32_t)(v >> 32)) << 32) | moved<CTRL, ROWS>((uint32_t)v);
+__device__ __forceinline__ u64 moved(u64 v, u64 none) {
+  return ((u64)moved<CTRL, ROWS>((uint32_t)(v >> 32), (uint32_t)(none >> 32)) << 32) |
+         moved<CTRL, ROWS>((uint32_t)v, (uint32_t)none);
+}
+template <typename U, typename F>
+__device__ __forceinline__ U running(U v, U none, F &&f) {
+  v = f(v, moved<0x111, 0xF>(v, none));  // from 1, 2, 4, 8 lanes below
+  v = f(v, moved<0x112, 0xF>(v, none));
+  v = f(v, moved<0x114, 0xF>(v, none));
+  v = f(v, moved<0x118, 0xF>(v, none));
+  v = f(v, moved<0x142, 0xA>(v, none));  // the last lane of row 0 to row 1, of 2 to 3
+  v = f(v, moved<0x143, 0xC>(v, none));  // the last lane of row 1 to rows 2 and 3
+  return v;
 }
 template <typename U>
 __device__ __forceinline__ U running_sum(U v) {
-  v += moved<0x111, 0xF>(v);  // from 1, 2, 4, 8 lanes below
-  v += moved<0x112, 0xF>(v);
-  v += moved<0x114, 0xF>(v);
-  v += moved<0x118, 0xF>(v);
-  v += moved<0x142, 0xA>(v);  // the last lane of row 0 to row 1, of 2 to 3
-  v += moved<0x143, 0xC>(v);  // the last lane of row 1 to rows 2 and 3
-  return v;
+  return running(v, (U)0, [](U a, U b) { return a + b; });
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ u64 lane_of(u64 v, int lane) {
+  return (u64)lane_of((uint32_t)(v >> 32), lane) << 32 | lane_of((uint32_t)v, lane);
+}
+template <typename U>
+__device__ __forceinline__ U wave_sum(U v) {
+  return lane_of(running_sum(v), 63);
+}
+template <typename U>
+__device__ __forceinline__ U wave_max(U v) {
+  return lane_of(running(v, (U)0, [](U a, U b) { return a > b ? a : b; }), 63);
+}
+template <typename U>
+__device__ __forceinline__ U wave_min(U v) {
+  return ~wave_max((U)~v);
 }
 
 struct Hist {
-  u64 mass[kBins * kCopies];
+  alignas(16) u64 mass[kBins * kCopies];
   uint32_t count[kBins * kCopies];
   u64 wave_mass[kSumWaves];
   uint32_t wave_count[kSumWaves];
@@ -232,14 +268,16 @@ struct Shared {
   uint32_t key[kList];
   int32_t index[kList];
   u64 sum[kMostWaves];
-  float best[kMostWaves];
-  int32_t first[kMostWaves];
   uint32_t small_key[kSmall];
   int32_t small_index[kSmall];
   // answers of wave 0
   u64 upto, own;
   uint32_t in_count, key_lo, key_hi;
   int n_list, n_small, token;
+  // of a row's slices
+  int length[kMostSlices + 7];
+  float base[kMostSlices + 7];
+  int shift[kMostSlices + 7];
 };
 
 // -------------------------------------------------------- sources of tokens
@@ -258,25 +296,27 @@ struct RowSource {
     return sizeof(T) == 4 ? __builtin_bit_cast(float, (uint32_t)p[i])
                           : __uint_as_float((uint32_t)p[i] << 16);
   }
+  __device__ __forceinline__ bool inside(int c) const { return begin(c) >= 0 && begin(c) + E <= n; }
+  __device__ __forceinline__ uint4 words(int c) const {  // of a piece that is inside
+    return *reinterpret_cast<const uint4 *>(p + begin(c));
+  }
+  static __device__ __forceinline__ float logit(const uint4 &w, int j) {
+    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+    return logit_of(sizeof(T) == 4 ? __uint_as_float(d[j * sizeof(T) / 4])
+                    : j & 1        ? __uint_as_float(d[j / 2] & 0xFFFF0000u)
+                                   : __uint_as_float(d[j / 2] << 16));
+  }
   __device__ __forceinline__ void load(int c, float (&v)[E]) const {
-    const int at = begin(c);
-    if (at >= 0 && at + E <= n) {
-      const uint4 w = *reinterpret_cast<const uint4 *>(p + at);
-      const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+    if (inside(c)) {
+      const uint4 w = words(c);
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] = logit(w, j);
+    } else {
+      const int at = begin(c);
 #pragma unroll
       for (int j = 0; j < E; ++j)
-        v[j] = sizeof(T) == 4 ? __uint_as_float(d[j * sizeof(T) / 4])
-               : j & 1        ? __uint_as_float(d[j / 2] & 0xFFFF0000u)
-                              : __uint_as_float(d[j / 2] << 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const bool in = at + j >= 0 && at + j < n;
-        v[j] = in ? one(at + j) : kNegInf;
-      }
+        v[j] = at + j >= 0 && at + j < n ? logit_of(one(at + j)) : kNegInf;
     }
-#pragma unroll
-    for (int j = 0; j < E; ++j) v[j] = logit_of(v[j]);
   }
   // f(logit, index) for each; also for -inf.
   template <typename F>
@@ -290,35 +330,71 @@ struct RowSource {
   }
 };
 
-// Logits in registers: pieces first + N threads' ones of a row.
+// Logits in registers: pieces first + N threads' ones of a row.  Loops over them
+// are not unrolled (registers are indexed): a workgroup goes through them once or
+// twice, and would wait for its instructions.
 template <typename T, int N>
 struct HeldSource {
   static constexpr int E = RowSource<T>::E;
-  float v[N][E];
+  typedef float held_t __attribute__((ext_vector_type(N * E)));
+  held_t v;
   int at;  // of the first
   __device__ __forceinline__ void load(const RowSource<T> &src, int slice) {
-    const int c0 = slice * N * (int)blockDim.x + threadIdx.x, pieces = src.pieces();
+    const int first = slice * N * (int)blockDim.x, c0 = first + threadIdx.x;
     at = src.begin(c0);
+    if (src.inside(first) && src.inside(first + N * (int)blockDim.x - 1)) {
+      uint4 w[N];  // all loads in flight at once
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int c = c0 + j * (int)blockDim.x;
-      if (c < pieces) {
-        src.load(c, v[j]);
-      } else {
+      for (int j = 0; j < N; ++j) w[j] = src.words(c0 + j * (int)blockDim.x);
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[j][i] = kNegInf;
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[j * E + i] = src.logit(w[j], i);
+      return;
+    }
+    // the row begins or ends within: pieces outside are replaced by the last
+    // one inside, if there is one, and then by nothing
+    const int lo = src.inside(0) ? 0 : 1, hi = (src.n + src.skip()) / E - 1;
+    if (hi >= lo) {
+      uint4 w[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        w[j] = src.words(min(max(c0 + j * (int)blockDim.x, lo), hi));
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = c0 + j * (int)blockDim.x;
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[j * E + i] = c >= lo && c <= hi ? src.logit(w[j], i) : kNegInf;
       }
+    } else {
+      v = held_t(kNegInf);
+    }
+    // the pieces of which only a part is inside: the row's first and last
+    const int edge[2] = {0, src.pieces() - 1};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && edge[1] == 0) break;
+      const int j = (edge[k] - c0) / (int)blockDim.x;
+      if (src.inside(edge[k]) || edge[k] < c0 || (edge[k] - c0) % (int)blockDim.x || j >= N) continue;
+      float x[E];
+      src.load(edge[k], x);
+#pragma unroll
+      for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (b == j) v[b * E + i] = x[i];
     }
   }
   template <typename F>
   __device__ __forceinline__ void each(F &&f) const {
+#pragma unroll 1
+    for (int j = 0; j < N; ++j) {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int i = 0; i < E; ++i) f(v[j][i], at + j * (int)blockDim.x * E + i);
+      for (int i = 0; i < E; ++i) f(v[j * E + i], at + j * (int)blockDim.x * E + i);
+    }
   }
-  // f(place, logit, index) for those that `in` picks: a wave takes its places
-  // from `counter` at once.  They are few, and read again.
+  // f(place, key, index) for those that `in` picks: a wave takes its places from
+  // `counter` at once.  They are few, and read again.
   template <typename In, typename F>
   __device__ __forceinline__ void pick(const RowSource<T> &src, int *counter, In &&in, F &&f) const {
     static_assert(N * E <= 32, "a bit each");
@@ -326,7 +402,7 @@ struct HeldSource {
 #pragma unroll
     for (int j = 0; j < N; ++j)
 #pragma unroll
-      for (int i = 0; i < E; ++i) mask |= in(v[j][i]) ? 1u << (j * E + i) : 0u;
+      for (int i = 0; i < E; ++i) mask |= in(v[j * E + i]) ? 1u << (j * E + i) : 0u;
     if (!__any(mask != 0)) return;
     const uint32_t mine = __popc(mask), upto = running_sum(mine);
     int place = 0;
@@ -335,7 +411,7 @@ struct HeldSource {
     for (; mask; mask &= mask - 1, ++place) {
       const int bit = __builtin_ctz(mask);
       const int index = at + bit / E * (int)blockDim.x * E + bit % E;
-      f(place, logit_of(src.one(index)), index);
+      f(place, key_of(logit_of(src.one(index))), index);
     }
   }
 };
@@ -349,22 +425,51 @@ struct ListSource {
   }
 };
 
-// The lists of a row's slices.
+// The lists of a row's slices, whose lengths are in LDS: a thread a place in the
+// lists (kMiddle threads), eight slices' loads at once.
 struct GatherSource {
-  const SliceHead *heads;
   const uint2 *list;
+  const int *lengths;
   int slices;
-  bool collected;
+  __device__ __forceinline__ void load(int s0, uint2 (&e)[8]) const {
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      e[j] = s0 + j < slices && t < lengths[s0 + j] ? list[(size_t)(s0 + j) * kSliceList + t]
+                                                    : make_uint2(kNoToken, 0);
+  }
   template <typename F>
   __device__ __forceinline__ void each(F &&f) const {
-    // a wave a slice
-    const int lane = threadIdx.x & 63;
-    for (int s = threadIdx.x >> 6; s < slices; s += blockDim.x >> 6) {
-      const int n = collected ? heads[s].collected : heads[s].listed;
-      for (int i = lane; i < n; i += 64) {
-        const uint2 e = list[(size_t)s * kSliceList + i];
-        f(value_of(e.x), (int)e.y);
+#pragma unroll 1
+    for (int s0 = 0; s0 < slices; s0 += 8) {
+      uint2 e[8];
+      load(s0, e);
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        if (e[0].x > kNoToken) f(value_of(e[0].x), (int)e[0].y);
+#pragma unroll
+        for (int i = 0; i < 7; ++i) e[i] = e[i + 1];
       }
+    }
+  }
+  // f(place, key, index) for those that `in` picks: a wave takes its places from
+  // `counter` eight slices at a time.
+  template <typename In, typename F>
+  __device__ __forceinline__ void pick(int *counter, In &&in, F &&f) const {
+#pragma unroll 1
+    for (int s0 = 0; s0 < slices; s0 += 8) {
+      uint2 e[8];
+      load(s0, e);
+      uint32_t mask = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mask |= e[j].x > kNoToken && in(value_of(e[j].x)) ? 1u << j : 0u;
+      const uint32_t mine = __popc(mask), upto = running_sum(mine);
+      int place = 0;
+      if ((threadIdx.x & 63) == 63 && upto) place = atomicAdd(counter, (int)upto);
+      place = __builtin_amdgcn_readlane(place, 63) + (int)(upto - mine);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (mask >> j & 1u) f(place++, e[j].x, (int)e[j].y);
     }
   }
 };
@@ -464,12 +569,9 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
     sh.in_count = 0;
   }
   __syncthreads();
-#pragma unroll
-  for (int off = 32; off; off >>= 1) {
-    lo = min(lo, (uint32_t)__shfl_xor((int)lo, off));
-    hi = max(hi, (uint32_t)__shfl_xor((int)hi, off));
-    n += (uint32_t)__shfl_xor((int)n, off);
-  }
+  lo = wave_min(lo);
+  hi = wave_max(hi);
+  n = wave_sum(n);
   if (lane == 0 && n) {
     atomicMin(&sh.key_lo, lo);
     atomicMax(&sh.key_hi, hi);
@@ -550,29 +652,25 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
   __syncthreads();
   if (threadIdx.x < 64) {
     const int m = min(sh.n_small, kSmall);
-    const uint32_t k = lane < m ? sh.small_key[lane] : 0;
-    const int i = lane < m ? sh.small_index[lane] : 0x7FFFFFFF;
-    const u64 w = lane < m ? weight(row, value_of(k)) : 0;
-    u64 upto = 0;
-    uint32_t rank = 0;  // with itself
-    for (int j = 0; j < m; ++j) {
-      const uint32_t kj = (uint32_t)__shfl((int)k, j);
-      const int ij = __shfl(i, j);
-      const u64 wj = shfl_u64(w, j);
-      if (kj > k || (kj == k && ij <= i)) {
-        upto += wj;
-        ++rank;
-      }
+    const uint32_t key = lane < m ? sh.small_key[lane] : 0;
+    const int index = lane < m ? sh.small_index[lane] : 0;
+    const u64 code = lane < m ? (u64)key << 32 | (uint32_t)~index : 0;
+    int rank = 0;
+    for (int j = 0; j < m; ++j) rank += lane_of(code, j) > code;
+    if (lane < m) {
+      sh.small_key[rank] = key;
+      sh.small_index[rank] = index;
     }
-    const u64 sum = by_count ? (u64)rank : upto, own = by_count ? 1 : w;
-    const uint64_t last_one = __ballot(lane < m && rank == (uint32_t)m);
-    r = within(r, last_one ? shfl_u64(sum, __builtin_ctzll(last_one)) : 0);
-    const bool it = lane < m && sum > r && sum - own <= r;
-    const uint64_t lanes = __ballot(it);
-    if (lanes ? lane == __builtin_ctzll(lanes) : lane == 0) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    const u64 w = lane < m ? weight(row, value_of(sh.small_key[lane])) : 0;
+    const u64 upto = running_sum(w);
+    r = within(r, by_count ? (u64)m : lane_of(upto, 63));
+    const uint64_t lanes = __ballot(lane < m && (by_count ? (u64)lane + 1 : upto) > r);
+    if (lane == (lanes ? __builtin_ctzll(lanes) : 0)) {
       sh.upto = by_index ? above + w : above + upto;
       sh.own = w;
-      sh.token = i;
+      sh.token = m ? sh.small_index[lane] : -1;
     }
   }
   __syncthreads();
@@ -591,7 +689,6 @@ struct Ask {
   bool nucleus;      // a cut by top_p
   u64 top_p, u;      // fractions of 2^64
   float min_p;       // 0: no cut
-  u64 least;         // its weight
   __device__ __forceinline__ bool greedy() const { return !(temperature > 0.f) || top_k == 1; }
   // Slices list their tokens: the first top_k, or those of min_p
   __device__ __forceinline__ bool few() const { return top_k > 0 && top_k <= kTopMost; }
@@ -618,8 +715,12 @@ __device__ __forceinline__ Ask ask_of(const SampleArgs &a, int at) {
   q.u = fraction(u);
   const float m = a.min_p ? m0 : 0.f;
   q.min_p = !(m > 0.f) ? 0.f : fminf(m, 1.f);
-  q.least = (u64)__builtin_ceil(__builtin_ldexp((double)q.min_p, a.bits));
   return q;
+}
+
+// What a token of min_p weighs.
+__device__ __forceinline__ u64 least_weight(const Row &row, const Ask &q) {
+  return (u64)__builtin_ceil((double)weight(row, row.largest, 0) * (double)q.min_p);
 }
 
 __device__ __forceinline__ u64 before(const Sums &s, int bin) { return bin ? s.mass[bin - 1] : 0; }
@@ -649,7 +750,9 @@ __device__ __forceinline__ Need need_of(const Sums &s, const Row &row, const Ask
   Need n{0, -1, 0, -1, 0, -1, 0, -1};
   u64 min_lo = mass_min, min_hi = mass_min;
   if (!known && q.min_p > 0.f) {
-    const int b = bin_of(row, (float)((double)row.largest + log((double)q.min_p) * q.temperature));
+    // (the logarithm within 1e-5, the logit's place within a bin, 0.07 of a
+    // temperature, of what min_p says)
+    const int b = bin_of(row, (float)((double)row.largest + (double)__logf(q.min_p) * q.temperature));
     n.m0 = max(0, b - 1);
     n.m1 = min(kBins - 1, b + 1);
     min_lo = before(s, n.m0);
@@ -706,16 +809,20 @@ __device__ __forceinline__ Found answer(const S &src, Shared &sh, const Row &row
   return f;
 }
 
-// f(place, logit, index) for the tokens of a source that `in` picks.
+// f(place, key, index) for the tokens of a source that `in` picks.
 template <typename T, int N, typename In, typename F>
 __device__ __forceinline__ void pick(const HeldSource<T, N> &src, const RowSource<T> &again, int *counter,
                                      In &&in, F &&f) {
   src.pick(again, counter, in, f);
 }
-template <typename S, typename L, typename In, typename F>
-__device__ __forceinline__ void pick(const S &src, const L &, int *counter, In &&in, F &&f) {
+template <typename L, typename In, typename F>
+__device__ __forceinline__ void pick(const GatherSource &src, const L &, int *counter, In &&in, F &&f) {
+  src.pick(counter, in, f);
+}
+template <typename T, typename L, typename In, typename F>
+__device__ __forceinline__ void pick(const RowSource<T> &src, const L &, int *counter, In &&in, F &&f) {
   src.each([&](float v, int i) {
-    if (in(v)) f(atomicAdd(counter, 1), v, i);
+    if (in(v)) f(atomicAdd(counter, 1), key_of(v), i);
   });
 }
 
@@ -726,9 +833,9 @@ __device__ __forceinline__ int list_tokens(const S &src, const L &again, Shared 
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
-  pick(src, again, &sh.n_list, in, [&](int j, float v, int i) {
+  pick(src, again, &sh.n_list, in, [&](int j, uint32_t key, int i) {
     if (j < kList) {
-      sh.key[j] = key_of(v);
+      sh.key[j] = key;
       sh.index[j] = i;
     }
   });
@@ -746,14 +853,15 @@ __device__ __forceinline__ u64 bins_of(const S &src, Shared &sh, const Row &row,
   __syncthreads();
   u64 mass_min = 0;
   const bool counts = q.top_k != 0;
+  const u64 least = least_weight(row, q);
   src.each([&](float v, int) {
-    const u64 w = weight(row, v);
-    add_to_bin(sh.hist, bin_of(row, v), w, counts && v > kNegInf);
-    if (w >= q.least) mass_min += w;
+    const int b = bin_of(row, v);
+    const u64 w = weight(row, v, b);
+    add_to_bin(sh.hist, b, w, counts && v > kNegInf);
+    if (w >= least) mass_min += w;
   });
-#pragma unroll
-  for (int off = 32; off; off >>= 1) mass_min += shfl_u64(mass_min, lane ^ off);
-  if (lane == 0) sh.sum[wave] = mass_min;
+  mass_min = running_sum(mass_min);
+  if (lane == 63) sh.sum[wave] = mass_min;
   sum_histogram(sh.hist, sh.bins);
   mass_min = 0;
   for (int w = 0; w < waves; ++w) mass_min += sh.sum[w];
@@ -778,9 +886,14 @@ __device__ __forceinline__ Found sorted_row(Shared &sh, int n, const Row &row, c
   __syncthreads();
   int rank = 0;
   if (wave * 64 < n) {
-    for (int i = 0; i < n; i += 8) {  // (codes behind the list are 0)
+    const ulonglong2 *const two = reinterpret_cast<const ulonglong2 *>(code);
+#pragma unroll 1
+    for (int i = 0; i < (n + 1) / 2; i += 8) {  // (codes behind the list are 0)
+      ulonglong2 c[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) rank += code[i + j] > mine;
+      for (int j = 0; j < 8; ++j) c[j] = two[i + j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) rank += (c[j].x > mine) + (c[j].y > mine);
     }
   }
   if (t < n) {
@@ -796,7 +909,7 @@ __device__ __forceinline__ Found sorted_row(Shared &sh, int n, const Row &row, c
   for (int i = 0; i < wave; ++i) sum += sh.sum[i];
   upto[t] = sum;
   // the last that weighs min_p (weights fall with the order, but for their rounding)
-  const uint64_t heavy = __ballot(t < n && w >= q.least);
+  const uint64_t heavy = __ballot(t < n && w >= least_weight(row, q));
   if (heavy && (t & 63) == 63 - __builtin_clzll(heavy)) atomicMax(&sh.upto, sum);
   __syncthreads();
   const u64 here = upto[n - 1], mass_min = sh.upto;
@@ -858,9 +971,10 @@ struct Limits {
 __device__ __forceinline__ Limits limits_of(const Row &row, const Ask &q, int last) {
   if (q.few()) return {row.bin_rate, last == kBins - 1 ? kNegInf : row.base - (float)last, last};
   if (!(q.min_p > 0.f)) return {1.f, kNegInf, kBins - 1};
+  // (the logarithm within 1e-5 of it)
   const double t = (double)q.temperature;
   return {1.f,
-          __double2float_rd((double)row.largest + log((double)q.min_p) * t * (1.0 + 1e-6) - 1e-6 * t),
+          __double2float_rd((double)row.largest + (double)__logf(q.min_p) * t * (1.0 + 1e-4) - 1e-4 * t),
           kBins - 1};
 }
 template <typename T, int N>
@@ -876,7 +990,7 @@ __device__ __forceinline__ Limits limits_of(const HeldSource<T, N> &src, const R
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int h = N > 1 ? 2 * j / N : 2 * i / E;
-      top[h] = fmaxf(top[h], src.v[j][i]);
+      top[h] = fmaxf(top[h], src.v[j * E + i]);
     }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -891,23 +1005,16 @@ __device__ __forceinline__ void write(const SampleArgs &a, int at, int token, fl
   if (a.probs) a.probs[at] = prob;
 }
 
-// The largest of (v, i) over the workgroup, the smallest i among equals.
-__device__ __forceinline__ void first_largest(float (&best)[kMostWaves], int32_t (&first)[kMostWaves],
-                                              float &v, int &i) {
-  const auto join = [&](float x, int j) {
-    if (x > v || (x == v && j < i)) {
-      v = x;
-      i = j;
-    }
-  };
-#pragma unroll
-  for (int off = 32; off; off >>= 1) join(__shfl_xor(v, off), __shfl_xor(i, off));
-  if ((threadIdx.x & 63) == 0) {
-    best[threadIdx.x >> 6] = v;
-    first[threadIdx.x >> 6] = i;
-  }
+// The largest of (v, i) over the workgroup, the smallest i among equals: as
+// one number, key and ~i.
+__device__ __forceinline__ void first_largest(u64 (&best)[kMostWaves], float &v, int &i) {
+  const u64 mine = wave_max((u64)key_of(v) << 32 | (uint32_t)~i);
+  if ((threadIdx.x & 63) == 0) best[threadIdx.x >> 6] = mine;
   __syncthreads();
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) join(best[w], first[w]);
+  u64 most = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) most = max(most, best[w]);
+  v = value_of((uint32_t)(most >> 32));
+  i = (int)~(uint32_t)most;
 }
 template <typename T, int N>
 __device__ __forceinline__ void first_of(const HeldSource<T, N> &src, float &best, int &first) {
@@ -937,7 +1044,7 @@ __global__ __launch_bounds__(kWide) void k_sample_row(SampleArgs a) {
   float best;
   int first;
   first_of(held, best, first);
-  first_largest(sh.best, sh.first, best, first);
+  first_largest(sh.sum, best, first);
   const Ask q = ask_of(a, at);
   if (best == kNegInf) return write(a, at, -1, 0.f);
   if (q.greedy()) return write(a, at, first, 1.f);
@@ -963,8 +1070,6 @@ template <typename T>
 __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   __shared__ Hist hist;
   __shared__ Sums sums;
-  __shared__ float sh_best[kMostWaves];
-  __shared__ int32_t sh_first[kMostWaves];
   __shared__ u64 sh_sum[kMostWaves];
   __shared__ int sh_listed;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -979,20 +1084,21 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   int first;
   first_of(held, best, first);
   if (threadIdx.x == 0) sh_listed = 0;
-  first_largest(sh_best, sh_first, best, first);
-  SliceHead head{best, first, 0.f, false, 0, 0, kBins - 1, 0};
+  first_largest(sh_sum, best, first);
+  SliceHead head{0.0, 0, best, first, 0.f, 0, 0, kBins - 1, 0, 0};
   if (best == kNegInf || q.greedy()) {
     if (threadIdx.x == 0) a.heads[rs] = head;
     return;
   }
   const Row row = row_of(best, q.temperature, a.bits);
   head.base = row.base;
+  head.ref = row.ref;
   const bool listed = q.listed(), all = q.all();
   if (listed) {
     const Limits l = limits_of(held, row, q, hist, sums);
     head.last = l.last;
-    held.pick(src, &sh_listed, l, [&](int n, float v, int i) {
-      if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key_of(v), (uint32_t)i);
+    held.pick(src, &sh_listed, l, [&](int n, uint32_t key, int i) {
+      if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key, (uint32_t)i);
     });
     __syncthreads();
     head.listed = sh_listed;
@@ -1001,13 +1107,24 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
       return;
     }
   }
-  head.binned = true;
+  head.binned = 1;
   clear_histogram(hist);
   __syncthreads();
-  const bool counts = q.top_k != 0;
-  held.each([&](float v, int) {
-    add_to_bin(hist, bin_of(row, v), weight(row, v), counts && v > kNegInf);
-  });
+  if (row.far) {
+    held.each([&](float v, int) {
+      const int b = bin_of(row, v);
+      add_to_bin(hist, b, weight(row, v, b), q.top_k != 0 && v > kNegInf);
+    });
+  } else {
+    held.each([&](float v, int) {
+      const int b = bin_of(row, v);
+      u64 w = near_weight(row, v);
+      asm volatile("" : "+v"(w));  // computed by all lanes, or the branch costs a move a step
+      if (b < kBins - 1) atomicAdd(&hist.mass[b * kCopies + (lane & (kCopies - 1))], w);
+    });
+    if (q.top_k != 0)
+      held.each([&](float v, int) { add_to_bin(hist, bin_of(row, v), 0, v > kNegInf); });
+  }
   __syncthreads();
   u64 total = 0;
   for (int i = threadIdx.x; i < kBins; i += kNarrow) {
@@ -1031,73 +1148,67 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   }
 }
 
-// A row's slices together.
+// A row's slices together, lanes of a wave for them.
 struct Joined {
   float largest;
   int first;
   bool whole;  // every slice has listed all that may stay of it
 };
 __device__ __forceinline__ Joined join_heads(const SliceHead *heads, int slices, const Ask &q) {
-  const int lane = threadIdx.x & 63;  // slices dealt out over the lanes of each wave
-  Joined r{kNegInf, -1, false};
-  int at = 0x7FFFFFFF;
+  u64 best = 0;
   bool more = false;
-  for (int s = lane; s < slices; s += 64) {
+  for (int s = threadIdx.x & 63; s < slices; s += 64) {
     const SliceHead h = heads[s];
-    if (h.largest > r.largest) {
-      r.largest = h.largest;
-      at = h.first;
-    }
+    best = max(best, (u64)key_of(h.largest) << 32 | (uint32_t)~h.first);
     more = more || h.listed > kSliceList;
   }
-#pragma unroll
-  for (int off = 32; off; off >>= 1) {
-    const float x = __shfl_xor(r.largest, off);
-    const int i = __shfl_xor(at, off);
-    if (x > r.largest || (x == r.largest && i < at)) {
-      r.largest = x;
-      at = i;
-    }
-  }
-  r.first = at;
-  r.whole = q.listed() && !__any(more);
-  return r;
+  best = wave_max(best);
+  return {value_of((uint32_t)(best >> 32)), (int)~(uint32_t)best, q.listed() && !__any(more)};
 }
-// What a slice's weights are multiplied by, as a fraction of 2^64 (0: by one).
-__device__ __forceinline__ u64 slice_factor(const Row &row, float largest) {
-  if (largest == row.largest) return 0;
-  const double f = exp2(((double)largest - (double)row.largest) * row.rate);
-  const u64 part = (u64)__builtin_ldexp(f, 64);
-  return f < 1.0 ? part ? part : 1 : 0;
+// What a slice's weights are shifted by.
+__device__ __forceinline__ int slice_shift(const Row &row, const SliceHead &h) {
+  if (row.far) return h.largest == row.largest ? 0 : 63;
+  return (int)__builtin_fmin(row.ref - h.ref, 63.0);
 }
-__device__ __forceinline__ u64 scaled(u64 m, u64 factor) { return factor ? __umul64hi(m, factor) : m; }
 
-// Weights and counts by bin of all slices, as running sums: a wave a slice.
-// Of a slice that has listed all that may stay, that.
+// Weights and counts by bin of all slices, as running sums: a thread a bin (of
+// kMiddle), eight slices' loads at once.  Of a slice that has listed all that may
+// stay, that.
 __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row &row, const Ask &q,
-                                          Hist &hist, Sums &to) {
-  clear_histogram(hist);
+                                          Shared &sh) {
+  const int t = threadIdx.x;
+  const bool counts = q.top_k != 0;
+  clear_histogram(sh.hist);
+  if (t < a.slices) {
+    const SliceHead h = a.heads[(size_t)r * a.slices + t];
+    sh.base[t] = h.base;
+    sh.shift[t] = h.largest > kNegInf ? slice_shift(row, h) : 0;
+    // a slice without tokens is an empty list
+    sh.length[t] = h.binned ? -1 : h.largest > kNegInf ? h.listed : 0;
+  }
   __syncthreads();
-  const int lane = threadIdx.x & 63;
-  for (int s = threadIdx.x >> 6; s < a.slices; s += blockDim.x >> 6) {
-    const size_t rs = (size_t)r * a.slices + s;
-    const SliceHead h = a.heads[rs];
-    if (!(h.largest > kNegInf)) continue;
-    if (!h.binned) {
-      for (int i = lane; i < h.listed; i += 64) {
-        const float v = value_of(a.list[rs * kSliceList + i].x);
-        add_to_bin(hist, bin_of(row, v), weight(row, v), q.top_k != 0);
-      }
-      continue;
+  const size_t from = (size_t)r * a.slices * kBins + t;
+#pragma unroll 1
+  for (int s0 = 0; s0 < a.slices; s0 += 8) {
+    u64 m[8];
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool binned = s0 + j < a.slices && sh.length[s0 + j] < 0;
+      m[j] = binned ? a.mass[from + (size_t)(s0 + j) * kBins] : 0;
+      c[j] = binned && counts ? a.count[from + (size_t)(s0 + j) * kBins] : 0;
     }
-    const u64 factor = slice_factor(row, h.largest);
-    for (int i = lane; i < kBins; i += 64) {
-      const u64 m = a.mass[rs * kBins + i];
-      const uint32_t c = a.count[rs * kBins + i];
-      if (m | c) add_to_bin(hist, row_bin(row, h.base, i), scaled(m, factor), c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (m[j] | c[j])
+        add_to_bin(sh.hist, row_bin(row, sh.base[s0 + j], t), m[j] >> sh.shift[s0 + j], c[j]);
     }
   }
-  sum_histogram(hist, to);
+  if (q.listed()) {
+    const GatherSource lists{a.list + (size_t)r * a.slices * kSliceList, sh.length, a.slices};
+    lists.each([&](float v, int) { add_to_bin(sh.hist, bin_of(row, v), weight(row, v), counts); });
+  }
+  sum_histogram(sh.hist, sh.bins);
 }
 
 template <typename T>
@@ -1114,26 +1225,25 @@ __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   u64 whole;
   if (joined.whole) {
     // all weights, and what the slices' own first top_k leave for the row's
+    // (every wave for itself; the lists' lengths all the same)
     u64 all = 0;
-    int last = kBins - 1;
+    uint32_t last = kBins - 1;
     for (int s = lane; s < a.slices; s += 64) {
       const SliceHead h = heads[s];
+      sh.length[s] = h.listed;
       if (!(h.largest > kNegInf)) continue;
-      if (q.all()) all += scaled(h.total, slice_factor(row, h.largest));
-      last = min(last, row_bin(row, h.base, h.last));
+      if (q.all()) all += h.total >> slice_shift(row, h);
+      last = min(last, (uint32_t)row_bin(row, h.base, h.last));
     }
-#pragma unroll
-    for (int off = 32; off; off >>= 1) {
-      if (q.all()) all += shfl_u64(all, lane ^ off);
-      last = min(last, __shfl_xor(last, off));
-    }
-    const GatherSource gather{heads, a.list + (size_t)r * a.slices * kSliceList, a.slices, false};
-    const int n = list_tokens(gather, gather, sh, limits_of(row, q, last));
+    all = wave_sum(all);
+    last = wave_min(last);
+    const GatherSource gather{a.list + (size_t)r * a.slices * kSliceList, sh.length, a.slices};
+    const int n = list_tokens(gather, gather, sh, limits_of(row, q, (int)last));
     const Found f = n <= kList ? listed_row(sh, n, row, q, !q.all(), all, &whole)
                                : whole_row(gather, gather, sh, row, q, !q.all(), all, &whole);
     return write(a, at, f.token, (float)((double)f.own / (double)whole));
   }
-  join_bins(a, r, row, q, sh.hist, sh.bins);
+  join_bins(a, r, row, q, sh);
   const u64 all = sh.bins.mass[kBins - 1];
   const Need need = need_of(sh.bins, row, q, all, all, false);
   RowState &state = a.state[r];
@@ -1163,8 +1273,8 @@ __global__ __launch_bounds__(kNarrow) void k_sample_collect(SampleArgs a) {
     __syncthreads();
     const Needed needed(row_of(a.state[r].largest, a.temperature ? a.temperature[at] : 1.f, a.bits),
                         a.state[r].need);
-    held.pick(src, &sh_n, needed, [&](int n, float v, int i) {
-      if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key_of(v), (uint32_t)i);
+    held.pick(src, &sh_n, needed, [&](int n, uint32_t key, int i) {
+      if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key, (uint32_t)i);
     });
     __syncthreads();
     if (threadIdx.x == 0) a.heads[rs].collected = sh_n;
@@ -1187,35 +1297,33 @@ __global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
     sh.bins.mass[i] = state.bins.mass[i];
     sh.bins.count[i] = state.bins.count[i];
   }
-  if (threadIdx.x == 0) sh.n_list = 0;
   bool more = false;
-  for (int s = lane; s < a.slices; s += 64) more = more || heads[s].collected > kSliceList;
+  for (int s = lane; s < a.slices; s += 64) {
+    const int n = heads[s].collected;
+    sh.length[s] = n;
+    more = more || n > kSliceList;
+  }
   const bool fits = !__any(more);
   __syncthreads();
   const u64 all = sh.bins.mass[kBins - 1];
   // the tokens in question, and of min_p's bins the weights that it leaves
-  u64 part = 0;
-  const auto look = [&](float v, int i, bool keep) {
-    if (!(v > kNegInf)) return;
-    const int b = bin_of(row, v);
-    if (b >= need.m0 && b <= need.m1) {
-      const u64 w = weight(row, v);
-      if (w >= q.least) part += w;
-    }
-    if (!keep) return;
-    const int j = atomicAdd(&sh.n_list, 1);
-    if (j < kList) {
-      sh.key[j] = key_of(v);
-      sh.index[j] = i;
-    }
-  };
   const RowSource<T> src = logits_of<T>(a, at);
-  const GatherSource gather{heads, a.list + (size_t)r * a.slices * kSliceList, a.slices, true};
-  if (fits) gather.each([&](float v, int i) { look(v, i, true); });
-  else if (need.m1 >= need.m0) src.each([&](float v, int i) { look(v, i, false); });
-#pragma unroll
-  for (int off = 32; off; off >>= 1) part += shfl_u64(part, lane ^ off);
-  if (lane == 0) sh.sum[wave] = part;
+  const GatherSource gather{a.list + (size_t)r * a.slices * kSliceList, sh.length, a.slices};
+  const int n = fits ? list_tokens(gather, gather, sh, [](float) { return true; }) : kList + 1;
+  u64 part = 0;
+  if (need.m1 >= need.m0) {
+    const u64 least = least_weight(row, q);
+    const auto look = [&](float v, int) {
+      const int b = bin_of(row, v);
+      if (b < need.m0 || b > need.m1) return;
+      const u64 w = weight(row, v, b);
+      if (w >= least) part += w;
+    };
+    if (n <= kList) ListSource{sh, n}.each(look);
+    else src.each(look);
+    part = running_sum(part);
+    if (lane == 63) sh.sum[wave] = part;
+  }
   __syncthreads();
   u64 mass_min = all;
   if (need.m1 >= need.m0) {
@@ -1224,10 +1332,8 @@ __global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
     mass_min = min(mass_min, sh.bins.mass[need.m1]);
   }
   u64 whole;
-  const Found f = !fits ? answer(src, sh, row, q, all, mass_min, &whole)
-                  : sh.n_list <= kList
-                      ? answer(ListSource{sh, sh.n_list}, sh, row, q, all, mass_min, &whole)
-                      : answer(gather, sh, row, q, all, mass_min, &whole);
+  const Found f = n <= kList ? answer(ListSource{sh, n}, sh, row, q, all, mass_min, &whole)
+                             : answer(src, sh, row, q, all, mass_min, &whole);
   write(a, at, f.token, (float)((double)f.own / (double)whole));
 }
 
@@ -1236,7 +1342,7 @@ __global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
 int weight_bits(int vocab) {
   int log = 12;
   while (1 << log < vocab) ++log;
-  return 62 - log;
+  return 63 - log;  // (the largest weighs between half of 2^bits and all of it)
 }
 
 // Slices of a row (none: a row is a workgroup's), and the workspace of the
