@@ -48,7 +48,10 @@ constexpr int kBins = 512;
 constexpr int kLaneBins = kBins / 64;
 constexpr int kSumWaves = 4;  // that sum up a histogram, two bins a lane
 static_assert(kBins == 2 * 64 * kSumWaves, "two bins a lane");
-constexpr int kCopies = 2;   // of a histogram, by lane: neighbours often share a bin
+constexpr int kCopyLog = 1;  // copies of a histogram, by lane: neighbours often share a bin
+constexpr int kCopies = 1 << kCopyLog;
+constexpr int kFewLog = 4;   // ... of one of few bins, where most of them do
+constexpr int kFewBins = kBins * kCopies >> kFewLog;
 constexpr int kList = 6144;  // tokens that answer() has in LDS
 constexpr int kSmall = 64;   // tokens that one wave ranks
 constexpr float kBinsPerOctave = 10.f;  // 51 octaves, which is all that weighs anything
@@ -58,6 +61,7 @@ constexpr int kRowMost = 32 * kWide;  // logits of a row that is not cut into sl
 constexpr int kSlice = 32 * kNarrow;  // logits of a slice
 constexpr int kSliceList = kMiddle;   // tokens that a slice may list
 static_assert(kBins == kMiddle, "a thread a bin");
+constexpr int kBatch = 8;  // slices whose loads are in flight at once
 constexpr int kMostSlices = RFPX_VOCAB_MAX / kSlice + 1;
 constexpr int kTopMost = 256;     // top_k of rows whose slices list their tokens
 constexpr int kRowsAtOnce = 512;  // rows of one set of launches, which bounds the workspace
@@ -120,10 +124,11 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
-// NaN is no token, as -inf; +inf counts as the largest number, so that all
-// that is computed of tokens is one.
+// NaN is no token, as -inf; +inf counts as the type's largest number, so that
+// all that is computed of tokens is one.
+template <typename T>
 __device__ __forceinline__ float logit_of(float x) {
-  return x > kNegInf ? fminf(x, 3.402823466e38f) : kNegInf;
+  return x > kNegInf ? fminf(x, __uint_as_float(sizeof(T) == 2 ? 0x7F7F0000u : 0x7F7FFFFFu)) : kNegInf;
 }
 
 // What weights and bins of a row, or a slice of it, are relative to.
@@ -132,13 +137,20 @@ struct Row {
   float bin_rate;  // bins a logit
   float base;      // the largest logit's bin, counted from 0
   int bits;
+  int key_zeros;   // low bits in which keys of one sign do not differ
   bool far;        // nothing but the largest logit weighs anything
   double rate;     // log2(e) / temperature
   double ref;      // a whole number, the largest logit times rate or above
+  // Of a key without those bits (which are ones below 0).
+  __device__ __forceinline__ float value(uint32_t k) const {
+    return value_of(key_zeros ? k << 16 | (k & 0x8000u ? 0u : 0xFFFFu) : k);
+  }
 };
 
+template <typename T>
 __device__ __forceinline__ Row row_of(float largest, float temperature, int bits) {
   Row r;
+  r.key_zeros = sizeof(T) == 2 ? 16 : 0;
   r.largest = largest;
   r.rate = 1.4426950408889634 / (double)temperature;
   // (above 0, so that -inf is in the last bin at any temperature)
@@ -275,9 +287,9 @@ struct Shared {
   uint32_t in_count, key_lo, key_hi;
   int n_list, n_small, token;
   // of a row's slices
-  int length[kMostSlices + 7];
-  float base[kMostSlices + 7];
-  int shift[kMostSlices + 7];
+  int length[kMostSlices + kBatch];
+  float base[kMostSlices + kBatch];
+  int shift[kMostSlices + kBatch];
 };
 
 // -------------------------------------------------------- sources of tokens
@@ -302,7 +314,7 @@ struct RowSource {
   }
   static __device__ __forceinline__ float logit(const uint4 &w, int j) {
     const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-    return logit_of(sizeof(T) == 4 ? __uint_as_float(d[j * sizeof(T) / 4])
+    return logit_of<T>(sizeof(T) == 4 ? __uint_as_float(d[j * sizeof(T) / 4])
                     : j & 1        ? __uint_as_float(d[j / 2] & 0xFFFF0000u)
                                    : __uint_as_float(d[j / 2] << 16));
   }
@@ -315,7 +327,7 @@ struct RowSource {
       const int at = begin(c);
 #pragma unroll
       for (int j = 0; j < E; ++j)
-        v[j] = at + j >= 0 && at + j < n ? logit_of(one(at + j)) : kNegInf;
+        v[j] = at + j >= 0 && at + j < n ? logit_of<T>(one(at + j)) : kNegInf;
     }
   }
   // f(logit, index) for each; also for -inf.
@@ -411,7 +423,7 @@ struct HeldSource {
     for (; mask; mask &= mask - 1, ++place) {
       const int bit = __builtin_ctz(mask);
       const int index = at + bit / E * (int)blockDim.x * E + bit % E;
-      f(place, key_of(logit_of(src.one(index))), index);
+      f(place, key_of(logit_of<T>(src.one(index))), index);
     }
   }
 };
@@ -426,49 +438,50 @@ struct ListSource {
 };
 
 // The lists of a row's slices, whose lengths are in LDS: a thread a place in the
-// lists (kMiddle threads), eight slices' loads at once.
+// lists (kMiddle threads), kBatch slices' loads at once.
 struct GatherSource {
+  static constexpr int B = kBatch;
   const uint2 *list;
   const int *lengths;
   int slices;
-  __device__ __forceinline__ void load(int s0, uint2 (&e)[8]) const {
+  __device__ __forceinline__ void load(int s0, uint2 (&e)[B]) const {
     const int t = threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < B; ++j)
       e[j] = s0 + j < slices && t < lengths[s0 + j] ? list[(size_t)(s0 + j) * kSliceList + t]
                                                     : make_uint2(kNoToken, 0);
   }
   template <typename F>
   __device__ __forceinline__ void each(F &&f) const {
 #pragma unroll 1
-    for (int s0 = 0; s0 < slices; s0 += 8) {
-      uint2 e[8];
+    for (int s0 = 0; s0 < slices; s0 += B) {
+      uint2 e[B];
       load(s0, e);
 #pragma unroll 1
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < B; ++j) {
         if (e[0].x > kNoToken) f(value_of(e[0].x), (int)e[0].y);
 #pragma unroll
-        for (int i = 0; i < 7; ++i) e[i] = e[i + 1];
+        for (int i = 0; i < B - 1; ++i) e[i] = e[i + 1];
       }
     }
   }
   // f(place, key, index) for those that `in` picks: a wave takes its places from
-  // `counter` eight slices at a time.
+  // `counter` a batch at a time.
   template <typename In, typename F>
   __device__ __forceinline__ void pick(int *counter, In &&in, F &&f) const {
 #pragma unroll 1
-    for (int s0 = 0; s0 < slices; s0 += 8) {
-      uint2 e[8];
+    for (int s0 = 0; s0 < slices; s0 += B) {
+      uint2 e[B];
       load(s0, e);
       uint32_t mask = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mask |= e[j].x > kNoToken && in(value_of(e[j].x)) ? 1u << j : 0u;
+      for (int j = 0; j < B; ++j) mask |= e[j].x > kNoToken && in(value_of(e[j].x)) ? 1u << j : 0u;
       const uint32_t mine = __popc(mask), upto = running_sum(mine);
       int place = 0;
       if ((threadIdx.x & 63) == 63 && upto) place = atomicAdd(counter, (int)upto);
       place = __builtin_amdgcn_readlane(place, 63) + (int)(upto - mine);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < B; ++j)
         if (mask >> j & 1u) f(place++, e[j].x, (int)e[j].y);
     }
   }
@@ -482,24 +495,37 @@ __device__ __forceinline__ void clear_histogram(Hist &h) {
     h.count[i] = 0;
   }
 }
-__device__ __forceinline__ void add_to_bin(Hist &h, int bin, u64 w, uint32_t n) {
-  const int at = bin * kCopies + (threadIdx.x & (kCopies - 1));
+__device__ __forceinline__ void add_to_bin(Hist &h, int bin, u64 w, uint32_t n, int log = kCopyLog) {
+  const int at = bin << log | (threadIdx.x & ((1 << log) - 1));
   if (w) atomicAdd(&h.mass[at], w);
   if (n) atomicAdd(&h.count[at], n);
 }
+// The weights of a source by bin, in a row that is not far.  (The branch is an
+// addition's alone: the polynomial in it costs a move a step.)
+template <typename S>
+__device__ __forceinline__ void add_weights(const S &src, Hist &h, const Row &row) {
+  const int copy = threadIdx.x & (kCopies - 1);
+  src.each([&](float v, int) {
+    const int b = bin_of(row, v);
+    u64 w = near_weight(row, v);
+    asm volatile("" : "+v"(w));
+    if (b < kBins - 1) atomicAdd(&h.mass[b * kCopies + copy], w);
+  });
+}
 // Running sums over the histogram's bins (between barriers of its own).
-__device__ __forceinline__ void sum_histogram(Hist &h, Sums &to) {
+__device__ __forceinline__ void sum_histogram(Hist &h, Sums &to, int log = kCopyLog) {
   __syncthreads();
   const int t = threadIdx.x, wave = uniform(t >> 6);
   u64 m0 = 0, m1 = 0, m = 0;
   uint32_t c0 = 0, c1 = 0, c = 0;
   if (wave < kSumWaves) {
-#pragma unroll
-    for (int k = 0; k < kCopies; ++k) {
-      m0 += h.mass[2 * t * kCopies + k];
-      m1 += h.mass[(2 * t + 1) * kCopies + k];
-      c0 += h.count[2 * t * kCopies + k];
-      c1 += h.count[(2 * t + 1) * kCopies + k];
+    if ((2 * t + 1) << log < kBins * kCopies) {
+      for (int k = 0; k < 1 << log; ++k) {
+        m0 += h.mass[(2 * t << log) + k];
+        m1 += h.mass[((2 * t + 1) << log) + k];
+        c0 += h.count[(2 * t << log) + k];
+        c1 += h.count[((2 * t + 1) << log) + k];
+      }
     }
     m = running_sum(m0 + m1);
     c = running_sum(c0 + c1);
@@ -552,11 +578,12 @@ template <typename S>
 __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by_count, u64 r,
                       u64 above, bool want_token) {
   const int lane = threadIdx.x & 63;
-  // the bin's keys and how many tokens it has
+  // the bin's keys (without the bits in which they do not differ) and how many
+  // tokens it has
   uint32_t lo = 0xFFFFFFFFu, hi = 0, n = 0;
   src.each([&](float v, int) {
     if (v > kNegInf && bin_of(row, v) == bin) {
-      const uint32_t k = key_of(v);
+      const uint32_t k = key_of(v) >> row.key_zeros;
       lo = min(lo, k);
       hi = max(hi, k);
       ++n;
@@ -588,7 +615,7 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
     if (!keys && last == 0x7FFFFFFF) {
       // all have one logit: the place among them is a division, and now ones
       // are summed
-      const u64 w = weight(row, value_of(lo));
+      const u64 w = weight(row, row.value(lo));
       if (!by_count && w) {
         const u64 place = within(r / w, n);
         above += place * w;
@@ -602,16 +629,17 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
     }
     const uint32_t span = keys ? hi - lo : (uint32_t)(last - first);
     const int shift = max(0, 23 - __builtin_clz(span));
+    const int log = (span >> shift) < kFewBins ? kFewLog : kCopyLog;
     __syncthreads();
     clear_histogram(sh.hist);
     __syncthreads();
     src.each([&](float v, int i) {
-      const uint32_t k = key_of(v);
-      if (k < lo || k > hi || i < first || i > last) return;
-      if (keys) add_to_bin(sh.hist, (hi - k) >> shift, weight(row, v), 1);
-      else add_to_bin(sh.hist, (i - first) >> shift, 0, 1);
+      const uint32_t k = key_of(v) >> row.key_zeros;
+      if (k < lo || k > hi || !(v > kNegInf) || i < first || i > last) return;
+      if (keys) add_to_bin(sh.hist, (hi - k) >> shift, weight(row, v), 1, log);
+      else add_to_bin(sh.hist, (i - first) >> shift, 0, 1, log);
     });
-    sum_histogram(sh.hist, sh.digits);
+    sum_histogram(sh.hist, sh.digits, log);
     r = within(r, by_count ? (u64)sh.digits.count[kBins - 1] : sh.digits.mass[kBins - 1]);
     const int d = bin_over(sh.digits, r, by_count);
     const u64 m0 = d ? sh.digits.mass[d - 1] : 0;
@@ -629,7 +657,7 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
   }
   Found f{above, 0, -1};
   if (n > kSmall) {  // many of one logit, and no index asked for
-    const u64 w = weight(row, value_of(lo));
+    const u64 w = weight(row, row.value(lo));
     f.own = w;
     f.upto = above + (within(by_count ? r : w ? r / w : 0, n) + 1) * w;
     return f;
@@ -641,11 +669,11 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
   if (threadIdx.x == 0) sh.n_small = 0;
   __syncthreads();
   src.each([&](float v, int i) {
-    const uint32_t k = key_of(v);
-    if (k < lo || k > hi || k <= kNoToken || i < first || i > last) return;
+    const uint32_t k = key_of(v) >> row.key_zeros;
+    if (k < lo || k > hi || !(v > kNegInf) || i < first || i > last) return;
     const int at = atomicAdd(&sh.n_small, 1);
     if (at < kSmall) {
-      sh.small_key[at] = k;
+      sh.small_key[at] = key_of(v);
       sh.small_index[at] = i;
     }
   });
@@ -854,15 +882,21 @@ __device__ __forceinline__ u64 bins_of(const S &src, Shared &sh, const Row &row,
   u64 mass_min = 0;
   const bool counts = q.top_k != 0;
   const u64 least = least_weight(row, q);
-  src.each([&](float v, int) {
-    const int b = bin_of(row, v);
-    const u64 w = weight(row, v, b);
-    add_to_bin(sh.hist, b, w, counts && v > kNegInf);
-    if (w >= least) mass_min += w;
-  });
-  mass_min = running_sum(mass_min);
-  if (lane == 63) sh.sum[wave] = mass_min;
+  const bool plain = !row.far && !counts && least == 0;
+  if (plain) {
+    add_weights(src, sh.hist, row);
+  } else {
+    src.each([&](float v, int) {
+      const int b = bin_of(row, v);
+      const u64 w = weight(row, v, b);
+      add_to_bin(sh.hist, b, w, counts && v > kNegInf);
+      if (w >= least) mass_min += w;
+    });
+    mass_min = running_sum(mass_min);
+    if (lane == 63) sh.sum[wave] = mass_min;
+  }
   sum_histogram(sh.hist, sh.bins);
+  if (plain) return sh.bins.mass[kBins - 1];
   mass_min = 0;
   for (int w = 0; w < waves; ++w) mass_min += sh.sum[w];
   return mass_min;
@@ -1048,7 +1082,7 @@ __global__ __launch_bounds__(kWide) void k_sample_row(SampleArgs a) {
   const Ask q = ask_of(a, at);
   if (best == kNegInf) return write(a, at, -1, 0.f);
   if (q.greedy()) return write(a, at, first, 1.f);
-  const Row row = row_of(best, q.temperature, a.bits);
+  const Row row = row_of<T>(best, q.temperature, a.bits);
   u64 whole;
   Found f;
   if (!q.all() && q.listed()) {
@@ -1090,7 +1124,7 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
     if (threadIdx.x == 0) a.heads[rs] = head;
     return;
   }
-  const Row row = row_of(best, q.temperature, a.bits);
+  const Row row = row_of<T>(best, q.temperature, a.bits);
   head.base = row.base;
   head.ref = row.ref;
   const bool listed = q.listed(), all = q.all();
@@ -1116,12 +1150,7 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
       add_to_bin(hist, b, weight(row, v, b), q.top_k != 0 && v > kNegInf);
     });
   } else {
-    held.each([&](float v, int) {
-      const int b = bin_of(row, v);
-      u64 w = near_weight(row, v);
-      asm volatile("" : "+v"(w));  // computed by all lanes, or the branch costs a move a step
-      if (b < kBins - 1) atomicAdd(&hist.mass[b * kCopies + (lane & (kCopies - 1))], w);
-    });
+    add_weights(held, hist, row);
     if (q.top_k != 0)
       held.each([&](float v, int) { add_to_bin(hist, bin_of(row, v), 0, v > kNegInf); });
   }
@@ -1172,7 +1201,7 @@ __device__ __forceinline__ int slice_shift(const Row &row, const SliceHead &h) {
 }
 
 // Weights and counts by bin of all slices, as running sums: a thread a bin (of
-// kMiddle), eight slices' loads at once.  Of a slice that has listed all that may
+// kMiddle), kBatch slices' loads at once.  Of a slice that has listed all that may
 // stay, that.
 __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row &row, const Ask &q,
                                           Shared &sh) {
@@ -1189,17 +1218,17 @@ __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row 
   __syncthreads();
   const size_t from = (size_t)r * a.slices * kBins + t;
 #pragma unroll 1
-  for (int s0 = 0; s0 < a.slices; s0 += 8) {
-    u64 m[8];
-    uint32_t c[8];
+  for (int s0 = 0; s0 < a.slices; s0 += kBatch) {
+    u64 m[kBatch];
+    uint32_t c[kBatch];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kBatch; ++j) {
       const bool binned = s0 + j < a.slices && sh.length[s0 + j] < 0;
       m[j] = binned ? a.mass[from + (size_t)(s0 + j) * kBins] : 0;
       c[j] = binned && counts ? a.count[from + (size_t)(s0 + j) * kBins] : 0;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kBatch; ++j) {
       if (m[j] | c[j])
         add_to_bin(sh.hist, row_bin(row, sh.base[s0 + j], t), m[j] >> sh.shift[s0 + j], c[j]);
     }
@@ -1221,7 +1250,7 @@ __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   const Joined joined = join_heads(heads, a.slices, q);
   if (joined.largest == kNegInf) return write(a, at, -1, 0.f);
   if (q.greedy()) return write(a, at, joined.first, 1.f);
-  const Row row = row_of(joined.largest, q.temperature, a.bits);
+  const Row row = row_of<T>(joined.largest, q.temperature, a.bits);
   u64 whole;
   if (joined.whole) {
     // all weights, and what the slices' own first top_k leave for the row's
@@ -1271,7 +1300,7 @@ __global__ __launch_bounds__(kNarrow) void k_sample_collect(SampleArgs a) {
     held.load(src, slice);
     if (threadIdx.x == 0) sh_n = 0;
     __syncthreads();
-    const Needed needed(row_of(a.state[r].largest, a.temperature ? a.temperature[at] : 1.f, a.bits),
+    const Needed needed(row_of<T>(a.state[r].largest, a.temperature ? a.temperature[at] : 1.f, a.bits),
                         a.state[r].need);
     held.pick(src, &sh_n, needed, [&](int n, uint32_t key, int i) {
       if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key, (uint32_t)i);
@@ -1291,7 +1320,7 @@ __global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
   const SliceHead *heads = a.heads + (size_t)r * a.slices;
   const Ask q = ask_of(a, at);
   const RowState &state = a.state[r];
-  const Row row = row_of(state.largest, q.temperature, a.bits);
+  const Row row = row_of<T>(state.largest, q.temperature, a.bits);
   const Need need = state.need;
   for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
     sh.bins.mass[i] = state.bins.mass[i];

@@ -78,8 +78,8 @@ size_t rfpx_sample_workspace_bytes(int n_rows, int vocab, int xtype);
  * stay.  tokens_dev int32 [n_rows] gets its index, probs_dev (fp32, or NULL)
  * its weight over that sum.  A temperature of 0 or less (or NaN) takes the
  * first token, with probability 1.  Logits of -inf or NaN are no tokens, +inf
- * counts as the largest finite number.  A row without tokens gets index -1 and
- * probability 0.
+ * counts as the type's largest finite number.  A row without tokens gets index
+ * -1 and probability 0.
  * temperature, top_p, min_p (fp32) and top_k (int32), each [n_rows], may be
  * NULL: 1, and no cut.  u below 0 or NaN counts as 0, from 1 on as just below.
  * Weights are held as whole multiples of 2^-s, s = 50 up to 4096 tokens and
