@@ -1349,6 +1349,7 @@ __global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
       if (w >= least) part += w;
     };
     if (n <= kList) ListSource{sh, n}.each(look);
+    else if (fits) gather.each(look);
     else src.each(look);
     part = running_sum(part);
     if (lane == 63) sh.sum[wave] = part;
@@ -1362,6 +1363,7 @@ __global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
   }
   u64 whole;
   const Found f = n <= kList ? answer(ListSource{sh, n}, sh, row, q, all, mass_min, &whole)
+                  : fits     ? answer(gather, sh, row, q, all, mass_min, &whole)
                              : answer(src, sh, row, q, all, mass_min, &whole);
   write(a, at, f.token, (float)((double)f.own / (double)whole));
 }
