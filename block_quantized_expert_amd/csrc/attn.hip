@@ -69,22 +69,41 @@ struct AttnArgs {
 };
 
 // The slots t0 .. t0 + 31 that a tree's column sees, a bit each: those before
-// `context`, and behind it those that its mask names, below `end`.
+// `context`, and behind it those that its mask names, below `end`.  The mask has
+// a word of zeros behind it.
 __device__ __forceinline__ uint32_t tree_bits(const uint32_t *mask, int words, int context, int t0,
                                               int end) {
-  const int off = t0 - context;
+  const int off = t0 - context, seen = end - t0;
   uint32_t bits = 0;
   if (off <= -32) {
     bits = 0xFFFFFFFFu;
   } else if (off < 0) {
-    bits = (words > 0 ? mask[0] << -off : 0u) | ((1u << -off) - 1u);
-  } else {
-    const int w = off >> 5, sh = off & 31;
-    if (w < words) bits = mask[w] >> sh;
-    if (sh && w + 1 < words) bits |= mask[w + 1] << (32 - sh);
+    bits = mask[0] << -off | ((1u << -off) - 1u);
+  } else if (off >> 5 < words) {
+    bits = __builtin_amdgcn_alignbit(mask[(off >> 5) + 1], mask[off >> 5], off & 31);
   }
-  const int seen = end - t0;
   return seen >= 32 ? bits : seen <= 0 ? 0u : bits & ((1u << seen) - 1u);
+}
+// x where bit k is set, else -inf; without a condition, which the compiler would
+// keep a pair of scalar registers for.
+__device__ __forceinline__ float if_bit(uint32_t bits, int k, float x) {
+  const uint32_t m = (uint32_t)((int)(bits << (31 - k)) >> 31);
+  return __uint_as_float((__float_as_uint(x) & m) | (0xFF800000u & ~m));
+}
+// The masks of `n` rows of a head from r0 on into LDS, one behind the other with
+// their zeros: none for rows that are not there, and for columns whose own slot
+// is negative.
+__device__ __forceinline__ void load_masks(const AttnArgs &a, uint32_t *to, int n, long long r0,
+                                           long long rows, int s0, int context) {
+  const int per = a.mask_words + 1;
+  for (int i = threadIdx.x; i < n * per; i += blockDim.x) {
+    const int w = i % per;
+    const long long r = r0 + i / per;
+    const int col = (int)(min(r, rows - 1) / a.group);
+    to[i] = w < a.mask_words && r < rows && context + col >= 0
+                ? a.masks[(size_t)(s0 + col) * a.mask_words + w]
+                : 0u;
+  }
 }
 
 __device__ __forceinline__ floatx4 mfma(const u32x4v &a, const u32x4v &b, const floatx4 &c) {
@@ -395,6 +414,8 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   __shared__ float sh_ml[W][RT * 16][3];
   __shared__ __align__(16) float sh_o[W][16][LD];
   __shared__ QShared<NB, VX> sh_q[RT];
+  // the rows' masks, where the waves' sums meet in the end
+  uint32_t *const sh_mask = reinterpret_cast<uint32_t *>(sh_o);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   // The last rows see most: they start first (a chunk over its own 2048 tokens,
@@ -411,9 +432,11 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
   const int32_t *table = a.v.table + (size_t)seq * a.v.pages_per_seq;
 
   for (long long r0 = (long long)rb0 * (16 * RT); r0 < rows; r0 += (long long)a.row_blocks * (16 * RT)) {
-    int vis[RT];  // (TREE: a column's row, -1 where its slot is negative)
+    int vis[RT];
     int first_vis, last_vis;
     if constexpr (TREE) {
+      static_assert(sizeof(sh_o) >= 16 * RT * (RFPX_TREE_COLS_MAX / 32 + 1) * 4, "masks");
+      load_masks(a, sh_mask, 16 * RT, r0, rows, s0, len - n_all);
       first_vis = max(0, len - n_all);
       last_vis = len;
     } else {
@@ -430,8 +453,7 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
       const bool live = r < rows;
       if (!live) r = rows - 1;
       const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
-      vis[t] = TREE ? (len - n_all + col < 0 ? -1 : s0 + col)
-                    : min(len, max(0, len - n_all + col + 1));
+      vis[t] = TREE ? 0 : min(len, max(0, len - n_all + col + 1));
       if (wave == t) {
         QTile<NB, VX> q;
         load_q<NB, VX>(a.q, (size_t)(s0 + col) * a.q_stride + (size_t)hd * D, live, g, q);
@@ -533,21 +555,18 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
         if constexpr (TREE) {
 #pragma unroll
           for (int t = 0; t < RT; ++t)
-            bits[t] = vis[t] < 0 ? 0u
-                                 : tree_bits(a.masks + (size_t)vis[t] * a.mask_words, a.mask_words,
-                                             len - n_all, t0, lim) >> (4 * g);
+            bits[t] = tree_bits(sh_mask + (16 * t + m) * (a.mask_words + 1), a.mask_words,
+                                len - n_all, t0, lim) >> (4 * g);
         }
-        const auto hidden = [&](int t, int u, int i) {
-          if constexpr (TREE) return !((bits[t] >> (16 * u + i)) & 1u);
-          else return t0 + 16 * u + 4 * g + i >= min(vis[t], lim);
-        };
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (hidden(t, u, i)) s[t][u][i] = kNegInf;
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (TREE) s[t][u][i] = if_bit(bits[t], 16 * u + i, s[t][u][i]);
+              else if (t0 + 16 * u + 4 * g + i >= min(vis[t], lim)) s[t][u][i] = kNegInf;
+            }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -561,8 +580,10 @@ __global__ __launch_bounds__(64 * W, NB == 8 ? 1 : 2) void k_attn(AttnArgs a) {
                 // a NaN block reaches the rows that see its token, no other
                 v.s[u][at >> 2] &= ~(0xFFu << (8 * (at & 3)));
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
-                  if (bad && !hidden(t, u, i)) poison[t] |= 1u << b;
+                for (int t = 0; t < RT; ++t) {
+                  if constexpr (TREE) poison[t] |= bad ? (bits[t] >> (16 * u + i) & 1u) << b : 0u;
+                  else if (bad && slot < min(vis[t], lim)) poison[t] |= 1u << b;
+                }
               }
             }
           }
@@ -926,6 +947,8 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
   ChunkK<NB> *buf_k = reinterpret_cast<ChunkK<NB> *>(lds);
   ChunkV<NB> *buf_v = reinterpret_cast<ChunkV<NB> *>(buf_k + 2);
   uint8_t *bad = reinterpret_cast<uint8_t *>(buf_v + 2);  // [2][NB][8 waves]: a bit a token
+  // TREE: the masks of the rows that the queries of the row block have
+  uint32_t *const sh_mask = reinterpret_cast<uint32_t *>(bad + 2 * NB * kChunkWaves);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 31, h = lane >> 5;
   // The last rows see most: they start first (4096 columns over their own
@@ -954,7 +977,8 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
     const bool live = r < rows;
     if (!live) r = rows - 1;
     const int col = (int)(r / a.group), hd = head * a.group + (int)(r % a.group);
-    const int vis = TREE && len - n_all + col < 0 ? 0 : sees(r);
+    const int vis = sees(r);
+    if constexpr (TREE) load_masks(a, sh_mask, kChunkRows, r0, rows, s0, len - n_all);
     u32x4v q[2 * NB];
     {
       const uint16_t *p = static_cast<const uint16_t *>(a.q) + (size_t)(s0 + col) * a.q_stride +
@@ -1044,11 +1068,11 @@ __global__ __launch_bounds__(64 * kChunkWaves) void k_attn_chunk(AttnArgs a) {
       const int lim = is_page(page_at(t0)) ? vis : 0;
       uint32_t in;
       if constexpr (TREE) {
-        in = tree_bits(a.masks + (size_t)(s0 + col) * a.mask_words, a.mask_words, len - n_all, t0, lim);
+        in = tree_bits(sh_mask + (32 * wave + m) * (a.mask_words + 1), a.mask_words, len - n_all, t0,
+                       lim);
         const uint32_t mine = in >> (4 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!((mine >> (8 * (i >> 2) + (i & 3))) & 1u)) o[i] = kNegInf;
+        for (int i = 0; i < 16; ++i) o[i] = if_bit(mine, 8 * (i >> 2) + (i & 3), o[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -1591,7 +1615,9 @@ hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
       : p.rt == 1           ? (one ? k_attn<NB, 1, 1, W1, TREE> : k_attn<NB, 1, 1, kWaves, TREE>)
                             : (one ? k_attn<NB, 1, RT, W1, TREE> : k_attn<NB, 1, RT, kWaves, TREE>);
   const size_t lds =
-      p.chunk ? 2 * sizeof(ChunkK<NB>) + 2 * sizeof(ChunkV<NB>) + 2 * NB * kChunkWaves : 0;
+      p.chunk ? 2 * sizeof(ChunkK<NB>) + 2 * sizeof(ChunkV<NB>) + 2 * NB * kChunkWaves +
+                    (TREE ? (size_t)kChunkRows * (a.mask_words + 1) * 4 : 0)
+              : 0;
   const hipError_t e = launch_k(k, grid, block, lds, s, a);
   if (e != hipSuccess || p.splits == 1) return e;
   const long long rh = (long long)a.n_rows * a.heads;
