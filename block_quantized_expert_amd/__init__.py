@@ -52,8 +52,8 @@ RFPX_ROPE_HALF, RFPX_ROPE_PAIRS = 0, 1
 
 # ... and include/rfpx_verify.h
 VERIFY_SYMBOLS = (
-    "rfpx_tree_masks", "rfpx_attn_tree_forward", "rfpx_sample_workspace_bytes", "rfpx_sample",
-    "rfpx_tree_accept", "rfpx_kv_commit",
+    "rfpx_tree_masks", "rfpx_attn_tree_workspace_bytes", "rfpx_attn_tree_forward",
+    "rfpx_sample_workspace_bytes", "rfpx_sample", "rfpx_tree_accept", "rfpx_kv_commit",
 )
 TREE_COLS_MAX = 1024
 
@@ -157,6 +157,7 @@ def lib():
             "rfpx_kv_evict_workspace_bytes": (S, [KP, BP, I]),
             "rfpx_kv_evict": (I, [KP, BP, I, I, P, P, P, P, P, P, S, P]),
             "rfpx_tree_masks": (I, [BP, I, P, P, I, P, P, P]),
+            "rfpx_attn_tree_workspace_bytes": (S, [KP, BP, I, I]),
             "rfpx_attn_tree_forward": (I, [KP, BP, P, L, I, I, I, F, P, I, P, L, P, P, S, P]),
             "rfpx_sample_workspace_bytes": (S, [I, I, I]),
             "rfpx_sample": (I, [P, L, I, I, I, P, P, P, P, P, P, P, P, S, P]),
@@ -832,6 +833,10 @@ def rfpx_tree_masks(batch: KvBatch, parents, base=None, mask_words: Optional[int
     return masks, positions
 
 
+def rfpx_attn_tree_workspace_bytes(cache: KvCache, batch: KvBatch, heads: int, rows: int) -> int:
+    return lib().rfpx_attn_tree_workspace_bytes(cache.ref, batch.ref, heads, rows)
+
+
 def rfpx_attn_tree_forward(cache: KvCache, batch: KvBatch, q, masks, scale: Optional[float] = None,
                            out=None, lse=None, ws=None, stream=None):
     """rfpx_attn_forward for a tree: every column sees the context and those of
@@ -849,9 +854,9 @@ def rfpx_attn_tree_forward(cache: KvCache, batch: KvBatch, q, masks, scale: Opti
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
     if ws is None:
-        n = rfpx_attn_workspace_bytes(cache, batch, heads, rows)
+        n = rfpx_attn_tree_workspace_bytes(cache, batch, heads, rows)
         if n == 0:
-            raise RfpxError("rfpx_attn_workspace_bytes", -2, lib().rfpx_last_error().decode())
+            raise RfpxError("rfpx_attn_tree_workspace_bytes", -2, lib().rfpx_last_error().decode())
         ws = _new(q, n, torch.uint8, stream)
     dev = _same_device(torch, cache.pool, batch.lens, q, masks, out, lse, ws)
     qp, qs = _rows("q", q)

@@ -1547,8 +1547,17 @@ struct AttnPlan {
 // of 128, rows of a sequence x tokens, k_attn and k_attn_chunk in us: 8192 x
 // 8192 422, 293; 8192 x 2048 95, 82; 512 x 16384 77, 61; and without that
 // 256 x 4096 (two sequences) 36, 43; 256 x 500 16, 30.
+//
+// Trees (several columns, whatever the length) take blocks of 16 rows also where
+// a wave then has eight tiles or fewer: there a wave's chain of tiles is longer
+// than what decoding them twice costs the chip.  Blocks of 32 and of 16 rows in
+// us, 8 kv heads of 128, columns x tokens: 16 x 1021 16.4, 11.8; 5 x 8192 20.6,
+// 14.6; 16 x 16384 27.0, 23.4; 16 sequences of 8 x 2000 22.7, 20.9; and at 16
+// tiles a wave 16 x 32768 32.4, 33.3; 8 of 16 x 4000 28.3, 29.0.  And of fp32
+// heads of 64, whose sums leave room for three workgroups a compute unit, they
+// fill that: 8 sequences of 12 columns to 8192 tokens 46.8 -> 35.5 us.
 AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, int n_rows,
-                   int xtype) {
+                   int xtype, bool tree) {
   AttnPlan p;
   const int group = heads / c->n_kv_heads;
   const long long rows = (long long)(b->max_cols > 1 ? b->max_cols : 1) * group;
@@ -1571,6 +1580,9 @@ AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, in
       p.splits = (int)s;
     }
   }
+  const long long few = 8 * 512 * kWaves;  // tiles of all workgroups, eight a wave
+  if (tree && pairs * ((rows + 15) / 16) * ((len + kTile - 1) / kTile) <= few) p.rt = 1;
+  const long long fill = tree && xtype == RFPX_X_F32 && c->head_dim == 64 ? 768 : 512;
   const long long block = p.chunk ? kChunkRows : 16 * p.rt;
   p.row_blocks = (int)clamp((rows + block - 1) / block, 1, most_rb);
   if (!p.chunk) {
@@ -1580,7 +1592,7 @@ AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, in
       p.splits = 1;
     } else {
       p.waves = kWaves;
-      p.splits = (int)clamp(clamp(512 / wgs, 1, 128), 1, (tiles + kWaves - 1) / kWaves);
+      p.splits = (int)clamp(clamp(fill / wgs, 1, 128), 1, (tiles + kWaves - 1) / kWaves);
       if (p.splits < 1) p.splits = 1;
     }
   }
@@ -1631,6 +1643,14 @@ hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
   return launch_k(j, jg, dim3(kThreads), 0, s, a);
 }
 
+size_t attn_workspace(const char *fn, const rfpx_kv_cache *c, const rfpx_kv_batch *b, int n_heads,
+                      int n_rows, bool tree) {
+  if (check_kv(fn, c, b, false) || check_heads(fn, c, n_heads, n_rows, RFPX_X_F32, 1.f)) return 0;
+  const size_t f = attn_plan(c, b, n_heads, n_rows, RFPX_X_F32, tree).total;
+  const size_t h = attn_plan(c, b, n_heads, n_rows, RFPX_X_BF16, tree).total;
+  return f > h ? f : h;
+}
+
 // rfpx_attn_forward, and with masks rfpx_attn_tree_forward.
 rfpx_status attn_forward(const char *fn, const rfpx_kv_cache *c, const rfpx_kv_batch *b,
                          const void *q, long long q_stride, int xtype, int n_heads, int n_rows,
@@ -1646,7 +1666,7 @@ rfpx_status attn_forward(const char *fn, const rfpx_kv_cache *c, const rfpx_kv_b
   if ((uintptr_t)lse % 4) return fail(RFPX_E_ALIGN, "%s: lse not 4-byte aligned", fn);
   if (!ws) return fail(RFPX_E_ARG, "%s: workspace is null", fn);
   if ((uintptr_t)ws % 256) return fail(RFPX_E_ALIGN, "%s: workspace not 256-byte aligned", fn);
-  const AttnPlan p = attn_plan(c, b, n_heads, n_rows, xtype);
+  const AttnPlan p = attn_plan(c, b, n_heads, n_rows, xtype, masks != nullptr);
   if (ws_bytes < p.total)
     return fail(RFPX_E_WORKSPACE, "%s: workspace holds %zu bytes, needs %zu", fn, ws_bytes, p.total);
   AttnArgs a{};
@@ -1688,11 +1708,12 @@ extern "C" {
 
 size_t rfpx_attn_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int n_heads,
                                  int n_rows) {
-  const char *fn = "rfpx_attn_workspace_bytes";
-  if (check_kv(fn, c, b, false) || check_heads(fn, c, n_heads, n_rows, RFPX_X_F32, 1.f)) return 0;
-  const size_t f = attn_plan(c, b, n_heads, n_rows, RFPX_X_F32).total;
-  const size_t h = attn_plan(c, b, n_heads, n_rows, RFPX_X_BF16).total;
-  return f > h ? f : h;
+  return attn_workspace("rfpx_attn_workspace_bytes", c, b, n_heads, n_rows, false);
+}
+
+size_t rfpx_attn_tree_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int n_heads,
+                                      int n_rows) {
+  return attn_workspace("rfpx_attn_tree_workspace_bytes", c, b, n_heads, n_rows, true);
 }
 
 rfpx_status rfpx_attn_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b, const void *q,

@@ -46,13 +46,17 @@ rfpx_status rfpx_tree_masks(const rfpx_kv_batch *b, int n_rows, const int32_t *p
                             const int32_t *base_dev, int mask_words, uint32_t *masks_dev,
                             int32_t *positions_dev, void *stream);
 
+/* Workspace of rfpx_attn_tree_forward; 0 if unsupported.  As
+ * rfpx_attn_workspace_bytes. */
+size_t rfpx_attn_tree_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int n_heads,
+                                      int n_rows);
+
 /* rfpx_attn_forward with other slots seen: column i of n sees slots 0 ..
  * lens[b] - n - 1, and of the step's slots lens[b] - n + j those whose bit j
  * is set in masks_dev [n_rows][mask_words] (its own among them: the bits alone
  * decide; bits of columns that do not exist, and columns that have no bit, are
  * not seen).  A column whose own slot is negative sees nothing.  Everything
- * else is as rfpx_attn_forward has it, the workspace too
- * (rfpx_attn_workspace_bytes). */
+ * else is as rfpx_attn_forward has it. */
 rfpx_status rfpx_attn_tree_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b,
                                    const void *q_dev, long long q_stride, int xtype, int n_heads,
                                    int n_rows, float scale, const uint32_t *masks_dev,

@@ -181,6 +181,9 @@ FORMS = [  # lens, cols, kv heads, group, head_dim, page, plan
     ([2000, 60], [7, 60], 2, 4, 128, 256, 131071),              # many splits, most of them empty
     ([500], [40], 2, 8, 128, 64, 65536),                        # the kernel of many rows
     ([1300, 37, 250], [30, 37, 17], 8, 8, 64, 32, 65536),
+    ([300, 37], [16, 9], 2, 4, 128, 64, 65536), ([310, 90], [16, 16], 2, 4, 64, 32, 65536),  # blocks of 32 rows
+    ([17 + i % 90 for i in range(70)], [16 - i % 3 for i in range(70)], 2, 4, 64, 32, 1000),  # ... in one launch
+    ([17 + i % 90 for i in range(70)], [16 - i % 3 for i in range(70)], 2, 4, 128, 64, 1000),
 ]
 
 

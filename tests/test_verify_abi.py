@@ -126,3 +126,11 @@ def test_sample_refusals(lib):
     for xt in (0, 1):
         assert lib.rfpx_sample_workspace_bytes(0, 1, xt) >= 256
         assert lib.rfpx_sample_workspace_bytes(1, 1 << 20, xt) >= 256
+
+
+def test_tree_workspace_depends_on_sizes_alone(lib):
+    one = lib.rfpx_attn_tree_workspace_bytes(C.byref(cache()), C.byref(batch()), 32, 5)
+    bare = lib.rfpx_attn_tree_workspace_bytes(C.byref(cache(pool=None)), C.byref(batch(lens=None, starts=None)), 32, 5)
+    assert one == bare >= 256
+    assert lib.rfpx_attn_tree_workspace_bytes(C.byref(cache()), C.byref(batch()), 12, 5) == 0
+    assert b"rfpx_attn_tree_workspace_bytes" in lib.rfpx_last_error()
