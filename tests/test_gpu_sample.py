@@ -59,13 +59,13 @@ class Expected:
             target = max(p, 0.0) * upto[-1]
             keep = min(int(np.searchsorted(upto, target)) + 1, w.size) if target > 0 else 1
             near = np.abs(upto - target).min()
-            self.clear = target == 0 or (w == 1).all() or near > 2 * self.e(upto[-1])
+            self.clear = target == 0 or ((w == 1) | (w == 0)).all() or near > 2 * self.e(upto[-1])
             order, w, upto = order[:keep], w[:keep], upto[:keep]
         else:
             self.clear = True
         if m > 0:
             m = min(m, 1.0)
-            self.clear &= bool(((np.abs(w - m) > 2 * self.e(1.0)) | (w == m)).all())
+            self.clear &= bool(((np.abs(w - m) > 2 * self.e(1.0)) | ((w == m) & (w == 1))).all())
             keep = int((w >= m).sum())
             order, w, upto = order[:keep], w[:keep], upto[:keep]
         self.order, self.w, self.upto, self.whole = order, w, upto, upto[-1]
@@ -255,6 +255,77 @@ def test_bins_that_hold_much():
         tokens, probs = sample(x, u, *zip(*s))
         for i in range(6):
             Expected(x[i].double().cpu().numpy(), *s[i]).check(tokens[i], probs[i], u[i])
+
+
+def bad_rows(n):
+    inf, nan = float("inf"), float("nan")
+    base = np.linspace(-3, 3, n)
+    at = np.arange(n)
+    return {
+        "none": np.full(n, -inf), "one": np.where(at == n - 2, 1.0, -inf), "last": np.where(at < n - 9000, -inf, base),
+        "masked": np.where(at % 3 == 0, base, -inf), "nan among": np.where(at % 5 == 0, nan, base),
+        "lowest": np.where(at % 2 == 0, -3.3895313892515355e38, base), "all lowest": np.full(n, -3.3895313892515355e38),
+        "inf": np.where(np.isin(at, (5, n - 7)), inf, base),
+        "far apart": np.where(at == 9, 3.3895313892515355e38, -3.3895313892515355e38),
+        "large": base * 1e30, "large and equal": np.where(at % 4 == 0, 2.0 ** 100, base),
+    }
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [40000, 131073])
+def test_numbers_that_are_no_logits_in_long_rows(n, dtype):
+    """As above, where rows are cut into slices, some of them without tokens."""
+    T = torch()
+    rows = bad_rows(n)
+    x = T.tensor(np.stack(list(rows.values())), device="cuda").to(getattr(T, dtype))
+    host = x.double().cpu().numpy()
+    r = len(rows)
+    for t, k, p, m in [(1.0, 0, 1.0, 0.0), (0.0, 0, 1.0, 0.0), (1.0, 7, 1.0, 0.0), (1.0, 0, 0.77, 0.0),
+                       (1.0, 0, 1.0, 0.123), (1.0, 300, 0.5, 0.9), (1e30, 0, 1.0, 0.0), (2.0 ** -140, 0, 0.9, 0.0)]:
+        u = 0.4321
+        tokens, probs = sample(x, [u] * r, [t] * r, [k] * r, [f32(p)] * r, [f32(m)] * r)
+        for i, name in enumerate(rows):
+            print(name, t, k, p, m, tokens[i], probs[i])
+            Expected(host[i], f32(t), k, f32(p), f32(m)).check(tokens[i], probs[i], f32(u))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_slices_that_list_too_much(dtype):
+    """Long rows whose first few, or tokens of some weight, are more than a
+    slice lists: in every slice, in one, and beside slices without any."""
+    T = torch()
+    rng = np.random.default_rng(31)
+    n = 131072
+    flat = np.full(n, 1.5)
+    one = rng.normal(size=n)
+    one[20000:24000] = 6.0
+    rare = np.full(n, -np.inf)
+    rare[50000:53000] = 2.0
+    rare[90000:90010] = np.linspace(1, 3, 10)
+    near = 8 + rng.random(n) * 0.5
+    rows = [flat, one, rare, near] * 6
+    s = [(1.0, 50, 1.0, 0.0), (1.0, 250, f32(0.5), 0.0), (1.0, 0, 1.0, f32(0.01)), (1.0, 0, f32(0.9), f32(0.3)),
+         (0.7, 3000, f32(0.8), f32(0.2)), (2.0, 200, f32(0.99), f32(0.6))]
+    s = [x for x in s for _ in range(4)]
+    x = T.tensor(np.stack(rows), device="cuda").to(getattr(T, dtype))
+    u = rng.random(24).astype(np.float32)
+    tokens, probs = sample(x, u, *zip(*s))
+    for i in range(24):
+        Expected(x[i].double().cpu().numpy(), *s[i]).check(tokens[i], probs[i], u[i])
+
+
+@pytest.mark.parametrize("dtype,n,rows", [("float32", 33000, 1100), ("bfloat16", 40001, 530), ("float32", 1 << 20, 3),
+                                          ("bfloat16", (1 << 20) - 7, 3)])
+def test_more_rows_than_are_done_at_once(dtype, n, rows):
+    T = torch()
+    g = T.Generator(device="cuda").manual_seed(n)
+    rng = np.random.default_rng(rows)
+    x = (T.randn((rows, n), generator=g, device="cuda") * 2).to(getattr(T, dtype))
+    u = rng.random(rows).astype(np.float32)
+    s = settings(rows, rng)
+    tokens, probs = sample(x, u, *zip(*s))
+    for i in [*range(0, rows, 97), rows - 1, *range(min(rows, 511), min(rows, 514))]:
+        Expected(x[i].double().cpu().numpy(), *s[i]).check(tokens[i], probs[i], u[i])
 
 
 def test_many_rows_draw_as_they_weigh():
