@@ -26,8 +26,8 @@
 //                     logit; and, if the row keeps the first of few, or tokens
 //                     of some weight, all of the slice that can be among them,
 //                     a list; or else the slice's weights by bin
-//   k_sample_decide   a workgroup a row: rows of lists are done; of the others
-//                     the bins that the questions fall into
+//   k_sample_decide   a workgroup a row: of rows of the second kind the bins
+//                     that the questions fall into
 //   k_sample_collect  the tokens of those bins (these rows are read once more)
 //   k_sample_pick     a workgroup a row: the questions
 // A slice's weights are relative to a power of two of its own, and shifted where
@@ -91,10 +91,9 @@ struct Sums {  // of a bin and those before it
   uint32_t count[kBins];
 };
 
-// What k_sample_decide says of a row that is not done.
+// What k_sample_decide says of a row without lists.
 struct RowState {
   float largest;
-  int first;
   Need need;
   Sums bins;
 };
@@ -108,7 +107,7 @@ struct SampleArgs {
   long long stride;
   int n_rows, vocab, bits;  // weights are multiples of 2^-bits
   int row0, rows, slices;
-  int *active;       // [1 + rows]: how many rows are not done, and which
+  int *active;       // [1 + rows]: how many rows have no lists, and which
   RowState *state;   // [rows]
   SliceHead *heads;  // [rows][slices]
   u64 *mass;         // [rows][slices][kBins]
@@ -1243,35 +1242,12 @@ __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row 
 template <typename T>
 __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   __shared__ Shared sh;
-  const int lane = threadIdx.x & 63;
   const int r = blockIdx.x, at = a.row0 + r;
-  const SliceHead *heads = a.heads + (size_t)r * a.slices;
   const Ask q = ask_of(a, at);
-  const Joined joined = join_heads(heads, a.slices, q);
-  if (joined.largest == kNegInf) return write(a, at, -1, 0.f);
-  if (q.greedy()) return write(a, at, joined.first, 1.f);
+  if (q.greedy()) return;
+  const Joined joined = join_heads(a.heads + (size_t)r * a.slices, a.slices, q);
+  if (joined.largest == kNegInf || joined.whole) return;
   const Row row = row_of<T>(joined.largest, q.temperature, a.bits);
-  u64 whole;
-  if (joined.whole) {
-    // all weights, and what the slices' own first top_k leave for the row's
-    // (every wave for itself; the lists' lengths all the same)
-    u64 all = 0;
-    uint32_t last = kBins - 1;
-    for (int s = lane; s < a.slices; s += 64) {
-      const SliceHead h = heads[s];
-      sh.length[s] = h.listed;
-      if (!(h.largest > kNegInf)) continue;
-      if (q.all()) all += h.total >> slice_shift(row, h);
-      last = min(last, (uint32_t)row_bin(row, h.base, h.last));
-    }
-    all = wave_sum(all);
-    last = wave_min(last);
-    const GatherSource gather{a.list + (size_t)r * a.slices * kSliceList, sh.length, a.slices};
-    const int n = list_tokens(gather, gather, sh, limits_of(row, q, (int)last));
-    const Found f = n <= kList ? listed_row(sh, n, row, q, !q.all(), all, &whole)
-                               : whole_row(gather, gather, sh, row, q, !q.all(), all, &whole);
-    return write(a, at, f.token, (float)((double)f.own / (double)whole));
-  }
   join_bins(a, r, row, q, sh);
   const u64 all = sh.bins.mass[kBins - 1];
   const Need need = need_of(sh.bins, row, q, all, all, false);
@@ -1282,7 +1258,6 @@ __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   }
   if (threadIdx.x == 0) {
     state.largest = joined.largest;
-    state.first = joined.first;
     state.need = need;
     a.active[1 + atomicAdd(a.active, 1)] = r;
   }
@@ -1311,16 +1286,45 @@ __global__ __launch_bounds__(kNarrow) void k_sample_collect(SampleArgs a) {
   }
 }
 
+// A row whose slices have listed all that may stay.
+__device__ __forceinline__ void pick_listed(const SampleArgs &a, int r, Shared &sh, const Row &row,
+                                            const Ask &q) {
+  const int lane = threadIdx.x & 63, at = a.row0 + r;
+  const SliceHead *heads = a.heads + (size_t)r * a.slices;
+  u64 whole;
+  // all weights, and what the slices' own first top_k leave for the row's
+  // (every wave for itself; the lists' lengths all the same)
+  u64 all = 0;
+  uint32_t last = kBins - 1;
+  for (int s = lane; s < a.slices; s += 64) {
+    const SliceHead h = heads[s];
+    sh.length[s] = h.listed;
+    if (!(h.largest > kNegInf)) continue;
+    if (q.all()) all += h.total >> slice_shift(row, h);
+    last = min(last, (uint32_t)row_bin(row, h.base, h.last));
+  }
+  all = wave_sum(all);
+  last = wave_min(last);
+  const GatherSource gather{a.list + (size_t)r * a.slices * kSliceList, sh.length, a.slices};
+  const int n = list_tokens(gather, gather, sh, limits_of(row, q, (int)last));
+  const Found f = n <= kList ? listed_row(sh, n, row, q, !q.all(), all, &whole)
+                             : whole_row(gather, gather, sh, row, q, !q.all(), all, &whole);
+  write(a, at, f.token, (float)((double)f.own / (double)whole));
+}
+
 template <typename T>
 __global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
   __shared__ Shared sh;
-  if ((int)blockIdx.x >= a.active[0]) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int r = a.active[1 + blockIdx.x], at = a.row0 + r;
+  const int r = blockIdx.x, at = a.row0 + r;
   const SliceHead *heads = a.heads + (size_t)r * a.slices;
   const Ask q = ask_of(a, at);
+  const Joined joined = join_heads(heads, a.slices, q);
+  if (joined.largest == kNegInf) return write(a, at, -1, 0.f);
+  if (q.greedy()) return write(a, at, joined.first, 1.f);
+  const Row row = row_of<T>(joined.largest, q.temperature, a.bits);
+  if (joined.whole) return pick_listed(a, r, sh, row, q);
   const RowState &state = a.state[r];
-  const Row row = row_of<T>(state.largest, q.temperature, a.bits);
   const Need need = state.need;
   for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
     sh.bins.mass[i] = state.bins.mass[i];
