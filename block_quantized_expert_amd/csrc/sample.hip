@@ -285,8 +285,14 @@ struct Shared {
   u64 upto, own;
   uint32_t in_count, key_lo, key_hi;
   int n_list, n_small, token;
-  // of a row's slices
-  int length[kMostSlices + kBatch];
+  int length[kMostSlices + kBatch];  // of the slices' lists
+};
+
+// What one that joins a row's slices shares.
+struct Joining {
+  Hist hist;
+  Sums bins;
+  int length[kMostSlices + kBatch];  // of lists (-1: weights by bin)
   float base[kMostSlices + kBatch];
   int shift[kMostSlices + kBatch];
 };
@@ -1203,7 +1209,7 @@ __device__ __forceinline__ int slice_shift(const Row &row, const SliceHead &h) {
 // kMiddle), kBatch slices' loads at once.  Of a slice that has listed all that may
 // stay, that.
 __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row &row, const Ask &q,
-                                          Shared &sh) {
+                                          Joining &sh) {
   const int t = threadIdx.x;
   const bool counts = q.top_k != 0;
   clear_histogram(sh.hist);
@@ -1241,7 +1247,7 @@ __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row 
 
 template <typename T>
 __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
-  __shared__ Shared sh;
+  __shared__ Joining sh;
   const int r = blockIdx.x, at = a.row0 + r;
   const Ask q = ask_of(a, at);
   if (q.greedy()) return;
