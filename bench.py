@@ -133,7 +133,9 @@ KERNEL_SOURCES = {"k_gateup": _DECODE_SOURCES, "k_down": _DECODE_SOURCES,
                   "k_attn_weights": ("attn.hip", *_ATTENTION_SOURCES),
                   "k_norm_rope": ("kvcache.hip", *_ATTENTION_SOURCES),
                   "k_kv_append": ("kvcache.hip", *_ATTENTION_SOURCES),
-                  "k_evict_select": ("evict.hip", *_ATTENTION_SOURCES)}
+                  "k_evict_select": ("evict.hip", *_ATTENTION_SOURCES),
+                  "k_kv_commit": ("tree.hip", *_ATTENTION_SOURCES),
+                  "k_sample_slices": ("sample.hip", "rfpx_impl.hpp", "abi.hip")}
 
 
 def kernel_source_hash(kernel: str, root: str = ROOT) -> str:
