@@ -53,7 +53,7 @@ constexpr int kCopies = 1 << kCopyLog;
 constexpr int kFewLog = 4;   // ... of one of few bins, where most of them do
 constexpr int kFewBins = kBins * kCopies >> kFewLog;
 constexpr int kList = 6144;  // tokens that answer() has in LDS
-constexpr int kSmall = 64;   // tokens that one wave ranks
+constexpr int kRank = 256;   // tokens that find() ranks by comparing each with all
 constexpr float kBinsPerOctave = 10.f;  // 51 octaves, which is all that weighs anything
 constexpr uint32_t kNoToken = 0x007FFFFFu;  // key of -inf, which NaN gets too
 constexpr float kNegInf = -__builtin_inff();
@@ -61,7 +61,8 @@ constexpr int kRowMost = 32 * kWide;  // logits of a row that is not cut into sl
 constexpr int kSlice = 32 * kNarrow;  // logits of a slice
 constexpr int kSliceList = kMiddle;   // tokens that a slice may list
 static_assert(kBins == kMiddle, "a thread a bin");
-constexpr int kBatch = 8;  // slices whose loads are in flight at once
+constexpr int kBatch = 4;       // loads of lists that are in flight at once
+constexpr int kBinsBatch = 24;  // ... of slices' bins
 constexpr int kMostSlices = RFPX_VOCAB_MAX / kSlice + 1;
 constexpr int kTopMost = 256;     // top_k of rows whose slices list their tokens
 constexpr int kRowsAtOnce = 512;  // rows of one set of launches, which bounds the workspace
@@ -209,6 +210,16 @@ __device__ __forceinline__ u64 weight(const Row &r, float v, int bin) {
 }
 __device__ __forceinline__ u64 weight(const Row &r, float v) { return weight(r, v, bin_of(r, v)); }
 
+// v >> n, of a lane's own n below 64, by operations of 32 bits.  (A 64-bit shift
+// whose amount lies in the last register that a wave has been given shifts some
+// lanes by something else when waves share a SIMD.  Amounts that all lanes share
+// are scalars.)
+__device__ __forceinline__ u64 shifted(u64 v, int n) {
+  const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+  const uint32_t low = __builtin_amdgcn_alignbit(hi, lo, (uint32_t)n & 31), high = hi >> (n & 31);
+  return n < 32 ? (u64)high << 32 | low : high;
+}
+
 // x as a fraction of 2^64, below 1.
 __device__ __forceinline__ u64 fraction(float x) {
   if (!(x > 0.f)) return 0;
@@ -267,7 +278,7 @@ __device__ __forceinline__ U wave_min(U v) {
 
 struct Hist {
   alignas(16) u64 mass[kBins * kCopies];
-  uint32_t count[kBins * kCopies];
+  alignas(16) uint32_t count[kBins * kCopies];
   u64 wave_mass[kSumWaves];
   uint32_t wave_count[kSumWaves];
 };
@@ -279,22 +290,21 @@ struct Shared {
   uint32_t key[kList];
   int32_t index[kList];
   u64 sum[kMostWaves];
-  uint32_t small_key[kSmall];
-  int32_t small_index[kSmall];
-  // answers of wave 0
+  // answers, and what is found out for them
   u64 upto, own;
-  uint32_t in_count, key_lo, key_hi;
-  int n_list, n_small, token;
-  int length[kMostSlices + kBatch];  // of the slices' lists
+  uint32_t key_lo, key_hi;
+  int n_list, n_in, token;
+  uint32_t ranks[kWide];
+  int length[kMostSlices];  // of the slices' lists
 };
 
 // What one that joins a row's slices shares.
 struct Joining {
   Hist hist;
   Sums bins;
-  int length[kMostSlices + kBatch];  // of lists (-1: weights by bin)
-  float base[kMostSlices + kBatch];
-  int shift[kMostSlices + kBatch];
+  int length[kMostSlices + kBinsBatch];  // of lists (-1: weights by bin)
+  float base[kMostSlices + kBinsBatch];
+  int shift[kMostSlices + kBinsBatch];
 };
 
 // -------------------------------------------------------- sources of tokens
@@ -442,53 +452,65 @@ struct ListSource {
   }
 };
 
-// The lists of a row's slices, whose lengths are in LDS: a thread a place in the
-// lists (kMiddle threads), kBatch slices' loads at once.
+// The lists of a row's slices, whose lengths are in LDS (below 0: none): a wave
+// takes 64 tokens of a list, kBatch times at once.
 struct GatherSource {
-  static constexpr int B = kBatch;
   const uint2 *list;
   const int *lengths;
   int slices;
-  __device__ __forceinline__ void load(int s0, uint2 (&e)[B]) const {
-    const int t = threadIdx.x;
+  // f(kBatch entries), kNoToken where there is none
+  template <typename F>
+  __device__ __forceinline__ void batches(F &&f) const {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6;
+#pragma unroll 1
+    for (int s0 = 0; s0 < slices; s0 += 64) {
+      const int len = s0 + lane < slices ? max(lengths[s0 + lane], 0) : 0;
+      const uint32_t upto = running_sum((uint32_t)(len + 63) / 64);
+      const int all = (int)lane_of(upto, 63);
+#pragma unroll 1
+      for (int k0 = wave; k0 < all; k0 += kBatch * waves) {
+        uint2 e[kBatch];
 #pragma unroll
-    for (int j = 0; j < B; ++j)
-      e[j] = s0 + j < slices && t < lengths[s0 + j] ? list[(size_t)(s0 + j) * kSliceList + t]
-                                                    : make_uint2(kNoToken, 0);
+        for (int j = 0; j < kBatch; ++j) {
+          const int k = k0 + j * waves;
+          const int s = __popcll(__ballot((int)upto <= k));  // (64: there is none)
+          const int at = (k - (s ? (int)lane_of(upto, s - 1) : 0)) * 64 + lane;
+          e[j] = s < 64 && at < (int)lane_of((uint32_t)len, s & 63)
+                     ? list[(size_t)(s0 + s) * kSliceList + at]
+                     : make_uint2(kNoToken, 0);
+        }
+        f(e);
+      }
+    }
   }
   template <typename F>
   __device__ __forceinline__ void each(F &&f) const {
+    batches([&](uint2 (&e)[kBatch]) {
 #pragma unroll 1
-    for (int s0 = 0; s0 < slices; s0 += B) {
-      uint2 e[B];
-      load(s0, e);
-#pragma unroll 1
-      for (int j = 0; j < B; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         if (e[0].x > kNoToken) f(value_of(e[0].x), (int)e[0].y);
 #pragma unroll
-        for (int i = 0; i < B - 1; ++i) e[i] = e[i + 1];
+        for (int i = 0; i < kBatch - 1; ++i) e[i] = e[i + 1];
       }
-    }
+    });
   }
   // f(place, key, index) for those that `in` picks: a wave takes its places from
   // `counter` a batch at a time.
   template <typename In, typename F>
   __device__ __forceinline__ void pick(int *counter, In &&in, F &&f) const {
-#pragma unroll 1
-    for (int s0 = 0; s0 < slices; s0 += B) {
-      uint2 e[B];
-      load(s0, e);
+    batches([&](uint2 (&e)[kBatch]) {
       uint32_t mask = 0;
 #pragma unroll
-      for (int j = 0; j < B; ++j) mask |= e[j].x > kNoToken && in(value_of(e[j].x)) ? 1u << j : 0u;
+      for (int j = 0; j < kBatch; ++j)
+        mask |= e[j].x > kNoToken && in(value_of(e[j].x)) ? 1u << j : 0u;
       const uint32_t mine = __popc(mask), upto = running_sum(mine);
       int place = 0;
       if ((threadIdx.x & 63) == 63 && upto) place = atomicAdd(counter, (int)upto);
       place = __builtin_amdgcn_readlane(place, 63) + (int)(upto - mine);
 #pragma unroll
-      for (int j = 0; j < B; ++j)
+      for (int j = 0; j < kBatch; ++j)
         if (mask >> j & 1u) f(place++, e[j].x, (int)e[j].y);
-    }
+    });
   }
 };
 
@@ -525,11 +547,17 @@ __device__ __forceinline__ void sum_histogram(Hist &h, Sums &to, int log = kCopy
   uint32_t c0 = 0, c1 = 0, c = 0;
   if (wave < kSumWaves) {
     if ((2 * t + 1) << log < kBins * kCopies) {
-      for (int k = 0; k < 1 << log; ++k) {
-        m0 += h.mass[(2 * t << log) + k];
-        m1 += h.mass[((2 * t + 1) << log) + k];
-        c0 += h.count[(2 * t << log) + k];
-        c1 += h.count[((2 * t + 1) << log) + k];
+      static_assert(kCopies == 2 && (1 << kFewLog) % kCopies == 0, "copies in pairs");
+#pragma unroll 4
+      for (int k = 0; k < 1 << log; k += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&h.mass[(2 * t << log) + k]);
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&h.mass[((2 * t + 1) << log) + k]);
+        const uint2 u = *reinterpret_cast<const uint2 *>(&h.count[(2 * t << log) + k]);
+        const uint2 v = *reinterpret_cast<const uint2 *>(&h.count[((2 * t + 1) << log) + k]);
+        m0 += x.x + x.y;
+        m1 += y.x + y.y;
+        c0 += u.x + u.y;
+        c1 += v.x + v.y;
       }
     }
     m = running_sum(m0 + m1);
@@ -572,6 +600,31 @@ struct Found {
   int token;  // its index, if that was asked for
 };
 
+// Ranks of n codes, no more than there are threads, by comparing each with all:
+// `ranks` (0s) gets how many are larger.  Behind the codes are 0s up to the next
+// power of two, from 64 on.  Where that is less than the workgroup, threads share
+// a code's comparisons.  (Between barriers of the caller.)
+__device__ __forceinline__ void rank_codes(const u64 *code, int n, uint32_t *ranks) {
+  const int t = threadIdx.x;
+  int log = 6;
+  while (1 << log < n) ++log;
+  const int part = uniform(t >> log), i = t & ((1 << log) - 1), parts = (int)blockDim.x >> log;
+  if (uniform(i & ~63) >= n) return;
+  const int each = ((n + parts - 1) / parts + 7) & ~7;
+  const int from = part * each, to = min(from + each, n);
+  const u64 mine = code[i];
+  uint32_t rank = 0;
+#pragma unroll 1
+  for (int j = from; j < to; j += 8) {
+    ulonglong2 c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = reinterpret_cast<const ulonglong2 *>(code + j)[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) rank += (c[k].x > mine) + (c[k].y > mine);
+  }
+  if (i < n && rank) atomicAdd(&ranks[i], rank);
+}
+
 // A place in a sum: the last one, if it is past that (sums of slices that came
 // together are off by their rounding).
 __device__ __forceinline__ u64 within(u64 r, u64 sum) { return r < sum ? r : sum ? sum - 1 : 0; }
@@ -582,40 +635,54 @@ __device__ __forceinline__ u64 within(u64 r, u64 sum) { return r < sum ? r : sum
 template <typename S>
 __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by_count, u64 r,
                       u64 above, bool want_token) {
-  const int lane = threadIdx.x & 63;
-  // the bin's keys (without the bits in which they do not differ) and how many
-  // tokens it has
-  uint32_t lo = 0xFFFFFFFFu, hi = 0, n = 0;
-  src.each([&](float v, int) {
+  const int t = threadIdx.x, wave = uniform(t >> 6);
+  u64 *const code = sh.hist.mass;      // of the tokens in question: logit, then the lower index
+  u64 *const sorted = sh.digits.mass;  // the same by rank
+  const auto begin = [&] {
+    __syncthreads();  // what was shared has been read
+    if (t < kRank) {
+      code[t] = 0;
+      sh.ranks[t] = 0;
+    }
+    if (t == 0) sh.n_in = 0;
+    __syncthreads();
+  };
+  const auto take = [&](float v, int i) {
+    const int at = atomicAdd(&sh.n_in, 1);
+    if (at < kRank) code[at] = (u64)key_of(v) << 32 | (uint32_t)~i;
+  };
+  // the bin's tokens, and their keys (without the bits in which they do not differ)
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  begin();
+  src.each([&](float v, int i) {
     if (v > kNegInf && bin_of(row, v) == bin) {
       const uint32_t k = key_of(v) >> row.key_zeros;
       lo = min(lo, k);
       hi = max(hi, k);
-      ++n;
+      take(v, i);
     }
   });
-  __syncthreads();  // the answers of an earlier call have been read
-  if (threadIdx.x == 0) {
+  if (t == 0) {
     sh.key_lo = 0xFFFFFFFFu;
     sh.key_hi = 0;
-    sh.in_count = 0;
   }
   __syncthreads();
-  lo = wave_min(lo);
-  hi = wave_max(hi);
-  n = wave_sum(n);
-  if (lane == 0 && n) {
-    atomicMin(&sh.key_lo, lo);
-    atomicMax(&sh.key_hi, hi);
-    atomicAdd(&sh.in_count, n);
+  uint32_t n = (uint32_t)sh.n_in;
+  const bool narrow = n > kRank;
+  if (narrow) {
+    lo = wave_min(lo);
+    hi = wave_max(hi);
+    if ((t & 63) == 0) {
+      atomicMin(&sh.key_lo, lo);
+      atomicMax(&sh.key_hi, hi);
+    }
+    __syncthreads();
+    lo = sh.key_lo;
+    hi = sh.key_hi;
   }
-  __syncthreads();
-  lo = sh.key_lo;
-  hi = sh.key_hi;
-  n = sh.in_count;
   int first = 0, last = 0x7FFFFFFF;  // indices that count: all, until the logit is known
   // digits of the distance from the bin's largest key, then of the index
-  while (n > kSmall && (lo < hi || (want_token && first < last))) {
+  while (n > kRank && (lo < hi || (want_token && first < last))) {
     const bool keys = lo < hi;
     if (!keys && last == 0x7FFFFFFF) {
       // all have one logit: the place among them is a division, and now ones
@@ -661,50 +728,44 @@ __device__ Found find(const S &src, Shared &sh, const Row &row, int bin, bool by
     }
   }
   Found f{above, 0, -1};
-  if (n > kSmall) {  // many of one logit, and no index asked for
+  if (n > kRank) {  // many of one logit, and no index asked for
     const u64 w = weight(row, row.value(lo));
     f.own = w;
     f.upto = above + (within(by_count ? r : w ? r / w : 0, n) + 1) * w;
     return f;
   }
-  // One wave ranks what is left.  (Where indices were counted, the weights
-  // before are in `above` already, and all weigh the same.)
+  if (narrow) {
+    begin();
+    src.each([&](float v, int i) {
+      const uint32_t k = key_of(v) >> row.key_zeros;
+      if (k >= lo && k <= hi && v > kNegInf && i >= first && i <= last) take(v, i);
+    });
+    __syncthreads();
+    n = (uint32_t)min(sh.n_in, kRank);
+  }
+  // They are ranked, and summed in that order by a thread each.
+  // (Where indices were counted, the weights before are in `above` already, and
+  // all weigh the same.)
   const bool by_index = last != 0x7FFFFFFF;
+  rank_codes(code, (int)n, sh.ranks);
   __syncthreads();
-  if (threadIdx.x == 0) sh.n_small = 0;
+  if (t < (int)n) sorted[sh.ranks[t]] = code[t];
   __syncthreads();
-  src.each([&](float v, int i) {
-    const uint32_t k = key_of(v) >> row.key_zeros;
-    if (k < lo || k > hi || !(v > kNegInf) || i < first || i > last) return;
-    const int at = atomicAdd(&sh.n_small, 1);
-    if (at < kSmall) {
-      sh.small_key[at] = key_of(v);
-      sh.small_index[at] = i;
-    }
-  });
+  const u64 mine = t < (int)n ? sorted[t] : 0;
+  const u64 w = t < (int)n ? weight(row, value_of((uint32_t)(mine >> 32))) : 0;
+  u64 sum = running_sum(w);
+  if ((t & 63) == 63) sh.sum[wave] = sum;
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int m = min(sh.n_small, kSmall);
-    const uint32_t key = lane < m ? sh.small_key[lane] : 0;
-    const int index = lane < m ? sh.small_index[lane] : 0;
-    const u64 code = lane < m ? (u64)key << 32 | (uint32_t)~index : 0;
-    int rank = 0;
-    for (int j = 0; j < m; ++j) rank += lane_of(code, j) > code;
-    if (lane < m) {
-      sh.small_key[rank] = key;
-      sh.small_index[rank] = index;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
-    const u64 w = lane < m ? weight(row, value_of(sh.small_key[lane])) : 0;
-    const u64 upto = running_sum(w);
-    r = within(r, by_count ? (u64)m : lane_of(upto, 63));
-    const uint64_t lanes = __ballot(lane < m && (by_count ? (u64)lane + 1 : upto) > r);
-    if (lane == (lanes ? __builtin_ctzll(lanes) : 0)) {
-      sh.upto = by_index ? above + w : above + upto;
-      sh.own = w;
-      sh.token = m ? sh.small_index[lane] : -1;
-    }
+  u64 all = 0;
+  for (int i = 0; i < (int)(n + 63) / 64; ++i) {
+    if (i == wave) sum += all;
+    all += sh.sum[i];
+  }
+  r = within(r, by_count ? (u64)n : all);
+  if (by_count || !all ? t == (int)r : t < (int)n && sum > r && sum - w <= r) {
+    sh.upto = by_index ? above + w : above + sum;
+    sh.own = w;
+    sh.token = n ? (int)~(uint32_t)mine : -1;
   }
   __syncthreads();
   f.upto = sh.upto;
@@ -921,21 +982,13 @@ __device__ __forceinline__ Found sorted_row(Shared &sh, int n, const Row &row, c
   const int index = t < n ? sh.index[t] : 0;
   const u64 mine = (u64)key << 32 | (uint32_t)~index;
   code[t] = t < n ? mine : 0;
+  sh.ranks[t] = 0;
   if (t == 0) sh.upto = 0;
   __syncthreads();
-  int rank = 0;
-  if (wave * 64 < n) {
-    const ulonglong2 *const two = reinterpret_cast<const ulonglong2 *>(code);
-#pragma unroll 1
-    for (int i = 0; i < (n + 1) / 2; i += 8) {  // (codes behind the list are 0)
-      ulonglong2 c[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = two[i + j];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) rank += (c[j].x > mine) + (c[j].y > mine);
-    }
-  }
+  rank_codes(code, n, sh.ranks);
+  __syncthreads();
   if (t < n) {
+    const uint32_t rank = sh.ranks[t];
     sh.key[rank] = key;
     sh.index[rank] = index;
   }
@@ -1163,15 +1216,15 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   u64 total = 0;
   for (int i = threadIdx.x; i < kBins; i += kNarrow) {
     u64 m = 0;
+#pragma unroll
+    for (int k = 0; k < kCopies; ++k) m += hist.mass[i * kCopies + k];
+    a.mass[rs * kBins + i] = m;
+    total += m;
+    if (q.top_k == 0) continue;  // (no one asks for numbers)
     uint32_t c = 0;
 #pragma unroll
-    for (int k = 0; k < kCopies; ++k) {
-      m += hist.mass[i * kCopies + k];
-      c += hist.count[i * kCopies + k];
-    }
-    a.mass[rs * kBins + i] = m;
+    for (int k = 0; k < kCopies; ++k) c += hist.count[i * kCopies + k];
     a.count[rs * kBins + i] = c;
-    total += m;
   }
   total = running_sum(total);
   if (lane == 63) sh_sum[wave] = total;
@@ -1223,19 +1276,19 @@ __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row 
   __syncthreads();
   const size_t from = (size_t)r * a.slices * kBins + t;
 #pragma unroll 1
-  for (int s0 = 0; s0 < a.slices; s0 += kBatch) {
-    u64 m[kBatch];
-    uint32_t c[kBatch];
+  for (int s0 = 0; s0 < a.slices; s0 += kBinsBatch) {
+    u64 m[kBinsBatch];
+    uint32_t c[kBinsBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (int j = 0; j < kBinsBatch; ++j) {
       const bool binned = s0 + j < a.slices && sh.length[s0 + j] < 0;
       m[j] = binned ? a.mass[from + (size_t)(s0 + j) * kBins] : 0;
       c[j] = binned && counts ? a.count[from + (size_t)(s0 + j) * kBins] : 0;
     }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (int j = 0; j < kBinsBatch; ++j) {
       if (m[j] | c[j])
-        add_to_bin(sh.hist, row_bin(row, sh.base[s0 + j], t), m[j] >> sh.shift[s0 + j], c[j]);
+        add_to_bin(sh.hist, row_bin(row, sh.base[s0 + j], t), m[j] >> uniform(sh.shift[s0 + j]), c[j]);
     }
   }
   if (q.listed()) {
@@ -1306,7 +1359,7 @@ __device__ __forceinline__ void pick_listed(const SampleArgs &a, int r, Shared &
     const SliceHead h = heads[s];
     sh.length[s] = h.listed;
     if (!(h.largest > kNegInf)) continue;
-    if (q.all()) all += h.total >> slice_shift(row, h);
+    if (q.all()) all += shifted(h.total, slice_shift(row, h));
     last = min(last, (uint32_t)row_bin(row, h.base, h.last));
   }
   all = wave_sum(all);
@@ -1319,7 +1372,7 @@ __device__ __forceinline__ void pick_listed(const SampleArgs &a, int r, Shared &
 }
 
 template <typename T>
-__global__ __launch_bounds__(kMiddle) void k_sample_pick(SampleArgs a) {
+__global__ __launch_bounds__(kMiddle, 4) void k_sample_pick(SampleArgs a) {
   __shared__ Shared sh;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = blockIdx.x, at = a.row0 + r;
