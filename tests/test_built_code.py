@@ -1,0 +1,81 @@
+"""What the built kernels must not hold (CPU: the library's own code, listed).
+
+A 64-bit shift whose amount lies in the last vector register that its wave has
+been given shifts some lanes by something else, now and then, when waves share
+a SIMD: k_sample_decide had one in a build of 96 registers, amount in v95, and
+sums of 63 bins of a wave came out wrong in a few rows of a thousand.  Amounts
+that a wave shares belong into scalars, others into shifts of 32 bits."""
+import os
+import re
+import shutil
+import struct
+import subprocess
+
+import pytest
+
+import block_quantized_expert_amd as bqe
+
+OBJDUMP = shutil.which("llvm-objdump") or "/opt/rocm/llvm/bin/llvm-objdump"
+SHIFT = re.compile(r"\bv_(?:lshlrev_b64|lshrrev_b64|ashrrev_i64)\w* +v\[\d+:\d+\], v(\d+)")
+REGISTER = re.compile(r"\bv(?:(\d+)\b|\[\d+:(\d+)\])")
+
+
+def code_objects(library):
+    """The bundled gfx950 code objects."""
+    at = library.find(b"__CLANG_OFFLOAD_BUNDLE__")
+    while at >= 0:
+        n, = struct.unpack_from("<Q", library, at + 24)
+        entry = at + 32
+        for _ in range(n):
+            offset, size, length = struct.unpack_from("<QQQ", library, entry)
+            name = library[entry + 24:entry + 24 + length]
+            entry += 24 + length
+            if size and b"gfx950" in name:
+                yield library[at + offset:at + offset + size]
+        at = library.find(b"__CLANG_OFFLOAD_BUNDLE__", at + 24)
+
+
+def last_register_shifts(listing):
+    """(kernel, register) of the shifts whose amount is a block's last register
+    with no register in use behind it."""
+    found = []
+    pieces = re.split(r"\n\w+ <([^>]+)>:\n", "\n" + listing)
+    for name, body in zip(pieces[1::2], pieces[2::2]):
+        amounts = {int(m) for m in SHIFT.findall(body)}
+        if amounts:
+            last = max(int(a or b) for a, b in REGISTER.findall(body))
+            found += [(name, a) for a in sorted(amounts) if a % 8 == 7 and a >= last]
+    return found
+
+
+def test_the_listing_is_read():
+    """The check finds what it is after, and only that."""
+    text = """
+0000000000001000 <kernel_a>:
+\tv_lshrrev_b64 v[2:3], v15, v[4:5]
+\tv_add_u32_e32 v14, v1, v2
+0000000000002000 <kernel_b>:
+\tv_lshrrev_b64 v[2:3], v15, v[4:5]
+\tglobal_load_dwordx2 v[16:17], v[4:5], off
+0000000000003000 <kernel_c>:
+\tv_lshlrev_b64 v[14:15], s3, v[4:5]
+\tv_lshrrev_b64 v[2:3], v14, v[14:15]
+"""
+    assert last_register_shifts(text) == [("kernel_a", 15)]
+
+
+def test_no_shift_by_the_last_register(tmp_path):
+    if not os.path.exists(OBJDUMP):
+        pytest.skip("no llvm-objdump here")
+    with open(bqe.LIB_PATH, "rb") as fh:
+        objects = list(code_objects(fh.read()))
+    assert objects
+    kernels = 0
+    for i, code in enumerate(objects):
+        path = tmp_path / f"{i}.o"
+        path.write_bytes(code)
+        listing = subprocess.run([OBJDUMP, "-d", "--mcpu=gfx950", "--no-show-raw-insn", str(path)],
+                                 check=True, capture_output=True, text=True).stdout
+        kernels += listing.count(">:\n")
+        assert last_register_shifts(listing) == []
+    assert kernels > 50
