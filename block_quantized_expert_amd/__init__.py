@@ -816,6 +816,8 @@ def rfpx_tree_masks(batch: KvBatch, parents, base=None, mask_words: Optional[int
     import torch
     rows = parents.shape[0]
     if masks is not None:
+        if masks.dim() != 2:
+            raise ValueError("masks must be [rows][words]")
         mask_words = masks.shape[1]
     elif mask_words is None:
         mask_words = max(1, (batch.max_cols + 31) // 32)
@@ -912,10 +914,12 @@ def rfpx_tree_accept(batch: KvBatch, parents, tokens, drawn, path=None, counts=N
     """The drafts that the drawn tokens confirm: path (int32 [seqs][path_cols],
     columns, then -1; path_cols is max_cols unless path is given), counts, the
     token drawn at the last of them, and the lengths that the sequences then
-    have.  parents, tokens and drawn are int32 [rows].  Returns (path, counts,
+    have (lens_out; batch.lens is still needed where rfpx_kv_commit follows).  parents, tokens and drawn are int32 [rows].  Returns (path, counts,
     next_tokens, lens_out)."""
     import torch
     rows, n, i32 = parents.shape[0], batch.n_seqs, torch.int32
+    if path is not None and path.dim() != 2:
+        raise ValueError("path must be [seqs][columns]")
     if path is None:
         path = _new(parents, (n, max(1, batch.max_cols)), i32, stream)
     counts = _new(parents, (n,), i32, stream) if counts is None else counts
@@ -936,6 +940,8 @@ def rfpx_kv_commit(cache: KvCache, batch: KvBatch, path, counts, acc=None, pos=N
     slots of the step, keys and values and, where given, acc (fp32) and pos
     (int32), [seqs][kv heads][slots]; lens is still that of the step."""
     import torch
+    if path.dim() != 2:
+        raise ValueError("path must be [seqs][columns]")
     n, cols = batch.n_seqs, path.shape[1]
     dev = _same_device(torch, cache.pool, batch.lens, path, counts, acc, pos)
     slots = _slots(cache, batch)

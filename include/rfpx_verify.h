@@ -85,11 +85,13 @@ size_t rfpx_sample_workspace_bytes(int n_rows, int vocab, int xtype);
  * counts as the type's largest finite number.  A row without tokens gets index
  * -1 and probability 0.
  * temperature, top_p, min_p (fp32) and top_k (int32), each [n_rows], may be
- * NULL: 1, and no cut.  u below 0 or NaN counts as 0, from 1 on as just below.
- * Weights are held as whole multiples of 2^-s, s = 50 up to 4096 tokens and
- * one less for each doubling of the vocabulary from there, and summed as whole numbers: the same
- * bit for bit from run to run, and no choice falls otherwise than in 64 bits
- * unless it lies within that rounding. */
+ * NULL: 1, and no cut (nor does a NaN of top_p or min_p cut).  u below 0 or NaN
+ * counts as 0, from 1 on as just below.  Weights are held as whole multiples of 2^-s, s = 50 up to
+ * 4096 tokens and one less for each doubling of the vocabulary from there, and
+ * summed as whole numbers: the same bit for bit from run to run, and no choice
+ * falls otherwise than in 64 bits unless it lies within that rounding.  At
+ * temperatures below 2^-100 only the tokens of the largest logit weigh
+ * anything. */
 rfpx_status rfpx_sample(const void *logits_dev, long long stride, int xtype, int n_rows, int vocab,
                         const float *u_dev, const float *temperature_dev,
                         const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev,
@@ -105,7 +107,8 @@ rfpx_status rfpx_sample(const void *logits_dev, long long stride, int xtype, int
  *   next[b]      the token drawn at the last       (int32 [n_seqs])
  *   lens_out[b]  lens[b] - n + counts[b], 0 or more  (int32 [n_seqs], or NULL)
  * A sequence without columns: no path, count 0, next -1.  lens_out may be
- * b->lens itself; rfpx_kv_commit reads the lengths from before. */
+ * b->lens itself, but not where rfpx_kv_commit follows with the same batch: that
+ * needs the lengths of the step. */
 rfpx_status rfpx_tree_accept(const rfpx_kv_batch *b, int n_rows, const int32_t *parents_dev,
                              const int32_t *tokens_dev, const int32_t *drawn_dev, int path_cols,
                              int32_t *path_dev, int32_t *counts_dev, int32_t *next_dev,

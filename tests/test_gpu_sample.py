@@ -401,3 +401,27 @@ def test_wrapper_refusals():
         with pytest.raises(bqe.RfpxError):
             bqe.rfpx_sample(kw.pop("logits"), kw.pop("u"), **kw)
     assert bqe.rfpx_sample(x[:0], u[:0]).shape == (0,)
+
+
+@pytest.mark.parametrize("seed", [1, 2])
+def test_many_long_rows_again_and_again(seed):
+    """As many rows as fill the chip several times over, in one call: every
+    row has the token and the probability that it has in a call of its own, run
+    after run (sums of many workgroups that share compute units)."""
+    T = torch()
+    g = T.Generator("cuda").manual_seed(seed)
+    rows, n = 512, 65536
+    x = T.randn((rows, n), generator=g, device="cuda") * 2.2
+    u = T.rand(rows, generator=g, device="cuda")
+    p = T.where(T.arange(rows, device="cuda") % 2 == 0, 1.0, 0.9).float()
+    one_probs = T.empty(rows, device="cuda")
+    one = T.cat([bqe.rfpx_sample(x[r:r + 1], u[r:r + 1], top_p=p[r:r + 1], probs=one_probs[r:r + 1])
+                 for r in range(rows)])
+    for _ in range(8):
+        probs = T.empty(rows, device="cuda")
+        tokens = bqe.rfpx_sample(x, u, top_p=p, probs=probs)
+        assert T.equal(tokens, one) and T.equal(probs, one_probs)
+    for r in range(0, rows, 37):
+        e = Expected(x[r].cpu().numpy(), p=float(p[r]))
+        assert e.clear
+        e.check(int(one[r]), float(one_probs[r]), float(u[r]))
