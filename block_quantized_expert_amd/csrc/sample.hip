@@ -17,8 +17,8 @@
 // same, so that a place among them is a division.
 //
 // find() narrows: bins of the distance from the largest logit, 10 an octave of
-// weight, then digits of the keys in one bin, until at most 64 tokens are left,
-// which one wave ranks, or tokens of one logit.
+// weight, then digits of the keys in one bin, until at most 256 tokens are left,
+// which are ranked by comparing each with all, or tokens of one logit.
 //
 // Rows of up to 32768 logits are a workgroup's each, in registers
 // (k_sample_row).  Longer ones are cut into slices:
@@ -31,7 +31,14 @@
 //   k_sample_collect  the tokens of those bins (these rows are read once more)
 //   k_sample_pick     a workgroup a row: the questions
 // A slice's weights are relative to a power of two of its own, and shifted where
-// the slices of a row come together.
+// the slices of a row come together (which rounds down: less than 2^-s a bin).
+//
+// Why not one workgroup for a row of any length: 64 rows would read through 64
+// compute units.  Why not slices for every row: four launches instead of one.
+// Measured on an MI355X, us a call in a graph, a workgroup a row / slices: 1 row of
+// 32000 fp32 logits by top_p 23.5 / 27.5, by top_k 14.0 / 22.2, greedy 7.3 / 10.5; 512
+// rows 67 / 81, 32 / 41, 20 / 23; 512 rows of 8000 37 / 47; one row of 4000 13.4 / 26.5.
+// Above 32768 logits the registers of a workgroup do not hold a row.
 #include "../../include/rfpx_verify.h"
 #include "rfpx_impl.hpp"
 
@@ -53,7 +60,9 @@ constexpr int kCopies = 1 << kCopyLog;
 constexpr int kFewLog = 4;   // ... of one of few bins, where most of them do
 constexpr int kFewBins = kBins * kCopies >> kFewLog;
 constexpr int kList = 6144;  // tokens that answer() has in LDS
-constexpr int kRank = 256;   // tokens that find() ranks by comparing each with all
+// Tokens that find() ranks by comparing each with all (64: one more digit, 4 us, for
+// most bins; 512: the same time as 256).
+constexpr int kRank = 256;
 constexpr float kBinsPerOctave = 10.f;  // 51 octaves, which is all that weighs anything
 constexpr uint32_t kNoToken = 0x007FFFFFu;  // key of -inf, which NaN gets too
 constexpr float kNegInf = -__builtin_inff();
@@ -1126,6 +1135,13 @@ __device__ __forceinline__ RowSource<T> logits_of(const SampleArgs &a, int at) {
 }
 
 // A workgroup a row, whose logits it holds.
+//
+// What bounds it: one compute unit.  A row of 32000 fp32 logits by top_p is 23 us:
+// 3.4 until the largest logit is known (128 KB through one compute unit), 7.5 for
+// the weights by bin (32 logits a thread, 15 operations of 64 bits each, four
+// cycles an operation and four waves on a SIMD), 2.3 for the list of the tokens in
+// question, and the questions of 2 to 4 us, chains of barriers and LDS reads.  Loops
+// over the registers are rolled: unrolled ones wait for their instructions.
 template <typename T, int N>
 __global__ __launch_bounds__(kWide) void k_sample_row(SampleArgs a) {
   __shared__ Shared sh;
@@ -1158,6 +1174,14 @@ __global__ __launch_bounds__(kWide) void k_sample_row(SampleArgs a) {
 template <typename T>
 constexpr int kPieces = kSlice / (kNarrow * RowSource<T>::E);
 
+// What bounds it: of rows that list their tokens, or take the first, HBM (512 rows
+// of 131072 fp32 logits, 268 MB: greedy 48 us, 5.5 TB/s; top_k or min_p 70, 3.8
+// TB/s); of rows whose weights go by bin, those weights, 25 vector operations a
+// logit, 15 of them of 64 bits (98 us; at four cycles each they are 45 us of every
+// SIMD's issue, and the read 52).  A wave has 76 registers, six waves on a SIMD; at
+// 64 it spills.  Tried and not kept: loads inside the loop over pieces (63 us greedy:
+// conversions between them made each wait for the one before).  Without its atomics
+// it is no faster.
 template <typename T>
 __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   __shared__ Hist hist;
@@ -1259,7 +1283,7 @@ __device__ __forceinline__ int slice_shift(const Row &row, const SliceHead &h) {
 }
 
 // Weights and counts by bin of all slices, as running sums: a thread a bin (of
-// kMiddle), kBatch slices' loads at once.  Of a slice that has listed all that may
+// kMiddle), kBinsBatch slices' loads at once.  Of a slice that has listed all that may
 // stay, that.
 __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row &row, const Ask &q,
                                           Joining &sh) {
@@ -1298,6 +1322,10 @@ __device__ __forceinline__ void join_bins(const SampleArgs &a, int r, const Row 
   sum_histogram(sh.hist, sh.bins);
 }
 
+// What bounds it: latency, of the settings, the heads, the bins and the sums in
+// turn, one after the other (64 rows 9 us, 512 rows of 17 slices, 36 MB, 11 us and 16
+// where every row comes here).  All bins of 24 slices are in flight at once: 8
+// took 11.5 and 14 us.
 template <typename T>
 __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   __shared__ Joining sh;
@@ -1322,6 +1350,8 @@ __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   }
 }
 
+// What bounds it: HBM, at 4.3 TB/s (512 rows that all come here, 268 MB, 62 us); of
+// 64 rows of mixed settings its start (9 us).
 template <typename T>
 __global__ __launch_bounds__(kNarrow) void k_sample_collect(SampleArgs a) {
   __shared__ int sh_n;
@@ -1371,6 +1401,10 @@ __device__ __forceinline__ void pick_listed(const SampleArgs &a, int r, Shared &
   write(a, at, f.token, (float)((double)f.own / (double)whole));
 }
 
+// What bounds it: chains of barriers, LDS reads and loads in one workgroup (64 rows
+// 17 to 20 us, 512 rows two to a compute unit 27): 2 for settings and heads, 2 to 4
+// for the lists, then two questions of 4 to 9 us by top_p, or the ranks of a list by
+// top_k.  Four waves a SIMD, which LDS allows.
 template <typename T>
 __global__ __launch_bounds__(kMiddle, 4) void k_sample_pick(SampleArgs a) {
   __shared__ Shared sh;
