@@ -56,7 +56,8 @@ size_t rfpx_attn_tree_workspace_bytes(const rfpx_kv_cache *c, const rfpx_kv_batc
  * is set in masks_dev [n_rows][mask_words] (its own among them: the bits alone
  * decide; bits of columns that do not exist, and columns that have no bit, are
  * not seen).  A column whose own slot is negative sees nothing.  Everything
- * else is as rfpx_attn_forward has it. */
+ * else is as rfpx_attn_forward has it.  (rfpx_attn_weights takes a step's columns
+ * as a chain: it has no form for trees.) */
 rfpx_status rfpx_attn_tree_forward(const rfpx_kv_cache *c, const rfpx_kv_batch *b,
                                    const void *q_dev, long long q_stride, int xtype, int n_heads,
                                    int n_rows, float scale, const uint32_t *masks_dev,
