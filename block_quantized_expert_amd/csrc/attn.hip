@@ -1542,7 +1542,7 @@ struct AttnPlan {
 };
 
 // Rows of a block: 16 where a sequence has no more, or fp32 is computed in
-// three terms; 32 otherwise.  A short sequence is one workgroup's, with no
+// three terms (but for some trees, below); 32 otherwise.  A short sequence is one workgroup's, with no
 // second launch; a longer one is split so that the workgroups fill the chip
 // once (two a compute unit), each wave with a tile at least.
 //
@@ -1559,7 +1559,11 @@ struct AttnPlan {
 // 14.6; 16 x 16384 27.0, 23.4; 16 sequences of 8 x 2000 22.7, 20.9; and at 16
 // tiles a wave 16 x 32768 32.4, 33.3; 8 of 16 x 4000 28.3, 29.0.  And of fp32
 // heads of 64, whose sums leave room for three workgroups a compute unit, they
-// fill that: 8 sequences of 12 columns to 8192 tokens 46.8 -> 35.5 us.
+// fill that: 8 sequences of 12 columns to 8192 tokens 46.8 -> 35.5 us.  Blocks of
+// 32 rows of those pay beyond the same eight tiles a wave, unless more than an
+// eighth of the blocks' rows would be none (blocks of 16, 32; 32 heads on 8): 16
+// sequences of 16 x 8192 80, 71; 4 of 64 x 4096 40, 33; 16 x 65536 56, 52; 8 of 24 x
+// 8192 54, 52; but 8 of 12 x 8192 39, 53.
 AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, int n_rows,
                    int xtype, bool tree) {
   AttnPlan p;
@@ -1586,7 +1590,12 @@ AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, in
   }
   const long long few = 8 * 512 * kWaves;  // tiles of all workgroups, eight a wave
   if (tree && pairs * ((rows + 15) / 16) * ((len + kTile - 1) / kTile) <= few) p.rt = 1;
-  const long long fill = tree && xtype == RFPX_X_F32 && c->head_dim == 64 ? 768 : 512;
+  const bool narrow = tree && xtype == RFPX_X_F32 && c->head_dim == 64;
+  const long long halves = (rows + 15) / 16;
+  if (narrow && pairs * halves * ((len + kTile - 1) / kTile) > few && len > 4 * kWavesOne * kTile &&
+      16 * ((rows + 31) / 32) <= 9 * halves)
+    p.rt = 2;
+  const long long fill = narrow ? 768 : 512;
   const long long block = p.chunk ? kChunkRows : 16 * p.rt;
   p.row_blocks = (int)clamp((rows + block - 1) / block, 1, most_rb);
   if (!p.chunk) {
@@ -1627,7 +1636,9 @@ hipError_t launch_attn(const AttnPlan &p, const AttnArgs &a, hipStream_t s) {
   const bool one = p.waves == kWavesOne;
   void (*k)(AttnArgs) =
       p.chunk               ? k_attn_chunk<NB == 8 ? 4 : NB, TREE>
-      : a.xtype == RFPX_X_F32 ? (one ? k_attn<NB, 3, 1, W1, TREE> : k_attn<NB, 3, 1, kWaves, TREE>)
+      : a.xtype == RFPX_X_F32 ? (one         ? k_attn<NB, 3, 1, W1, TREE>
+                                 : p.rt == 2 ? k_attn<NB, 3, NB == 2 && TREE ? 2 : 1, kWaves, TREE>
+                                             : k_attn<NB, 3, 1, kWaves, TREE>)
       : p.rt == 1           ? (one ? k_attn<NB, 1, 1, W1, TREE> : k_attn<NB, 1, 1, kWaves, TREE>)
                             : (one ? k_attn<NB, 1, RT, W1, TREE> : k_attn<NB, 1, RT, kWaves, TREE>);
   const size_t lds =

@@ -240,7 +240,8 @@ def test_attention_of_any_bits(hk, group, d, cols, plan, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-@pytest.mark.parametrize("hk,heads,d,plan", [(1, 4, 64, 0), (2, 8, 128, 0), (1, 4, 256, 0), (2, 16, 128, 65536)])
+@pytest.mark.parametrize("hk,heads,d,plan", [(1, 4, 64, 0), (2, 8, 128, 0), (1, 4, 256, 0), (2, 16, 128, 65536),
+                                             (2, 16, 64, 65536)])
 def test_attention_beside_nan(hk, heads, d, plan, dtype):
     """Columns whose keys or values are not finite reach those that see them."""
     t = torch()
