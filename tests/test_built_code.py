@@ -67,6 +67,9 @@ def test_the_listing_is_read():
 def test_no_shift_by_the_last_register(tmp_path):
     if not os.path.exists(OBJDUMP):
         pytest.skip("no llvm-objdump here")
+    if not os.path.exists(bqe.LIB_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
     with open(bqe.LIB_PATH, "rb") as fh:
         objects = list(code_objects(fh.read()))
     assert objects
