@@ -1350,29 +1350,28 @@ __global__ __launch_bounds__(kMiddle) void k_sample_decide(SampleArgs a) {
   }
 }
 
-// What bounds it: HBM, at 4.3 TB/s (512 rows that all come here, 268 MB, 62 us); of
-// 64 rows of mixed settings its start (9 us).
+// What bounds it: HBM (512 rows that all come here, 268 MB, 45 us; slices that took
+// several tasks in turn had twice the registers and took 61); of 64 rows of mixed
+// settings its start (9 us).
 template <typename T>
 __global__ __launch_bounds__(kNarrow) void k_sample_collect(SampleArgs a) {
   __shared__ int sh_n;
-  const int tasks = a.active[0] * a.slices;
-  for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int r = a.active[1 + task / a.slices], slice = task % a.slices, at = a.row0 + r;
-    const size_t rs = (size_t)r * a.slices + slice;
-    const RowSource<T> src = logits_of<T>(a, at);
-    HeldSource<T, kPieces<T>> held;
-    held.load(src, slice);
-    if (threadIdx.x == 0) sh_n = 0;
-    __syncthreads();
-    const Needed needed(row_of<T>(a.state[r].largest, a.temperature ? a.temperature[at] : 1.f, a.bits),
-                        a.state[r].need);
-    held.pick(src, &sh_n, needed, [&](int n, uint32_t key, int i) {
-      if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key, (uint32_t)i);
-    });
-    __syncthreads();
-    if (threadIdx.x == 0) a.heads[rs].collected = sh_n;
-    __syncthreads();
-  }
+  const int task = blockIdx.x;
+  if (task >= a.active[0] * a.slices) return;
+  const int r = a.active[1 + task / a.slices], slice = task % a.slices, at = a.row0 + r;
+  const size_t rs = (size_t)r * a.slices + slice;
+  const RowSource<T> src = logits_of<T>(a, at);
+  HeldSource<T, kPieces<T>> held;
+  held.load(src, slice);
+  if (threadIdx.x == 0) sh_n = 0;
+  __syncthreads();
+  const Needed needed(row_of<T>(a.state[r].largest, a.temperature ? a.temperature[at] : 1.f, a.bits),
+                      a.state[r].need);
+  held.pick(src, &sh_n, needed, [&](int n, uint32_t key, int i) {
+    if (n < kSliceList) a.list[rs * kSliceList + n] = make_uint2(key, (uint32_t)i);
+  });
+  __syncthreads();
+  if (threadIdx.x == 0) a.heads[rs].collected = sh_n;
 }
 
 // A row whose slices have listed all that may stay.
@@ -1522,11 +1521,10 @@ hipError_t launch_sample(const SamplePlan &p, SampleArgs a, uint8_t *w, hipStrea
   hipError_t e = hipSuccess;
   for (a.row0 = 0; a.row0 < a.n_rows && e == hipSuccess; a.row0 += p.rows) {
     a.rows = a.n_rows - a.row0 < p.rows ? a.n_rows - a.row0 : p.rows;
-    const int all = a.rows * a.slices;
     e = launch_k(k_sample_slices<T>, dim3(a.slices, a.rows), dim3(kNarrow), 0, s, a);
     if (e == hipSuccess) e = launch_k(k_sample_decide<T>, dim3(a.rows), dim3(kMiddle), 0, s, a);
     if (e == hipSuccess)
-      e = launch_k(k_sample_collect<T>, dim3(all < 2048 ? all : 2048), dim3(kNarrow), 0, s, a);
+      e = launch_k(k_sample_collect<T>, dim3(a.rows * a.slices), dim3(kNarrow), 0, s, a);
     if (e == hipSuccess) e = launch_k(k_sample_pick<T>, dim3(a.rows), dim3(kMiddle), 0, s, a);
   }
   return e;
