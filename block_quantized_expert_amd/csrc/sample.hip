@@ -145,6 +145,7 @@ struct Row {
   float largest;
   float bin_rate;  // bins a logit
   float base;      // the largest logit's bin, counted from 0
+  float lowest;    // what is below weighs nothing
   int bits;
   int key_zeros;   // low bits in which keys of one sign do not differ
   bool far;        // nothing but the largest logit weighs anything
@@ -167,14 +168,21 @@ __device__ __forceinline__ Row row_of(float largest, float temperature, int bits
   r.base = floorf(largest * r.bin_rate);
   r.bits = bits;
   r.ref = __builtin_ceil((double)largest * r.rate);
-  // (from 2^40 on the next smaller logit is more than 2^15 octaves below)
-  r.far = !(__builtin_fabs(r.ref) < 1099511627776.0) || !(r.rate < 1.2676506002282294e30);
+  // (from 2^30 on the next smaller logit, 2^-24 of it or more away, is 64 octaves or
+  // more below)
+  r.far = !(__builtin_fabs(r.ref) < 1073741824.0) || !(r.rate < 1.2676506002282294e30);
+  // (bits + 2 octaves below, where less than a quarter of a unit is left; rounded
+  // down, and above -inf)
+  r.lowest = fmaxf(__double2float_rd((double)largest - (bits + 2) * 0.6931471805599453 * (double)temperature),
+                   -3.4028234663852886e38f);
   return r;
 }
 
 // The bin of a logit: no larger for a larger one.  Whole numbers of the logit
 // itself, so that bins of slices differ by a whole number too.  Where products
 // overflow, and what is left of two of them is no number, it is the first.
+// Products of large logits are rounded, by more than a bin from 2^24 bins on: a
+// bin says where a logit stands among others, and not what it weighs.
 __device__ __forceinline__ int bin_of(const Row &r, float v) {
   const float b = r.base - floorf(v * r.bin_rate);
   return (int)fminf(fmaxf(b, 0.f), (float)(kBins - 1));
@@ -184,8 +192,9 @@ __device__ __forceinline__ int row_bin(const Row &r, float slice_base, int i) {
   return slice_base == r.base ? i : (int)fminf((float)i + (r.base - slice_base), (float)(kBins - 1));
 }
 
-// 2^(v rate - ref) in units of 2^-bits, rounded to the nearest, of a logit that
-// is not in the last bin (what is weighs less than half a unit).  With v rate = m
+// 2^(v rate - ref) in units of 2^-bits, rounded to the nearest, of a logit of
+// `lowest` or more in a row that is not far (which is less than 200 octaves below the
+// largest, bits + 2 and one step of fp32, so that the exponent is one).  With v rate = m
 // + f, m whole and |f| <= 1/2, 2^f is the polynomial 1 + f q(f) of degree 10 of
 // least relative error (3e-16, by Remez' exchange); the product is never rounded.
 // Adding 1.5 * 2^52, less ref and plus bits, leaves the exponent in the low bits;
@@ -213,11 +222,10 @@ __device__ __forceinline__ u64 near_weight(const Row &r, float v) {
   y[1] &= 0xFFFFFu;
   return __builtin_bit_cast(u64, y);
 }
-__device__ __forceinline__ u64 weight(const Row &r, float v, int bin) {
+__device__ __forceinline__ u64 weight(const Row &r, float v) {
   if (r.far) return v == r.largest ? 1ull << r.bits : 0;
-  return bin < kBins - 1 ? near_weight(r, v) : 0;
+  return v >= r.lowest ? near_weight(r, v) : 0;
 }
-__device__ __forceinline__ u64 weight(const Row &r, float v) { return weight(r, v, bin_of(r, v)); }
 
 // v >> n, of a lane's own n below 64, by operations of 32 bits.  (A 64-bit shift
 // whose amount lies in the last register that a wave has been given shifts some
@@ -545,7 +553,7 @@ __device__ __forceinline__ void add_weights(const S &src, Hist &h, const Row &ro
     const int b = bin_of(row, v);
     u64 w = near_weight(row, v);
     asm volatile("" : "+v"(w));
-    if (b < kBins - 1) atomicAdd(&h.mass[b * kCopies + copy], w);
+    if (v >= row.lowest) atomicAdd(&h.mass[b * kCopies + copy], w);
   });
 }
 // Running sums over the histogram's bins (between barriers of its own).
@@ -823,7 +831,7 @@ __device__ __forceinline__ Ask ask_of(const SampleArgs &a, int at) {
 
 // What a token of min_p weighs.
 __device__ __forceinline__ u64 least_weight(const Row &row, const Ask &q) {
-  return (u64)__builtin_ceil((double)weight(row, row.largest, 0) * (double)q.min_p);
+  return (u64)__builtin_ceil((double)weight(row, row.largest) * (double)q.min_p);
 }
 
 __device__ __forceinline__ u64 before(const Sums &s, int bin) { return bin ? s.mass[bin - 1] : 0; }
@@ -963,7 +971,7 @@ __device__ __forceinline__ u64 bins_of(const S &src, Shared &sh, const Row &row,
   } else {
     src.each([&](float v, int) {
       const int b = bin_of(row, v);
-      const u64 w = weight(row, v, b);
+      const u64 w = weight(row, v);
       add_to_bin(sh.hist, b, w, counts && v > kNegInf);
       if (w >= least) mass_min += w;
     });
@@ -1229,7 +1237,7 @@ __global__ __launch_bounds__(kNarrow) void k_sample_slices(SampleArgs a) {
   if (row.far) {
     held.each([&](float v, int) {
       const int b = bin_of(row, v);
-      add_to_bin(hist, b, weight(row, v, b), q.top_k != 0 && v > kNegInf);
+      add_to_bin(hist, b, weight(row, v), q.top_k != 0 && v > kNegInf);
     });
   } else {
     add_weights(held, hist, row);
@@ -1441,7 +1449,7 @@ __global__ __launch_bounds__(kMiddle, 4) void k_sample_pick(SampleArgs a) {
     const auto look = [&](float v, int) {
       const int b = bin_of(row, v);
       if (b < need.m0 || b > need.m1) return;
-      const u64 w = weight(row, v, b);
+      const u64 w = weight(row, v);
       if (w >= least) part += w;
     };
     if (n <= kList) ListSource{sh, n}.each(look);
