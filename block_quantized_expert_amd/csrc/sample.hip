@@ -829,6 +829,14 @@ __device__ __forceinline__ Ask ask_of(const SampleArgs &a, int at) {
   return q;
 }
 
+// How far from the largest logit one of min_p lies (0 or less, the logarithm within
+// 1e-5 of it).  At an infinite temperature all tokens weigh the same, and none is too
+// far: there the product with the logarithm of 1 is no number.
+__device__ __forceinline__ double depth_of_min_p(const Ask &q) {
+  const double d = (double)__logf(q.min_p) * (double)q.temperature;
+  return d == d ? d : -__builtin_inf();
+}
+
 // What a token of min_p weighs.
 __device__ __forceinline__ u64 least_weight(const Row &row, const Ask &q) {
   return (u64)__builtin_ceil((double)weight(row, row.largest) * (double)q.min_p);
@@ -861,9 +869,8 @@ __device__ __forceinline__ Need need_of(const Sums &s, const Row &row, const Ask
   Need n{0, -1, 0, -1, 0, -1, 0, -1};
   u64 min_lo = mass_min, min_hi = mass_min;
   if (!known && q.min_p > 0.f) {
-    // (the logarithm within 1e-5, the logit's place within a bin, 0.07 of a
-    // temperature, of what min_p says)
-    const int b = bin_of(row, (float)((double)row.largest + (double)__logf(q.min_p) * q.temperature));
+    // (its place within a bin, 0.07 of a temperature, of what min_p says)
+    const int b = bin_of(row, (float)((double)row.largest + depth_of_min_p(q)));
     n.m0 = max(0, b - 1);
     n.m1 = min(kBins - 1, b + 1);
     min_lo = before(s, n.m0);
@@ -1069,7 +1076,7 @@ __device__ __forceinline__ Found whole_row(const S &src, const L &long_way, Shar
 // has at most its own first top_k, and where so many of its threads' largest
 // logits (of each half of what a thread holds) lie in the bins to `last`, they
 // do.  (min_p is taken a little lower than it is, by far more than anything is
-// rounded.)
+// rounded.)  The largest logit is always among them.
 struct Limits {
   float scale, least;
   int last;
@@ -1080,10 +1087,9 @@ struct Limits {
 __device__ __forceinline__ Limits limits_of(const Row &row, const Ask &q, int last) {
   if (q.few()) return {row.bin_rate, last == kBins - 1 ? kNegInf : row.base - (float)last, last};
   if (!(q.min_p > 0.f)) return {1.f, kNegInf, kBins - 1};
-  // (the logarithm within 1e-5 of it)
-  const double t = (double)q.temperature;
   return {1.f,
-          __double2float_rd((double)row.largest + (double)__logf(q.min_p) * t * (1.0 + 1e-4) - 1e-4 * t),
+          __double2float_rd((double)row.largest + depth_of_min_p(q) * (1.0 + 1e-4) -
+                            1e-4 * (double)q.temperature),
           kBins - 1};
 }
 template <typename T, int N>

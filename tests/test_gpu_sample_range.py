@@ -68,3 +68,45 @@ def test_many_neighbours_of_one_logit(large, n):
         for i in range(6):
             e = Expected(host[i].astype(np.float64), t)
             e.check(tokens[i], probs[i], u[i])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [300, 5000, 30000, 70001])
+def test_infinite_temperature(n, dtype):
+    """All tokens weigh the same and min_p, of 1 and more too, cuts none of them:
+    the place drawn is a whole number.  Logits of any size, and tokens at -inf."""
+    T = torch()
+    rng = np.random.default_rng(n)
+    inf = float("inf")
+    base = rng.normal(size=n) * 3
+    some = np.where(rng.random(n) < 0.3, -inf, base)
+    x = T.tensor(np.stack([base, some, base * 1e38 / 12]), device="cuda").to(getattr(T, dtype))
+    host = x.double().cpu().numpy()
+    u = np.array([0.0, 0.375, 0.9990234375], np.float32)
+    for m in (1.0, 3.0, inf, 0.5, 1e-30):
+        for k, p in ((0, 1.0), (0, 0.5), (400, 1.0), (100, 1.0), (400, 0.5)):
+            tokens, probs = sample(x, u, [inf] * 3, [k] * 3, [p] * 3, [m] * 3)
+            for i in range(3):
+                order = np.argsort(-host[i], kind="stable")[:int((host[i] > -inf).sum())]
+                order = order[:k] if 0 < k < order.size else order
+                stays = order.size if p == 1 else -(-order.size // 2)
+                assert tokens[i] == order[int(float(u[i]) * stays)], (m, k, p, i)
+                assert probs[i] == f32(1 / stays), (m, k, p, i)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [300, 30000, 70001])
+def test_min_p_at_temperatures_of_any_size(n, dtype):
+    """min_p alone, and with cuts besides, from where the largest logit alone
+    weighs anything to where all weigh the same."""
+    T = torch()
+    rng = np.random.default_rng(n + 1)
+    x = T.tensor(rng.normal(size=(4, n)) * 3, device="cuda").to(getattr(T, dtype))
+    host = x.double().cpu().numpy()
+    u = rng.random(4).astype(np.float32)
+    for t in (1e-30, 1e-12, 1e-4, 0.05, 1e4, 1e30, 3e38):
+        for m in (1.0, 2.0, 0.30000001):
+            for k, p in ((0, 1.0), (400, 1.0), (0, 0.625)):
+                tokens, probs = sample(x, u, [t] * 4, [k] * 4, [p] * 4, [m] * 4)
+                for i in range(4):
+                    Expected(host[i], f32(t), k, f32(p), f32(m)).check(tokens[i], probs[i], u[i])
