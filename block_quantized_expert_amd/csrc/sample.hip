@@ -169,8 +169,8 @@ __device__ __forceinline__ Row row_of(float largest, float temperature, int bits
   r.bits = bits;
   r.ref = __builtin_ceil((double)largest * r.rate);
   // (from 2^30 on the next smaller logit, 2^-24 of it or more away, is 64 octaves or
-  // more below)
-  r.far = !(__builtin_fabs(r.ref) < 1073741824.0) || !(r.rate < 1.2676506002282294e30);
+  // more below; and rates stay below what fp32 holds)
+  r.far = !(__builtin_fabs(r.ref) < 1073741824.0) || !(temperature >= 7.888609052210118e-31f);
   // (bits + 2 octaves below, where less than a quarter of a unit is left; rounded
   // down, and above -inf)
   r.lowest = fmaxf(__double2float_rd((double)largest - (bits + 2) * 0.6931471805599453 * (double)temperature),

@@ -110,3 +110,25 @@ def test_min_p_at_temperatures_of_any_size(n, dtype):
                 tokens, probs = sample(x, u, [t] * 4, [k] * 4, [p] * 4, [m] * 4)
                 for i in range(4):
                     Expected(host[i], f32(t), k, f32(p), f32(m)).check(tokens[i], probs[i], u[i])
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [600, 40000])
+def test_the_lowest_temperatures(n, dtype):
+    """Logits as small as a temperature of 2^-100 count as any; below, only the
+    largest weighs anything."""
+    T = torch()
+    rng = np.random.default_rng(n + 2)
+    x = T.tensor(-rng.random((4, n)) * 8, device="cuda").to(getattr(T, dtype)) * 2.0 ** -100
+    x[:, 5] = 0.0
+    x[:2, 9] = 0.0
+    host = x.double().cpu().numpy()
+    u = np.array([0.3, 0.9, 0.3, 0.9], np.float32)
+    for t in (2.0 ** -99, 1.2 * 2.0 ** -100, 2.0 ** -100):
+        for k, p in ((0, 1.0), (3, 1.0), (0, 0.6)):
+            tokens, probs = sample(x, u, [t] * 4, [k] * 4, [f32(p)] * 4)
+            for i in range(4):
+                Expected(host[i], f32(t), k, f32(p)).check(tokens[i], probs[i], u[i])
+    for t in (f32(0.99 * 2.0 ** -100), 2.0 ** -130, 2.0 ** -149):
+        tokens, probs = sample(x, u, [t] * 4)
+        assert tokens == [5, 9, 5, 5] and probs == [0.5, 0.5, 1.0, 1.0]
