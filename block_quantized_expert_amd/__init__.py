@@ -914,8 +914,9 @@ def rfpx_tree_accept(batch: KvBatch, parents, tokens, drawn, path=None, counts=N
     """The drafts that the drawn tokens confirm: path (int32 [seqs][path_cols],
     columns, then -1; path_cols is max_cols unless path is given), counts, the
     token drawn at the last of them, and the lengths that the sequences then
-    have (lens_out; batch.lens is still needed where rfpx_kv_commit follows).  parents, tokens and drawn are int32 [rows].  Returns (path, counts,
-    next_tokens, lens_out)."""
+    have (lens_out; batch.lens is still needed where rfpx_kv_commit follows, and
+    has to be what the pages hold at most).  parents, tokens and drawn are int32
+    [rows].  Returns (path, counts, next_tokens, lens_out)."""
     import torch
     rows, n, i32 = parents.shape[0], batch.n_seqs, torch.int32
     if path is not None and path.dim() != 2:

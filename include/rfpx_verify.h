@@ -21,6 +21,12 @@
  * RFPX_TREE_COLS_MAX of them; rows of columns behind that, rows at or behind
  * starts[n_seqs] and at or behind n_rows are neither read nor written, except
  * that rfpx_attn_tree_forward computes any number of columns.
+ *
+ * rfpx_tree_masks and rfpx_tree_accept have no cache and take lens as it
+ * stands, past pages_per_seq * page_tokens and below 0 too.  The other calls
+ * count it as that, or as 0: of a sequence that has outgrown its pages lens has
+ * to be set to what they hold before the step, or the two would go on from
+ * slots that are not there.
  */
 #ifndef RFPX_VERIFY_H
 #define RFPX_VERIFY_H
@@ -120,9 +126,10 @@ rfpx_status rfpx_tree_accept(const rfpx_kv_batch *b, int n_rows, const int32_t *
  * pos_dev (fp32 and int32 [n_seqs][n_kv_heads][pages_per_seq * page_tokens],
  * each or both NULL) the same slots.  lens and starts are those of the step.
  * The path is ascending, so that an entry is its own index or more; an entry
- * below its index or that is no column of the step is passed over.  Slots that
- * are negative or have no page in the pool keep their keys and values.
- * Sequences must not share the pages of the step's columns. */
+ * below its index or that is no column of the step is passed over, and so is one
+ * that would move to a negative slot.  A move from or to a slot without a page in
+ * the pool carries acc and pos only.  Sequences must not share the pages of the
+ * step's columns. */
 rfpx_status rfpx_kv_commit(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int path_cols,
                            const int32_t *path_dev, const int32_t *counts_dev, float *acc_dev,
                            int32_t *pos_dev, void *stream);

@@ -739,3 +739,15 @@ def test_wrapper_refusals():
         bqe.rfpx_tree_masks(c.batch, parents, mask_words=33)
     with pytest.raises(bqe.RfpxError):
         bqe.rfpx_tree_masks(batch_of([9000], [0, 2000]), parents)
+
+
+def test_lengths_are_taken_as_they_stand():
+    """Masks and acceptance know no cache: lengths past any pages, and below 0."""
+    b = batch_of([1 << 30, -5, 3], [0, 2, 4, 8], max_len=64)
+    parents = ints([-1, 0, -1, 0, -1, 0, 1, 2])
+    _, pos = bqe.rfpx_tree_masks(b, parents)
+    assert pos.tolist() == [(1 << 30) - 2, (1 << 30) - 1, -7, -6, -1, 0, 1, 2]
+    tokens, drawn = ints([9, 1, 9, 1, 9, 1, 2, 3]), ints([1, 7, 0, 7, 1, 2, 0, 0])
+    path, counts, following, after = bqe.rfpx_tree_accept(b, parents, tokens, drawn)
+    assert path.tolist() == [[0, 1, -1, -1], [0, -1, -1, -1], [0, 1, 2, -1]] and counts.tolist() == [2, 1, 3]
+    assert following.tolist() == [7, 0, 0] and after.tolist() == [1 << 30, 0, 2]
