@@ -37,7 +37,12 @@
 // read once, into LDS.  Measured on an MI355X, 32 query heads on 8 kv heads of 128: a
 // tree of 64 columns over 131071 tokens 172 us and 8 for the join, 0.8 PFLOP/s, as
 // many causal columns the same; 16 columns of 1021 tokens 12.4 us, a chain of loads;
-// 8 sequences of 12 columns to 8192 tokens, fp32 heads of 64, 34 us and 4.
+// 8 sequences of 12 columns to 8192 tokens, fp32 heads of 64, 34 us and 4.  The masks'
+// addresses and bits cost a lane about 26 registers.  bf16 heads of 128 in blocks of 32
+// rows have none left (247 as a chain): 16 are kept in scratch, 68 bytes a lane, and 5
+// and 16 columns over 131071 tokens take 44.7 and 68.9 us, as chains 41.9 and 67.2.
+// Tried and not kept: bits of one row tile at a time, and of NaN blocks only where
+// there is one (the same 16).
 #include "../../include/rfpx_verify.h"
 #include "rfpx_attn.hpp"
 
@@ -1558,12 +1563,21 @@ struct AttnPlan {
 // us, 8 kv heads of 128, columns x tokens: 16 x 1021 16.4, 11.8; 5 x 8192 20.6,
 // 14.6; 16 x 16384 27.0, 23.4; 16 sequences of 8 x 2000 22.7, 20.9; and at 16
 // tiles a wave 16 x 32768 32.4, 33.3; 8 of 16 x 4000 28.3, 29.0.  And of fp32
-// heads of 64, whose sums leave room for three workgroups a compute unit, they
-// fill that: 8 sequences of 12 columns to 8192 tokens 46.8 -> 35.5 us.  Blocks of
-// 32 rows of those pay beyond the same eight tiles a wave, unless more than an
-// eighth of the blocks' rows would be none (blocks of 16, 32; 32 heads on 8): 16
-// sequences of 16 x 8192 80, 71; 4 of 64 x 4096 40, 33; 16 x 65536 56, 52; 8 of 24 x
-// 8192 54, 52; but 8 of 12 x 8192 39, 53.
+// heads of 64, whose sums leave room for three workgroups a compute unit (161
+// registers), they fill that: 8 sequences of 12 columns to 8192 tokens 46.8 -> 35.5
+// us.  Blocks of 32 rows of those pay beyond the same eight tiles a wave, unless more
+// than an eighth of the blocks' rows would be none (blocks of 16, 32; 32 heads on 8,
+// calls in a graph): 16 sequences of 16 x 8192 93, 86; 16 x 65536 52, 50; 8 of 24 x
+// 8192 68, 62; 9 of 32 x 8192 115, 109; 16 to 16 x 8192, of uneven lengths, 78, 68; but
+// 4 of 64 x 4096 49, 52; 8 of 12 x 8192 39, 53 (so blocks of 16).  Of blocks of 32 only
+// two workgroups fit (225 registers), and 768 are a round and a half.  Neither number is
+// better at all sizes (768, 512): 16 of 16 x 8192 79, 76; 4 of 64 x 4096 49, 45; 5 of 32
+// x 8192 67, 61; but 8 of 24 x 8192 64, 75; 9 of 32 x 8192 109, 133, where 512 leaves a
+// quarter of the places empty; 5 to 32 x 8192, of uneven lengths, 37, 51.
+//
+// These rules are about shapes, and would shorten chains of several columns alike
+// (16 x 1021 15.4 us as a chain, 11.9 as a tree); those keep the plans that they
+// had, and with them their outputs bit for bit.
 AttnPlan attn_plan(const rfpx_kv_cache *c, const rfpx_kv_batch *b, int heads, int n_rows,
                    int xtype, bool tree) {
   AttnPlan p;

@@ -20,8 +20,9 @@
 // weight, then digits of the keys in one bin, until at most 256 tokens are left,
 // which are ranked by comparing each with all, or tokens of one logit.
 //
-// Rows of up to 32768 logits are a workgroup's each, in registers
-// (k_sample_row).  Longer ones are cut into slices:
+// Rows of up to 32765 fp32 or 32761 bf16 logits (32768, less what one that begins off
+// 16 bytes costs) are a workgroup's each, in registers (k_sample_row).  Longer ones are
+// cut into slices:
 //   k_sample_slices   a workgroup holds its slice in registers: its largest
 //                     logit; and, if the row keeps the first of few, or tokens
 //                     of some weight, all of the slice that can be among them,
@@ -38,7 +39,7 @@
 // Measured on an MI355X, us a call in a graph, a workgroup a row / slices: 1 row of
 // 32000 fp32 logits by top_p 23.5 / 27.5, by top_k 14.0 / 22.2, greedy 7.3 / 10.5; 512
 // rows 67 / 81, 32 / 41, 20 / 23; 512 rows of 8000 37 / 47; one row of 4000 13.4 / 26.5.
-// Above 32768 logits the registers of a workgroup do not hold a row.
+// Above those the registers of a workgroup do not hold a row.
 #include "../../include/rfpx_verify.h"
 #include "rfpx_impl.hpp"
 
@@ -63,7 +64,7 @@ constexpr int kList = 6144;  // tokens that answer() has in LDS
 // Tokens that find() ranks by comparing each with all (64: one more digit, 4 us, for
 // most bins; 512: the same time as 256).
 constexpr int kRank = 256;
-constexpr float kBinsPerOctave = 10.f;  // 51 octaves, which is all that weighs anything
+constexpr float kBinsPerOctave = 10.f;  // 51 octaves; what is below weighs a unit at most
 constexpr uint32_t kNoToken = 0x007FFFFFu;  // key of -inf, which NaN gets too
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kRowMost = 32 * kWide;  // logits of a row that is not cut into slices
@@ -1156,7 +1157,9 @@ __device__ __forceinline__ RowSource<T> logits_of(const SampleArgs &a, int at) {
 // the weights by bin (32 logits a thread, 15 operations of 64 bits each, four
 // cycles an operation and four waves on a SIMD), 2.3 for the list of the tokens in
 // question, and the questions of 2 to 4 us, chains of barriers and LDS reads.  Loops
-// over the registers are rolled: unrolled ones wait for their instructions.
+// over the registers are rolled: unrolled ones wait for their instructions.  A wave
+// has 128 registers, which 16 waves leave it, and keeps 8 in scratch (36 bytes a lane)
+// in rows above 16384 logits, 2 in rows of bf16 above 8192.
 template <typename T, int N>
 __global__ __launch_bounds__(kWide) void k_sample_row(SampleArgs a) {
   __shared__ Shared sh;
@@ -1193,7 +1196,7 @@ constexpr int kPieces = kSlice / (kNarrow * RowSource<T>::E);
 // of 131072 fp32 logits, 268 MB: greedy 48 us, 5.5 TB/s; top_k or min_p 70, 3.8
 // TB/s); of rows whose weights go by bin, those weights, 25 vector operations a
 // logit, 15 of them of 64 bits (98 us; at four cycles each they are 45 us of every
-// SIMD's issue, and the read 52).  A wave has 76 registers, six waves on a SIMD; at
+// SIMD's issue, and the read 52).  A wave has 78 registers, six waves on a SIMD; at
 // 64 it spills.  Tried and not kept: loads inside the loop over pieces (63 us greedy:
 // conversions between them made each wait for the one before).  Without its atomics
 // it is no faster.
