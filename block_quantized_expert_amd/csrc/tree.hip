@@ -32,7 +32,7 @@ struct MaskArgs {
 // A workgroup a sequence, a thread a column: it climbs to its root, and since
 // parents come before their children its words are done from the last to the
 // first.  Two launches less than a matrix of ancestors by squaring, and no
-// more reads than bits are set.  One tree of 16 columns takes 1.9 us on an MI355X,
+// more reads than bits are set.  One tree of 16 columns takes 2.0 us on an MI355X,
 // 64 of up to 256 columns 4.8.  Of 64 trees of 256 in 12 levels, 4.2 us, 2.4 are the
 // launch and two dependent reads (one word, no climb), 0.9 the stores of eight words
 // a lane (no climb 3.3), 0.9 the climb; it bounds deep trees: a chain of 256 28 us.
@@ -78,7 +78,7 @@ struct AcceptArgs {
 // A workgroup a sequence: every column whose token was drawn at its parent
 // offers itself as the parent's next one (the smallest number wins, so the
 // order of the offers is of no account), and one thread follows the chain.  One
-// tree of 16 columns takes 1.9 us on an MI355X, 64 of up to 256 columns 4.1, the
+// tree of 16 columns takes 2.2 us on an MI355X, 64 of up to 256 columns 4.0, the
 // launch and dependent reads; a chain of 256 that is all confirmed 17, the walk.
 __global__ __launch_bounds__(kThreads) void k_tree_accept(AcceptArgs a) {
   __shared__ int drawn[kColsMax], child[kColsMax];
@@ -127,7 +127,7 @@ struct CommitArgs {
 // ascend, so whatever the moves of one turn write lies before all that a later
 // turn reads, and within a turn every read comes before the barrier and every
 // write behind it.  What bounds it is a chain of three reads (lengths, path, page)
-// before a token's: one tree of 16 columns 4.0 us on an MI355X, 64 trees of 64 and 8
+// before a token's: one tree of 16 columns 4.1 us on an MI355X, 64 trees of 64 and 8
 // kv heads 4.2.
 template <int NB>
 __global__ __launch_bounds__(kThreads) void k_kv_commit(CommitArgs a) {
